@@ -426,6 +426,149 @@ tpk_status tpk_tiers_sync(tpk_tiers* tiers);
 tpk_status tpk_tiers_destroy(tpk_tiers* tiers);
 
 /*
+ * A serving step over pages whose lengths live on the device
+ * -----------------------------------------------------------
+ * The four calls below take request lengths, page tables and token maps from device
+ * memory, so a step captured once in a CUDA graph is replayed while requests grow,
+ * shrink and change places: tpk_kv_tables_update turns old and new lengths into page
+ * tables and slot maps, tpk_kv_rope_append rotates the new queries and keys and
+ * stores keys and values into the pages, tpk_decode_attn_paged attends one new token
+ * per request, tpk_cross_attn_paged attends any number of query tokens per request
+ * to paged states of another length (an encoder's, or a prompt's own).  They follow
+ * the conventions above (ownership, pointers, streams, errors); their pools are
+ * [slot][kv_heads][64][head_dim] of bfloat16 or float16, their page table is int32
+ * [n_req][max_pages] (row b: the slots of request b's pages in order).  There is no
+ * counterpart in the pages this library follows.
+ */
+enum { TPK_BF16 = 0, TPK_F16 = 1 };
+typedef struct {
+  int kv_heads;      /* H in [1, 1024] */
+  int group;         /* G query heads per KV head, in [1, 128]; query head j reads KV head j / G */
+  int head_dim;      /* D: 64, 128 or 256 */
+  int page_tokens;   /* must be 64 */
+  int dtype;         /* of q, k, v and the pools: TPK_BF16 or TPK_F16 */
+  float sm_scale;    /* softmax scale, finite; 0 selects 1/sqrt(head_dim) */
+  int64_t kv_slots;  /* slots in each pool, > 0; kv_slots * kv_heads * 64 < 2^31 */
+  int max_pages;     /* entries per page-table row (the attention calls), > 0 */
+} tpk_paged_shape;
+
+/*
+ * Page tables and slot maps from request lengths.  Request b grows from len_old[b] to
+ * len_new[b] tokens, shrinks (a draft taken back, or 0: finished) or stays.  With
+ * have = ceil(len_old / 64) and want = ceil(len_new / 64) pages:
+ *   - requests that shrink give back pages [want, have): in request order, then page
+ *     order, they are pushed on the stack of free slots (free_slots[0 .. n_free));
+ *   - requests that grow then take want - have slots each from the top of that stack,
+ *     in request order: page have + j gets the j-th one below its predecessors'.
+ * A request is refused (granted[b] = 0, its length and pages unchanged, its tokens'
+ * slots -1) if a length is negative, if have or want exceeds max_pages, if its tokens
+ * end past max_tokens, or if the stack holds too few slots for it: a request that
+ * needs pages is granted when the pages taken by it and all before it -- refused for
+ * want of slots or not -- are on the stack.
+ *   len_old, len_new  dev int32 [n_req]
+ *   page_table        dev int32 [n_req][max_pages], updated in place (entries past a
+ *                     request's pages are left as they were)
+ *   free_slots        dev int32 [free_cap], updated in place; n_free_in, n_free_out: dev
+ *                     int32 [1] (a count out of [0, free_cap] is clamped; pages given
+ *                     back past free_cap are dropped and set bit 0 of the device status)
+ *   len_out           dev int32 [n_req]: the length each request has now
+ *   granted           dev int32 [n_req]
+ *   tok_off           dev int32 [n_req + 1]: where each request's new tokens begin (the
+ *                     running sum of max(0, len_new - len_old), clamped to max_tokens)
+ *   slot_map          dev int64 [max_tokens]: slot * 64 + row of each new token; -1 for
+ *                     a refused request's tokens and past the last one
+ *   positions         dev int32 [max_tokens]: its position (0 past the last)
+ *   token_req         dev int32 [max_tokens]: its request (-1 past the last)
+ * n_free_out may be n_free_in, len_out may be len_old or len_new: updated in place.
+ * Other outputs overlap nothing.  n_req in [1, 4096], n_req * max_pages < 2^31;
+ * max_tokens >= 0 (its three maps may be null if 0).
+ */
+tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old, const int32_t* len_new,
+                                int32_t* page_table, int32_t* free_slots, int free_cap, const int32_t* n_free_in,
+                                int32_t* n_free_out, int32_t* len_out, int32_t* granted, int32_t* tok_off,
+                                int64_t* slot_map, int32_t* positions, int32_t* token_req, int max_tokens,
+                                tpk_stream_t stream);
+
+/*
+ * Rotary positions with up to four axes, and the store of new keys and values into
+ * their pages.  Token t's row of q (or k) is [heads][D] at q + t * q_stride elements.
+ * The first rot_dim channels of each head are rotated, pair j of rot_dim / 2 by the
+ * angle positions[axis_of[j]][t] * inv_freq[j]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * where pair j is channels (j, j + rot_dim / 2), or (2 j, 2 j + 1) if interleaved; the
+ * other channels are copied.  The angle is reduced in fixed point, exact to 2^-32
+ * turns at any 32-bit position; the products run in float32 and are rounded once.
+ * Rotated queries go to q_out (rows of q_out_stride elements; may be q itself with the
+ * same stride), rotated keys and the values to row slot_map[t] of the pools.
+ * A token with a negative slot is padding: its rows of q_out and of the pools are left
+ * as they were; one with a slot past kv_slots * 64 is left out too and sets bit 0 of
+ * the device status.  Tokens of one call must have distinct slots.
+ *   positions  dev int32 [n_axes][n_tokens]
+ *   axis_of    host uint8 [rot_dim / 2], each < n_axes; NULL: axis 0 everywhere
+ *   inv_freq   dev float32 [rot_dim / 2], finite
+ *   slot_map   dev int64 [n_tokens]; NULL only without keys (every row is then live)
+ * q and q_out may both be NULL (store only); k, v and both pools may all be NULL
+ * (rotate q only).  rot_dim is a multiple of 16, at most head_dim; 0 stores k as it is
+ * (positions and inv_freq are then not read).  Strides are multiples of 8 elements, at
+ * least heads * head_dim; shape->max_pages and sm_scale are not used.
+ */
+tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const int32_t* positions, int n_axes, const uint8_t* axis_of, const float* inv_freq,
+                              int rot_dim, int interleaved, const int64_t* slot_map, void* q_out,
+                              int64_t q_out_stride, void* k_pool, void* v_pool, tpk_stream_t stream);
+
+/*
+ * Attention of one new token per request over its pages.  Request b's query heads
+ * attend tokens [tok_begin[b], n_tokens[b]) (tok_begin NULL: from 0; a sliding window
+ * otherwise); token t lives in row t % 64 of slot page_table[b][t / 64].  The work is
+ * split into equal page ranges over the whole device whatever the lengths, and joined
+ * in a fixed order by a second small launch, so results are bit-reproducible.
+ *   q          dev [n_req] rows of q_stride elements, [H*G][D]
+ *   n_tokens, tok_begin: dev int32 [n_req] (values out of [0, 64 * max_pages] are
+ *              clamped into it and set bit 0 of the device status)
+ *   o          dev [n_req] rows of o_stride elements, [H*G][D]: of shape->dtype, or
+ *              float32 if o_f32 (what tpk_merge_lse folds with other tiers' partials)
+ *   lse        dev float32 [n_req][H*G]
+ * A request that sees nothing gets o = 0, lse = -inf.  Pool rows outside the attended
+ * range may hold anything, NaN and infinities too.  A page-table entry outside the pool
+ * is skipped and sets bit 0 of the device status.
+ * ws: dev workspace of tpk_decode_paged_workspace_bytes(shape, n_req) bytes (no
+ * initialisation); calls sharing one must not overlap on the GPU.  n_req in [1, 4096].
+ * Strides are multiples of 8 elements, at least H*G*D.  Capturable once the device has
+ * seen one uncaptured call of the same head_dim and dtype.
+ */
+size_t tpk_decode_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req);
+tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const void* q, int64_t q_stride,
+                                 const void* k_pool, const void* v_pool, const int32_t* page_table,
+                                 const int32_t* n_tokens, const int32_t* tok_begin, void* o, int64_t o_stride,
+                                 int o_f32, float* lse, void* ws, size_t ws_bytes, tpk_stream_t stream);
+
+/*
+ * Cross attention of ragged queries to paged states of another length.  Query tokens
+ * q_off[b] .. q_off[b + 1] - 1 of request b attend its states [0, n_tokens[b]), each
+ * with its own part of them if kv_range is given: query token i sees states
+ * [kv_range[i][0], kv_range[i][1]) of its request (clips of a video, images before a
+ * token; (0, i + 1) is a causal prompt).  Ranges are cut to [0, n_tokens[b]); an empty
+ * one gives o = 0 and lse = -inf.
+ *   q          dev [n_q] rows of q_stride elements, [H*G][D]
+ *   q_off      dev int32 [n_req + 1], not decreasing (values are clamped into [0, n_q];
+ *              rows of o and lse outside [q_off[0], q_off[n_req]) are left as they were)
+ *   n_tokens   dev int32 [n_req] (clamped as above); kv_range: dev int32 [n_q][2] or NULL
+ *   o          dev [n_q] rows of o_stride elements, of shape->dtype; lse: dev float32
+ *              [n_q][H*G]
+ * States within n_tokens[b] must be finite; pool rows past it may hold anything.
+ * ws: dev workspace of tpk_cross_paged_workspace_bytes(shape, n_req, n_q) bytes (no
+ * initialisation); calls sharing one must not overlap on the GPU.  n_req in [1, 4096];
+ * n_q >= 0 (0 is a no-op).  Strides, errors and capture as for tpk_decode_attn_paged.
+ */
+size_t tpk_cross_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_q);
+tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q, const void* q, int64_t q_stride,
+                                const int32_t* q_off, const void* k_pool, const void* v_pool,
+                                const int32_t* page_table, const int32_t* n_tokens, const int32_t* kv_range, void* o,
+                                int64_t o_stride, float* lse, void* ws, size_t ws_bytes, tpk_stream_t stream);
+
+/*
  * Measurement hook: while set, every decode-kernel launch of the library (the
  * partial calls and the decode launch of the multi-request call, not its fold) is
  * preceded by a record of `before` and followed by a record of `after` on the

@@ -24,11 +24,14 @@ __all__ = [
     "get_device_status",
     "static_scratch_bytes", "decode_hybrid_batched_static", "Stager", "Tiers", "TiersPlan",
     "PACK13_RECORD_BYTES", "PACK13_PLANE_ENC", "PACK13_PLANE_RAW", "kv_pack13_pages", "kv_unpack13_pages",
+    "PagedShape", "BF16", "F16", "kv_tables_update", "kv_rope_append", "decode_paged_workspace_bytes",
+    "decode_attn_paged", "cross_paged_workspace_bytes", "cross_attn_paged",
 ]
 
 RECORD_BYTES = 35072
 PACK13_RECORD_BYTES, PACK13_PLANE_ENC, PACK13_PLANE_RAW = 65552, 26656, 32768
 IMPL_DEFAULT, IMPL_SIMT, IMPL_TENSOR = 0, 1, 2
+BF16, F16 = 0, 1
 STATUS_NAMES = {0: "TPK_OK", 1: "TPK_ERR_INVALID", 2: "TPK_ERR_UNSUPPORTED", 3: "TPK_ERR_CUDA",
                 4: "TPK_ERR_BOUNDS", 5: "TPK_ERR_NOMEM", 6: "TPK_ERR_TIMEOUT", 7: "TPK_ERR_FORMAT"}
 
@@ -42,6 +45,16 @@ class Shape(ctypes.Structure):
                  kv_slots=0, rec_slots=0, int_query=0):
         super().__init__(kv_heads, group, head_dim, page_tokens, sm_scale, impl, kv_slots, rec_slots,
                          int(int_query))
+
+
+class PagedShape(ctypes.Structure):
+    """Shape of the calls over device-side lengths (tpk_paged_shape)."""
+    _fields_ = [("kv_heads", ctypes.c_int), ("group", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_tokens", ctypes.c_int), ("dtype", ctypes.c_int), ("sm_scale", ctypes.c_float),
+                ("kv_slots", ctypes.c_int64), ("max_pages", ctypes.c_int)]
+
+    def __init__(self, kv_heads, group, head_dim, page_tokens=64, dtype=BF16, sm_scale=0.0, kv_slots=0, max_pages=0):
+        super().__init__(kv_heads, group, head_dim, page_tokens, dtype, sm_scale, kv_slots, max_pages)
 
 
 class TiersPlan(ctypes.Structure):
@@ -119,6 +132,18 @@ def lib():
         L.tpk_tiers_destroy.argtypes = [vp]
         for name in ("tpk_tiers_create", "tpk_tiers_update", "tpk_tiers_step", "tpk_tiers_sync",
                      "tpk_tiers_destroy", "tpk_tiers_create_layers", "tpk_tiers_update_layers"):
+            getattr(L, name).restype = i32
+        gp = ctypes.POINTER(PagedShape)
+        L.tpk_kv_tables_update.argtypes = [i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp]
+        L.tpk_kv_rope_append.argtypes = [gp, i32, vp, i64, vp, i64, vp, i64, vp, i32, vp, vp, i32, i32, vp, vp, i64,
+                                         vp, vp, vp]
+        L.tpk_decode_paged_workspace_bytes.argtypes = [gp, i32]
+        L.tpk_decode_paged_workspace_bytes.restype = sz
+        L.tpk_decode_attn_paged.argtypes = [gp, i32, vp, i64, vp, vp, vp, vp, vp, vp, i64, i32, vp, vp, sz, vp]
+        L.tpk_cross_paged_workspace_bytes.argtypes = [gp, i32, i32]
+        L.tpk_cross_paged_workspace_bytes.restype = sz
+        L.tpk_cross_attn_paged.argtypes = [gp, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, sz, vp]
+        for name in ("tpk_kv_tables_update", "tpk_kv_rope_append", "tpk_decode_attn_paged", "tpk_cross_attn_paged"):
             getattr(L, name).restype = i32
         for name in ("tpk_kv_quantize_pages", "tpk_kv_quantize_pages_given_scales", "tpk_kv_pack13_pages",
                      "tpk_kv_unpack13_pages", "tpk_decode_attn_exact",
@@ -252,6 +277,58 @@ def hybrid_plan(shape, n_exact_tokens, n_int8_pages, resident_blocks=0):
                                  int(resident_blocks), se.ctypes.data_as(ip), s8.ctypes.data_as(ip),
                                  ctypes.byref(units)))
     return se, s8, units.value
+
+
+def kv_tables_update(n_req, max_pages, len_old, len_new, page_table, free_slots, free_cap, n_free_in, n_free_out,
+                     len_out, granted, tok_off, slot_map, positions, token_req, max_tokens, stream=None):
+    """Page tables and slot maps on the GPU from old and new request lengths (see
+    tpk_kv_tables_update); every array is a device buffer."""
+    _check(lib().tpk_kv_tables_update(n_req, max_pages, _ptr(len_old), _ptr(len_new), _ptr(page_table),
+                                      _ptr(free_slots), free_cap, _ptr(n_free_in), _ptr(n_free_out), _ptr(len_out),
+                                      _ptr(granted), _ptr(tok_off), _ptr(slot_map), _ptr(positions), _ptr(token_req),
+                                      max_tokens, _stream(stream)))
+
+
+def kv_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, positions, n_axes, axis_of, inv_freq,
+                   rot_dim, interleaved, slot_map, q_out, q_out_stride, k_pool, v_pool, stream=None):
+    """Rotate q and k at positions of up to four axes and store k and v into their
+    pages (see tpk_kv_rope_append).  axis_of is a host array of rot_dim / 2 axis
+    numbers (None: axis 0); q and q_out, or k, v and the pools, may be None."""
+    if axis_of is not None:
+        axis_of = np.ascontiguousarray(axis_of, np.uint8)
+        if axis_of.shape != (rot_dim // 2,):
+            raise ValueError(f"axis_of has shape {axis_of.shape}, not ({rot_dim // 2},)")
+    _check(lib().tpk_kv_rope_append(ctypes.byref(shape), n_tokens, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
+                                    v_stride, _ptr(positions), n_axes,
+                                    None if axis_of is None else axis_of.ctypes.data, _ptr(inv_freq), rot_dim,
+                                    int(interleaved), _ptr(slot_map), _ptr(q_out), q_out_stride, _ptr(k_pool),
+                                    _ptr(v_pool), _stream(stream)))
+
+
+def decode_paged_workspace_bytes(shape, n_req):
+    return int(lib().tpk_decode_paged_workspace_bytes(ctypes.byref(shape), n_req))
+
+
+def decode_attn_paged(shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, tok_begin, o, o_stride, o_f32,
+                      lse, ws, ws_bytes, stream=None):
+    """One new token per request over a paged cache whose lengths are device arrays
+    (see tpk_decode_attn_paged)."""
+    _check(lib().tpk_decode_attn_paged(ctypes.byref(shape), n_req, _ptr(q), q_stride, _ptr(k_pool), _ptr(v_pool),
+                                       _ptr(page_table), _ptr(n_tokens), _ptr(tok_begin), _ptr(o), o_stride,
+                                       int(o_f32), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def cross_paged_workspace_bytes(shape, n_req, n_q):
+    return int(lib().tpk_cross_paged_workspace_bytes(ctypes.byref(shape), n_req, n_q))
+
+
+def cross_attn_paged(shape, n_req, n_q, q, q_stride, q_off, k_pool, v_pool, page_table, n_tokens, kv_range, o,
+                     o_stride, lse, ws, ws_bytes, stream=None):
+    """Ragged query tokens over paged states of another length (see
+    tpk_cross_attn_paged)."""
+    _check(lib().tpk_cross_attn_paged(ctypes.byref(shape), n_req, n_q, _ptr(q), q_stride, _ptr(q_off), _ptr(k_pool),
+                                      _ptr(v_pool), _ptr(page_table), _ptr(n_tokens), _ptr(kv_range), _ptr(o),
+                                      o_stride, _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def set_decode_timing_events(before=None, after=None):

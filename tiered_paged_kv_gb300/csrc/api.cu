@@ -29,7 +29,11 @@ __device__ int g_tpk_status;
 
 namespace tpk {
 void set_error(const char* msg);
-}
+int* device_status_word();
+int device_sms();
+void* tensor_map_encoder();
+uint64_t wait_limit_ns();
+}  // namespace tpk
 
 namespace {
 
@@ -255,6 +259,16 @@ tpk_status launch_decode(const tpk_shape* s, const DecodeParams& p, const ReqPla
 }  // namespace
 
 void tpk::set_error(const char* msg) { g_err = msg; }
+
+// For the other translation units: the status word and SM count of the current
+// device, the tensor-map encoder and the limit of the bounded waits.
+int* tpk::device_status_word() { return status_ptr(); }
+int tpk::device_sms() { return num_sms(); }
+void* tpk::tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
+uint64_t tpk::wait_limit_ns() {
+  const uint64_t w = g_test_wait_ns.load(std::memory_order_relaxed);
+  return w > 0 ? w : kWaitLimitNs;
+}
 
 extern "C" {
 

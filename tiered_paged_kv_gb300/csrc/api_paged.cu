@@ -1,0 +1,300 @@
+// Host side of the calls over device-side lengths: argument validation, tensor maps
+// and launches.  Lengths, tables and slot maps stay on the device, so what can be
+// checked here is shapes, strides, alignment and sizes; the kernels clamp or skip the
+// rest and report it in the device status word.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "paged.cuh"
+#include "tpk.h"
+
+namespace tpk {
+void set_error(const char* msg);
+int* device_status_word();
+void* tensor_map_encoder();
+uint64_t wait_limit_ns();
+}  // namespace tpk
+
+using namespace tpk;
+
+namespace {
+
+tpk_status fail(tpk_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  set_error(buf);
+  return s;
+}
+
+tpk_status cuda_fail(cudaError_t e, const char* what) {
+  return fail(TPK_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+constexpr int kMaxHeads = 1024, kMaxGroup = 128, kMaxTableRow = (1 << 25) - 1;
+
+tpk_status check_paged(const tpk_paged_shape* s) {
+  if (!s) return fail(TPK_ERR_INVALID, "shape is null");
+  if (s->kv_heads < 1 || s->kv_heads > kMaxHeads) return fail(TPK_ERR_INVALID, "kv_heads %d out of [1, %d]", s->kv_heads, kMaxHeads);
+  if (s->group < 1 || s->group > kMaxGroup) return fail(TPK_ERR_INVALID, "group %d out of [1, %d]", s->group, kMaxGroup);
+  if (s->head_dim != 64 && s->head_dim != 128 && s->head_dim != 256)
+    return fail(TPK_ERR_UNSUPPORTED, "head_dim %d (64, 128 or 256 supported)", s->head_dim);
+  if (s->page_tokens != kPageTokens) return fail(TPK_ERR_UNSUPPORTED, "page_tokens %d (only 64 supported)", s->page_tokens);
+  if (s->dtype != TPK_BF16 && s->dtype != TPK_F16) return fail(TPK_ERR_INVALID, "dtype %d", s->dtype);
+  if (!std::isfinite(s->sm_scale)) return fail(TPK_ERR_INVALID, "sm_scale is not finite");
+  if (s->kv_slots < 1) return fail(TPK_ERR_INVALID, "kv_slots %lld < 1", (long long)s->kv_slots);
+  if (s->kv_slots > 0x7fffffffLL / ((int64_t)s->kv_heads * kPageTokens))
+    return fail(TPK_ERR_UNSUPPORTED, "pool too large for one tensor map");
+  return TPK_OK;
+}
+
+tpk_status check_stride(const char* what, int64_t stride, int64_t least) {
+  if (stride < least) return fail(TPK_ERR_INVALID, "%s %lld < %lld", what, (long long)stride, (long long)least);
+  if (stride % 8) return fail(TPK_ERR_INVALID, "%s %lld is not a multiple of 8 elements", what, (long long)stride);
+  return TPK_OK;
+}
+
+// Pools as 2-D tensors [slot * H * 64][D] with page-high boxes of 64 channels and the
+// 128-byte swizzle.
+tpk_status make_maps(PagedParams& p, const tpk_paged_shape* s, const void* k_pool, const void* v_pool) {
+  typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  EncodeFn fn = reinterpret_cast<EncodeFn>(tensor_map_encoder());
+  if (!fn) return fail(TPK_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[2] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->kv_slots * s->kv_heads * kPageTokens};
+  const cuuint64_t strides[1] = {(cuuint64_t)s->head_dim * 2};
+  const cuuint32_t box[2] = {64, kPageTokens}, estr[2] = {1, 1};
+  const void* pools[2] = {k_pool, v_pool};
+  CUtensorMap* maps[2] = {&p.kmap, &p.vmap};
+  for (int i = 0; i < 2; ++i) {
+    const CUresult r = fn(maps[i], s->dtype == TPK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          2, const_cast<void*>(pools[i]), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(TPK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  }
+  return TPK_OK;
+}
+
+// Workspace of a split launch: the numbering table, then the partials.
+size_t split_ws_bytes(const tpk_paged_shape* s, int n_req) {
+  const size_t slots = 2 * (size_t)kPagedMaxBlocks * kRowTile;
+  return align256((size_t)(n_req + 1) * 8) + align256(2 * slots * 4) + slots * s->head_dim * 4;
+}
+
+void place_ws(PagedParams& p, int n_req, void* ws) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.prefix = reinterpret_cast<int64_t*>(w);
+  w += align256((size_t)(n_req + 1) * 8);
+  p.part_ml = reinterpret_cast<float*>(w);
+  w += align256(4 * (size_t)kPagedMaxBlocks * kRowTile * 4);
+  p.part_o = reinterpret_cast<float*>(w);
+}
+
+bool sized(const tpk_paged_shape* s, int n_req) {
+  return s && n_req >= 1 && n_req <= kMaxPagedReq && (s->head_dim == 64 || s->head_dim == 128 || s->head_dim == 256);
+}
+
+// What both attention calls check and fill in.
+tpk_status begin_attention(PagedParams& p, const tpk_paged_shape* s, int n_req, const void* q, int64_t q_stride,
+                           const void* k_pool, const void* v_pool, const int32_t* page_table, const int32_t* n_tokens,
+                           void* o, int64_t o_stride, float* lse, void* ws, size_t ws_bytes, size_t need) {
+  if (s->max_pages < 1 || s->max_pages > kMaxTableRow)
+    return fail(TPK_ERR_INVALID, "max_pages %d out of [1, %d]", s->max_pages, kMaxTableRow);
+  if (n_req < 1 || n_req > kMaxPagedReq) return fail(TPK_ERR_INVALID, "n_req %d out of [1, %d]", n_req, kMaxPagedReq);
+  if (!q || !k_pool || !v_pool || !page_table || !n_tokens || !o || !lse || !ws)
+    return fail(TPK_ERR_INVALID, "null pointer argument");
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(o) || !aligned16(ws))
+    return fail(TPK_ERR_INVALID, "q, pools, o and ws must be 16-byte aligned");
+  const int64_t row = (int64_t)s->kv_heads * s->group * s->head_dim;
+  tpk_status st = check_stride("q_stride", q_stride, row);
+  if (st == TPK_OK) st = check_stride("o_stride", o_stride, row);
+  if (st != TPK_OK) return st;
+  if (ws_bytes < need) return fail(TPK_ERR_NOMEM, "workspace %zu bytes < %zu required", ws_bytes, need);
+  std::memset(&p, 0, sizeof p);
+  p.status = device_status_word();
+  if (!p.status) return fail(TPK_ERR_CUDA, "cannot resolve the device status word");
+  st = make_maps(p, s, k_pool, v_pool);
+  if (st != TPK_OK) return st;
+  p.q = static_cast<const uint16_t*>(q);
+  p.o = o;
+  p.lse = lse;
+  p.table = page_table;
+  p.lens = n_tokens;
+  p.q_stride = q_stride;
+  p.o_stride = o_stride;
+  p.kv_slots = s->kv_slots;
+  p.wait_ns = wait_limit_ns();
+  const float scale = s->sm_scale == 0.f ? 1.f / std::sqrt((float)s->head_dim) : s->sm_scale;
+  p.qscale = scale * kLog2e;
+  p.n_req = n_req;
+  p.max_pages = s->max_pages;
+  p.H = s->kv_heads;
+  p.G = s->group;
+  place_ws(p, n_req, ws);
+  return TPK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old, const int32_t* len_new,
+                                int32_t* page_table, int32_t* free_slots, int free_cap, const int32_t* n_free_in,
+                                int32_t* n_free_out, int32_t* len_out, int32_t* granted, int32_t* tok_off,
+                                int64_t* slot_map, int32_t* positions, int32_t* token_req, int max_tokens,
+                                tpk_stream_t stream) {
+  if (n_req < 1 || n_req > kMaxPagedReq) return fail(TPK_ERR_INVALID, "n_req %d out of [1, %d]", n_req, kMaxPagedReq);
+  if (max_pages < 1 || max_pages > kMaxTableRow || (int64_t)n_req * max_pages > 0x7fffffffLL)
+    return fail(TPK_ERR_INVALID, "page table of %d x %d entries", n_req, max_pages);
+  if (free_cap < 0) return fail(TPK_ERR_INVALID, "free_cap %d < 0", free_cap);
+  if (free_cap > 0x7fffffff - n_req * max_pages) return fail(TPK_ERR_INVALID, "free_cap %d too large", free_cap);
+  if (max_tokens < 0 || max_tokens > 0x7fffffff - 16384) return fail(TPK_ERR_INVALID, "max_tokens %d", max_tokens);
+  if (!len_old || !len_new || !page_table || !n_free_in || !n_free_out || !len_out || !granted || !tok_off ||
+      (free_cap > 0 && !free_slots) || (max_tokens > 0 && (!slot_map || !positions || !token_req)))
+    return fail(TPK_ERR_INVALID, "null pointer argument");
+  TablesParams p;
+  p.len_old = len_old;
+  p.len_new = len_new;
+  p.page_table = page_table;
+  p.free_slots = free_slots;
+  p.n_free_in = n_free_in;
+  p.n_free_out = n_free_out;
+  p.len_out = len_out;
+  p.granted = granted;
+  p.tok_off = tok_off;
+  p.slot_map = slot_map;
+  p.positions = positions;
+  p.token_req = token_req;
+  p.status = device_status_word();
+  if (!p.status) return fail(TPK_ERR_CUDA, "cannot resolve the device status word");
+  p.n_req = n_req;
+  p.max_pages = max_pages;
+  p.free_cap = free_cap;
+  p.max_tokens = max_tokens;
+  const cudaError_t e = launch_tables(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TPK_OK : cuda_fail(e, "tables launch");
+}
+
+tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const int32_t* positions, int n_axes, const uint8_t* axis_of, const float* inv_freq,
+                              int rot_dim, int interleaved, const int64_t* slot_map, void* q_out,
+                              int64_t q_out_stride, void* k_pool, void* v_pool, tpk_stream_t stream) {
+  tpk_status st = check_paged(shape);
+  if (st != TPK_OK) return st;
+  const int H = shape->kv_heads, HQ = H * shape->group, D = shape->head_dim;
+  if (n_tokens < 0) return fail(TPK_ERR_INVALID, "n_tokens %d < 0", n_tokens);
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 16) return fail(TPK_ERR_INVALID, "rot_dim %d (a multiple of 16 up to %d)", rot_dim, D);
+  if (interleaved != 0 && interleaved != 1) return fail(TPK_ERR_INVALID, "interleaved %d (0 or 1)", interleaved);
+  const bool queries = q || q_out, keys = k || v || k_pool || v_pool;
+  if (queries && !(q && q_out)) return fail(TPK_ERR_INVALID, "q and q_out go together");
+  if (keys && !(k && v && k_pool && v_pool)) return fail(TPK_ERR_INVALID, "k, v and both pools go together");
+  if (!queries && !keys) return fail(TPK_ERR_INVALID, "nothing to rotate or store");
+  if (keys && !slot_map) return fail(TPK_ERR_INVALID, "null slot_map");
+  if (rot_dim > 0) {
+    if (!positions || !inv_freq) return fail(TPK_ERR_INVALID, "null positions or inv_freq");
+    if (n_axes < 1 || n_axes > 4) return fail(TPK_ERR_INVALID, "n_axes %d out of [1, 4]", n_axes);
+  }
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool))
+    return fail(TPK_ERR_INVALID, "q, k, v, q_out and pools must be 16-byte aligned");
+  if (queries) {
+    st = check_stride("q_stride", q_stride, (int64_t)HQ * D);
+    if (st == TPK_OK) st = check_stride("q_out_stride", q_out_stride, (int64_t)HQ * D);
+    if (st != TPK_OK) return st;
+    if (q == q_out && q_stride != q_out_stride) return fail(TPK_ERR_INVALID, "q_out is q with another stride");
+  }
+  if (keys) {
+    st = check_stride("k_stride", k_stride, (int64_t)H * D);
+    if (st == TPK_OK) st = check_stride("v_stride", v_stride, (int64_t)H * D);
+    if (st != TPK_OK) return st;
+  }
+  RopeParams p;
+  std::memset(&p, 0, sizeof p);
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    p.axis_of[j] = axis_of ? axis_of[j] : 0;
+    if (p.axis_of[j] >= n_axes) return fail(TPK_ERR_INVALID, "axis_of[%d] = %d of %d axes", j, p.axis_of[j], n_axes);
+  }
+  if (n_tokens == 0) return TPK_OK;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_pool = static_cast<uint16_t*>(k_pool);
+  p.v_pool = static_cast<uint16_t*>(v_pool);
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.slot_map = slot_map;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.slot_limit = shape->kv_slots * kPageTokens;
+  p.status = device_status_word();
+  if (!p.status) return fail(TPK_ERR_CUDA, "cannot resolve the device status word");
+  p.n_tokens = n_tokens;
+  p.H = H;
+  p.HQ = queries ? HQ : 0;
+  p.D = D;
+  p.rot = rot_dim;
+  const cudaError_t e = launch_rope(p, shape->dtype, interleaved, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TPK_OK : cuda_fail(e, "rotary store launch");
+}
+
+size_t tpk_decode_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req) {
+  return sized(shape, n_req) ? split_ws_bytes(shape, n_req) : 0;
+}
+
+tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const void* q, int64_t q_stride,
+                                 const void* k_pool, const void* v_pool, const int32_t* page_table,
+                                 const int32_t* n_tokens, const int32_t* tok_begin, void* o, int64_t o_stride,
+                                 int o_f32, float* lse, void* ws, size_t ws_bytes, tpk_stream_t stream) {
+  tpk_status st = check_paged(shape);
+  if (st != TPK_OK) return st;
+  if (o_f32 != 0 && o_f32 != 1) return fail(TPK_ERR_INVALID, "o_f32 %d (0 or 1)", o_f32);
+  PagedParams p;
+  st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
+                       tpk_decode_paged_workspace_bytes(shape, n_req));
+  if (st != TPK_OK) return st;
+  p.begin = tok_begin;
+  p.o_f32 = o_f32;
+  p.n_q = n_req;
+  const cudaError_t e = launch_paged_split(p, shape->head_dim, shape->dtype, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TPK_OK : cuda_fail(e, "paged decode launch");
+}
+
+size_t tpk_cross_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_q) {
+  return sized(shape, n_req) && n_q >= 0 ? split_ws_bytes(shape, n_req) : 0;
+}
+
+tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q, const void* q, int64_t q_stride,
+                                const int32_t* q_off, const void* k_pool, const void* v_pool,
+                                const int32_t* page_table, const int32_t* n_tokens, const int32_t* kv_range, void* o,
+                                int64_t o_stride, float* lse, void* ws, size_t ws_bytes, tpk_stream_t stream) {
+  tpk_status st = check_paged(shape);
+  if (st != TPK_OK) return st;
+  if (n_q < 0 || (int64_t)n_q * shape->kv_heads * shape->group > 0x7fffffffLL)
+    return fail(TPK_ERR_INVALID, "n_q %d (at most 2^31 query rows)", n_q);
+  if (!q_off) return fail(TPK_ERR_INVALID, "null pointer argument");
+  PagedParams p;
+  st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
+                       tpk_cross_paged_workspace_bytes(shape, n_req, n_q));
+  if (st != TPK_OK) return st;
+  if (n_q == 0) return TPK_OK;
+  p.q_off = q_off;
+  p.range = kv_range;
+  p.n_q = n_q;
+  const cudaError_t e = launch_paged_split(p, shape->head_dim, shape->dtype, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TPK_OK : cuda_fail(e, "cross attention launch");
+}
+
+}  // extern "C"

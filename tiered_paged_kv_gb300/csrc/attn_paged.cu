@@ -1,0 +1,551 @@
+// Attention of few query rows over paged keys and values whose lengths live on the
+// device: one new token per request, or a handful of query tokens per request.
+//
+// A run is 16 query rows of one (request, KV head): the G heads of a new token, or
+// (token, head) pairs of cross attention.  Every run of a request reads the same pages,
+// so request b costs pages_b * runs_b, and its pages of work are numbered request by
+// request, run by run.  Each of the N blocks of the launch takes an equal range of
+// those numbers, whatever the lengths: the device stays evenly loaded and the split
+// needs no host-side lengths.  A run inside one block's range is written out at once;
+// one that crosses ranges leaves a partial (running maximum, sum, unnormalised o) in
+// the block's two workspace slots -- slot 0: a run entered in the middle, slot 1: one
+// left before its end -- and the fold kernel joins the partials in block order.
+//
+// Within a block a producer warp walks the range and feeds a ring of page stages by TMA
+// (64 tokens of keys and of values, 128-byte swizzle); four consumer warps take 16 of
+// the 64 tokens each and keep their own online softmax, joined when a run ends.  Both
+// products run on mma.sync m16n8k16 with float32 accumulators.  The weights enter PV
+// as two 16-bit planes (the rounded weight and what the rounding left, about 16 bits in
+// bfloat16), so they add no error of their own next to the rounding of the output; with
+// at most 8 query rows the planes are the two halves of one 16-row operand and cost
+// nothing.  A tensor tile of 128 rows would hold 8 or 16 useful ones; the few rows make
+// the kernel bound by HBM (4 H D bytes per attended token against 4 H G D operations).
+#include "paged.cuh"
+
+namespace tpk {
+
+constexpr int kConsumers = 4;
+constexpr int kPagedThreads = (kConsumers + 1) * 32;
+constexpr float kEmpty = -__builtin_huge_valf();
+
+template <int D>
+struct SplitCfg {
+  static constexpr int kPageBytes = kPageTokens * D * 2;   // keys or values of one page
+  static constexpr int kStageBytes = 2 * kPageBytes;
+  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 3 : 4;
+  static constexpr int kBlocksPerSm = D == 256 ? 1 : D == 128 ? 2 : 3;
+  static constexpr int kRowStride = D + 8;  // floats: spreads the rows of the joined o over the banks
+  static constexpr int kJoinBytes = kConsumers * 8 * kRowStride * 4;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kJoinBytes;
+};
+
+struct SplitShared {
+  uint64_t full[4];
+  uint64_t empty[4];
+  int valid[4];
+  float m[kConsumers][kRowTile];
+  float l[kConsumers][kRowTile];
+  int64_t scan[kPagedThreads / 32];
+  int64_t total;
+  int64_t lo;       // this block's range starts here
+  int64_t base;     // first number of the request it starts in
+  int first;        // that request
+};
+
+// Runs and pages of request b.
+__device__ __forceinline__ int request_runs(const PagedParams& p, int b) {
+  int first, count;
+  request_rows(p, b, first, count);
+  return p.H * (int)(((int64_t)count * p.G + kRowTile - 1) / kRowTile);
+}
+__device__ __forceinline__ int request_pages(const PagedParams& p, int b, int& page0) {
+  int lo, hi;
+  request_span(p, b, lo, hi);
+  page0 = lo >> 6;
+  return hi > lo ? ((hi + 63) >> 6) - page0 : 0;
+}
+__device__ __forceinline__ int64_t per_block(int64_t total, int blocks) { return (total + blocks - 1) / blocks; }
+
+// One stretch of pages of one run.
+struct Segment {
+  int b, run, page, count, pages;  // pages [page, page + count) of the run's `pages`
+  int page0;                       // the run's first page in the request
+};
+
+// Steps through a block's range, segment by segment.
+struct Walk {
+  int64_t at, end, base;
+  int b;
+  __device__ __forceinline__ bool next(const PagedParams& p, Segment& s) {
+    if (at >= end) return false;
+    for (;;) {
+      s.pages = request_pages(p, b, s.page0);
+      const int64_t work = (int64_t)s.pages * request_runs(p, b);
+      if (at < base + work) break;
+      base += work;
+      ++b;
+    }
+    const int64_t local = at - base;
+    s.b = b;
+    s.run = (int)(local / s.pages);
+    s.page = (int)(local - (int64_t)s.run * s.pages);
+    s.count = (int)min((int64_t)(s.pages - s.page), end - at);
+    at += s.count;
+    return true;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void store_pair(const PagedParams& p, int64_t row, int head, int D, int c, float x, float y) {
+  const int64_t at = row * p.o_stride + (int64_t)head * D + c;
+  if (p.o_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at) = make_float2(x, y);
+  else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at) = T::pack(x, y);
+}
+
+// Row r of a run: its query token and query head; false past the run's last row.
+__device__ __forceinline__ bool run_row(const PagedParams& p, int first, int count, int h, int tile, int r, int& token,
+                                        int& head) {
+  const int64_t i = (int64_t)tile * kRowTile + r;
+  if (i >= (int64_t)count * p.G) return false;
+  const int t = (int)(i / p.G);
+  token = first + t;
+  head = h * p.G + (int)(i - (int64_t)t * p.G);
+  return true;
+}
+
+template <typename T, int D, bool kSmall>  // kSmall: runs have at most 8 rows
+__global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_constant__ PagedParams p) {
+  using C = SplitCfg<D>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  float* join = reinterpret_cast<float*>(stages + C::kStages * C::kStageBytes);
+  __shared__ SplitShared S;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // ---- the numbering: this block's range, and (block 0) the table for the fold
+  if (tid < C::kStages) {
+    mbar_init(&S.full[tid], 1);
+    mbar_init(&S.empty[tid], kConsumers);
+    fence_mbar_init();
+  }
+  const int each = (p.n_req + kPagedThreads - 1) / kPagedThreads;
+  const int b0 = min(tid * each, p.n_req), b1 = min(b0 + each, p.n_req);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    int page0;
+    mine += (int64_t)request_pages(p, b, page0) * request_runs(p, b);
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += up;
+  }
+  if (lane == 31) S.scan[warp] = inc;
+  if (tid == 0) S.first = -1;
+  __syncthreads();
+  int64_t total = 0, before = inc - mine;
+#pragma unroll
+  for (int w = 0; w < kPagedThreads / 32; ++w) {
+    if (w < warp) before += S.scan[w];
+    total += S.scan[w];
+  }
+  const int64_t per = per_block(total, gridDim.x);
+  const int64_t lo = min(per * blockIdx.x, total), hi = min(lo + per, total);
+  if ((lo < hi && lo >= before && lo < before + mine) || blockIdx.x == 0) {
+    int64_t at = before;
+    for (int b = b0; b < b1; ++b) {
+      int page0;
+      const int64_t work = (int64_t)request_pages(p, b, page0) * request_runs(p, b);
+      if (lo < hi && lo >= at && lo < at + work) {
+        S.first = b;
+        S.base = at;
+      }
+      if (blockIdx.x == 0) p.prefix[b] = at;
+      at += work;
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) p.prefix[p.n_req] = total;
+  __syncthreads();
+
+  // ---- requests that attend nothing
+  for (int b = blockIdx.x; b < p.n_req; b += gridDim.x) {
+    int page0, first, count;
+    if (request_pages(p, b, page0) > 0) continue;
+    request_rows(p, b, first, count);
+    const int HQ = p.H * p.G;
+    for (int64_t i = tid; i < (int64_t)count * HQ * (D / 2); i += kPagedThreads) {
+      const int64_t r = i / (D / 2);
+      store_pair<T>(p, first + r / HQ, (int)(r % HQ), D, (int)(i % (D / 2)) * 2, 0.f, 0.f);
+    }
+    for (int64_t i = tid; i < (int64_t)count * HQ; i += kPagedThreads) p.lse[(int64_t)first * HQ + i] = kEmpty;
+  }
+  if (lo >= hi) return;
+
+  Walk walk{lo, hi, S.base, S.first};
+  Segment s;
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------- producer
+    int item = 0;
+    bool dead = false;
+    while (!dead && walk.next(p, s)) {
+      const int tiles = request_runs(p, s.b) / p.H;
+      const int h = s.run / tiles;
+      const int32_t* row = p.table + (int64_t)s.b * p.max_pages + s.page0 + s.page;
+      for (int j0 = 0; j0 < s.count && !dead; j0 += 32) {
+        const int entry = j0 + lane < s.count ? row[j0 + lane] : 0;
+        const int n = min(32, s.count - j0);
+        for (int j = 0; j < n; ++j, ++item) {
+          const int64_t slot = __shfl_sync(0xffffffffu, entry, j);
+          const int st = item % C::kStages;
+          if (item >= C::kStages) {
+            const bool ok = mbar_wait(&S.empty[st], ((item / C::kStages) - 1) & 1, p.status, p.wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) {
+              dead = true;
+              break;
+            }
+          }
+          if (lane == 0) {
+            const bool ok = slot >= 0 && slot < p.kv_slots;
+            S.valid[st] = ok;
+            if (ok) {
+              uint8_t* k = stages + st * C::kStageBytes;
+              const int y = (int)((slot * p.H + h) * kPageTokens);
+              mbar_arrive_expect_tx(&S.full[st], C::kStageBytes);
+#pragma unroll
+              for (int c = 0; c < D; c += 64) tma_load_2d(k + c * 128, &p.kmap, c, y, &S.full[st]);
+#pragma unroll
+              for (int c = 0; c < D; c += 64)
+                tma_load_2d(k + C::kPageBytes + c * 128, &p.vmap, c, y, &S.full[st]);
+            } else {
+              atomicOr(p.status, kStatusBadSlot);
+              mbar_arrive(&S.full[st]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (dead)  // let the copies in flight land before the block ends
+      for (int i = max(0, item - C::kStages); i < item; ++i)
+        mbar_wait(&S.full[i % C::kStages], (i / C::kStages) & 1, p.status, p.wait_ns);
+    return;
+  }
+
+  // --------------------------------------------------------------- consumers
+  // Thread (g, t) = (lane / 4, lane % 4) owns query row g (and g + 8), and of each
+  // 8-token (8-channel) tile tokens (channels) 2t and 2t + 1.
+  const int g = lane >> 2, t = lane & 3;
+  const int r8 = lane & 7, i8 = lane >> 3;  // ldmatrix: row r8 of matrix i8
+  bool dead = false;
+  int item = 0;
+  while (walk.next(p, s)) {
+    int first, count, tok_lo, tok_hi;
+    request_rows(p, s.b, first, count);
+    request_span(p, s.b, tok_lo, tok_hi);
+    const int tiles = request_runs(p, s.b) / p.H;
+    const int h = s.run / tiles, tile = s.run - h * tiles;
+    // ---- the query rows as A operands, and the tokens each row sees
+    uint32_t q[D / 16][kSmall ? 2 : 4];
+    int see_lo[2], see_hi[2];
+#pragma unroll
+    for (int half = 0; half < (kSmall ? 1 : 2); ++half) {
+      int token, head;
+      const bool live = run_row(p, first, count, h, tile, g + 8 * half, token, head);
+      see_lo[half] = tok_lo;
+      see_hi[half] = live ? tok_hi : tok_lo;
+      if (live && p.range) {
+        see_lo[half] = max(tok_lo, p.range[2 * (int64_t)token]);
+        see_hi[half] = min(tok_hi, p.range[2 * (int64_t)token + 1]);
+      }
+      const uint32_t* src =
+          reinterpret_cast<const uint32_t*>(p.q + (live ? (int64_t)token * p.q_stride + (int64_t)head * D : 0));
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][half] = live ? src[8 * k + t] : 0;
+        q[k][half + (kSmall ? 1 : 2)] = live ? src[8 * k + t + 4] : 0;
+      }
+    }
+    float acc[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+    float m[2] = {kEmpty, kEmpty}, l[2] = {0.f, 0.f};
+
+    for (int j = 0; j < s.count; ++j, ++item) {
+      const int st = item % C::kStages;
+      if (!dead) {
+        const bool ok = mbar_wait(&S.full[st], (item / C::kStages) & 1, p.status, p.wait_ns);
+        dead = !__all_sync(0xffffffffu, ok);
+      }
+      if (!dead && S.valid[st]) {
+        uint8_t* ks = stages + st * C::kStageBytes;
+        uint8_t* vs = ks + C::kPageBytes;
+        const int tok0 = (s.page0 + s.page + j) * kPageTokens + warp * 16;  // this warp's first token
+        // rows outside the request's span may hold NaN: their weight is 0, their
+        // values are cleared
+        if (tok0 < tok_lo || tok0 + 16 > tok_hi) {
+          for (int i = lane; i < 16 * (D / 8); i += 32) {
+            const int r = i / (D / 8), c = i % (D / 8);
+            if (tok0 + r < tok_lo || tok0 + r >= tok_hi)
+              *reinterpret_cast<uint4*>(vs + (c >> 3) * 8192 + (warp * 16 + r) * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();  // the stage is filled by TMA again later
+          __syncwarp();
+        }
+        // ---- scores of 16 tokens: two 8-token tiles, two chains each
+        float sc[2][2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[n][x][e] = 0.f;
+        const uint32_t krow = smem_u32(ks) + (warp * 16 + (i8 >> 1) * 8 + r8) * 128;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t kb[4], a[4];
+          const int c = 2 * k + (i8 & 1);  // 16-byte piece of the row
+          ldmatrix_x4(kb, krow + (c >> 3) * 8192 + (((c & 7) ^ r8) << 4));
+          a[0] = q[k][0];
+          a[1] = kSmall ? 0 : q[k][1];
+          a[2] = q[k][kSmall ? 1 : 2];
+          a[3] = kSmall ? 0 : q[k][3];
+          T::mma(sc[0][k & 1], a, kb[0], kb[1]);
+          T::mma(sc[1][k & 1], a, kb[2], kb[3]);
+        }
+        // ---- online softmax in base 2
+        uint32_t hi[2][2], lw[2][2];  // [row half][token tile]: rounded weights, and what that left
+        float scale[2];
+        bool same = true;
+#pragma unroll
+        for (int half = 0; half < (kSmall ? 1 : 2); ++half) {
+          float x[4];
+          float top = kEmpty;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = e >> 1, w = 2 * half + (e & 1);
+            const int tok = tok0 + 8 * n + 2 * t + (e & 1);
+            const bool seen = tok >= see_lo[half] && tok < see_hi[half];
+            x[e] = seen ? (sc[n][0][w] + sc[n][1][w]) * p.qscale : kEmpty;
+            top = fmaxf(top, x[e]);
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float mn = fmaxf(m[half], top);
+          const float ref = mn == kEmpty ? 0.f : mn;
+          scale[half] = exp2f(m[half] - ref);  // 0 while nothing was seen
+          same = same && (mn == m[half]);
+          m[half] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = exp2f(x[e] - ref);
+            sum += x[e];
+          }
+          l[half] = l[half] * scale[half] + sum;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            hi[half][n] = T::pack(x[2 * n], x[2 * n + 1]);
+            const float2 back = T::unpack(hi[half][n]);
+            lw[half][n] = T::pack(x[2 * n] - back.x, x[2 * n + 1] - back.y);
+          }
+        }
+        if (!__all_sync(0xffffffffu, same)) {
+          const float s0 = scale[0], s1 = kSmall ? scale[0] : scale[1];
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            acc[n][0] *= s0;
+            acc[n][1] *= s0;
+            acc[n][2] *= s1;
+            acc[n][3] *= s1;
+          }
+        }
+        // ---- o += weights * values (16 tokens: one k step)
+        uint32_t a[4], a2[4];
+        if (kSmall) {
+          a[0] = hi[0][0];
+          a[1] = lw[0][0];
+          a[2] = hi[0][1];
+          a[3] = lw[0][1];
+        } else {
+          a[0] = hi[0][0];
+          a[1] = hi[1][0];
+          a[2] = hi[0][1];
+          a[3] = hi[1][1];
+          a2[0] = lw[0][0];
+          a2[1] = lw[1][0];
+          a2[2] = lw[0][1];
+          a2[3] = lw[1][1];
+        }
+        const uint32_t vrow = smem_u32(vs) + (warp * 16 + (i8 & 1) * 8 + r8) * 128;
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t vb[4];
+          const int c = 2 * n + (i8 >> 1);
+          ldmatrix_x4_trans(vb, vrow + (c >> 3) * 8192 + (((c & 7) ^ r8) << 4));
+          T::mma(acc[2 * n], a, vb[0], vb[1]);
+          T::mma(acc[2 * n + 1], a, vb[2], vb[3]);
+          if (!kSmall) {
+            T::mma(acc[2 * n], a2, vb[0], vb[1]);
+            T::mma(acc[2 * n + 1], a2, vb[2], vb[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.empty[st]);
+    }
+
+    // ---- join the four warps' states
+#pragma unroll
+    for (int half = 0; half < (kSmall ? 1 : 2); ++half) {
+      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+      if (t == 0) {
+        S.m[warp][g + 8 * half] = m[half];
+        S.l[warp][g + 8 * half] = l[half];
+      }
+    }
+    named_barrier(1, kConsumers * 32);
+    const bool whole = s.count == s.pages;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (s.page == 0 ? 1 : 0);
+    const int HQ = p.H * p.G;
+#pragma unroll
+    for (int half = 0; half < (kSmall ? 1 : 2); ++half) {
+      float top = kEmpty;
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, S.m[w][g + 8 * half]);
+      const float f = m[half] == kEmpty ? 0.f : exp2f(m[half] - top);
+      float* dst = join + (warp * 8 + g) * C::kRowStride + 2 * t;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        const float x = kSmall ? acc[n][0] + acc[n][2] : acc[n][2 * half];
+        const float y = kSmall ? acc[n][1] + acc[n][3] : acc[n][2 * half + 1];
+        *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(x * f, y * f);
+      }
+      named_barrier(1, kConsumers * 32);
+      // 16 threads per row
+      const int row = tid >> 4, r = row + 8 * half;
+      float M = kEmpty, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, S.m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w)
+        if (S.m[w][r] != kEmpty) L += exp2f(S.m[w][r] - M) * S.l[w][r];
+      int token, head;
+      if (run_row(p, first, count, h, tile, r, token, head) && !dead) {
+        const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        for (int c = (tid & 15) * 2; c < D; c += 32) {
+          float x = 0.f, y = 0.f;
+#pragma unroll
+          for (int w = 0; w < kConsumers; ++w) {
+            const float2 v = *reinterpret_cast<const float2*>(join + (w * 8 + row) * C::kRowStride + c);
+            x += v.x;
+            y += v.y;
+          }
+          if (whole) store_pair<T>(p, token, head, D, c, x * inv, y * inv);
+          else *reinterpret_cast<float2*>(p.part_o + (slot * kRowTile + r) * D + c) = make_float2(x, y);
+        }
+        if ((tid & 15) == 0) {
+          if (whole) {
+            p.lse[(int64_t)token * HQ + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
+          } else {
+            p.part_ml[slot * kRowTile + r] = M;
+            p.part_ml[(2 * (int64_t)gridDim.x + slot) * kRowTile + r] = L;
+          }
+        }
+      }
+      named_barrier(1, kConsumers * 32);
+    }
+  }
+}
+
+// Joins the partials of the runs that cross block ranges: block (i, r) takes row r of
+// the run that holds the first number of range i + 1, if range i is the run's first.
+template <typename T, int D>
+__global__ void __launch_bounds__(D / 4) fold_paged_kernel(const __grid_constant__ PagedParams p, int blocks, int rows) {
+  const int i = blockIdx.x / rows, r = blockIdx.x % rows, c = threadIdx.x * 4;
+  const int64_t total = p.prefix[p.n_req];
+  const int64_t per = per_block(total, blocks);
+  const int64_t cut = per * (i + 1);
+  if (cut >= total) return;
+  int lo = 0, hi = p.n_req - 1;
+  while (lo < hi) {  // the request that holds number `cut`
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.prefix[mid] <= cut) lo = mid; else hi = mid - 1;
+  }
+  const int b = lo;
+  int page0, first, count, token, head;
+  const int pages = request_pages(p, b, page0);
+  const int64_t base = p.prefix[b];
+  const int run = (int)((cut - base) / pages);
+  const int64_t start = base + (int64_t)run * pages, end = start + pages;
+  if (start == cut || start < per * i) return;  // not crossed here, or joined at an earlier cut
+  request_rows(p, b, first, count);
+  const int tiles = request_runs(p, b) / p.H;
+  const int h = run / tiles;
+  if (!run_row(p, first, count, h, run - h * tiles, r, token, head)) return;
+  const int n = (int)((end - 1) / per) - i + 1;  // blocks i .. i + n - 1 hold a piece
+  // block i left the run before its end, the others entered it in the middle
+  auto slot = [&](int k) { return (2 * (int64_t)(i + k) + (k == 0 ? 1 : 0)) * kRowTile + r; };
+  const float* part_l = p.part_ml + 2 * (int64_t)blocks * kRowTile;
+  float M = kEmpty;
+  for (int k = 0; k < n; ++k) M = fmaxf(M, p.part_ml[slot(k)]);
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M != kEmpty) {
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const int64_t at = slot(k);
+      const float w = exp2f(p.part_ml[at] - M);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + c);
+      L += w * part_l[at];
+      o.x += w * v.x;
+      o.y += w * v.y;
+      o.z += w * v.z;
+      o.w += w * v.w;
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  store_pair<T>(p, token, head, D, c, o.x * inv, o.y * inv);
+  store_pair<T>(p, token, head, D, c + 2, o.z * inv, o.w * inv);
+  if (c == 0) p.lse[(int64_t)token * p.H * p.G + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
+}
+
+int device_sms();
+
+template <typename T, int D, bool kSmall>
+static cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
+  using C = SplitCfg<D>;
+  static DeviceOnce once;
+  cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(split_kernel<T, D, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int blocks = min(device_sms() * C::kBlocksPerSm, kPagedMaxBlocks);
+  split_kernel<T, D, kSmall><<<blocks, kPagedThreads, C::kSmem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || blocks == 1) return e;
+  const int rows = p.q_off ? kRowTile : min(p.G, kRowTile);
+  fold_paged_kernel<T, D><<<(blocks - 1) * rows, D / 4, 0, stream>>>(p, blocks, rows);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+static cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
+  return !p.q_off && p.G <= 8 ? launch_t<T, D, true>(p, stream) : launch_t<T, D, false>(p, stream);
+}
+
+template <typename T>
+static cudaError_t launch_dim(const PagedParams& p, int D, cudaStream_t stream) {
+  return D == 64 ? launch_rows<T, 64>(p, stream) : D == 128 ? launch_rows<T, 128>(p, stream)
+                                                            : launch_rows<T, 256>(p, stream);
+}
+
+cudaError_t launch_paged_split(const PagedParams& p, int D, int dtype, cudaStream_t stream) {
+  return dtype == 0 ? launch_dim<Bf16>(p, D, stream) : launch_dim<F16>(p, D, stream);
+}
+
+}  // namespace tpk

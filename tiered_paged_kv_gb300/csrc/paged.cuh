@@ -1,0 +1,150 @@
+// What the kernels over device-side lengths share: the launch parameters, the two
+// 16-bit types, the warp-level matrix and shared-memory instructions as inline PTX.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace tpk {
+
+constexpr int kMaxPagedReq = 4096;
+
+// ------------------------------------------------------------------ tables
+struct TablesParams {
+  const int32_t* len_old;
+  const int32_t* len_new;
+  int32_t* page_table;
+  int32_t* free_slots;
+  const int32_t* n_free_in;
+  int32_t* n_free_out;
+  int32_t* len_out;
+  int32_t* granted;
+  int32_t* tok_off;
+  int64_t* slot_map;
+  int32_t* positions;
+  int32_t* token_req;
+  int* status;
+  int n_req, max_pages, free_cap, max_tokens;
+};
+cudaError_t launch_tables(const TablesParams& p, cudaStream_t stream);
+
+// ------------------------------------------------------------ rotary store
+struct RopeParams {
+  const uint16_t* q;  // null: no queries
+  const uint16_t* k;  // null: no keys and values
+  const uint16_t* v;
+  uint16_t* q_out;
+  uint16_t* k_pool;
+  uint16_t* v_pool;
+  const int32_t* positions;
+  const float* inv_freq;
+  const int64_t* slot_map;  // null: every row is live
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int64_t slot_limit;  // kv_slots * 64
+  int* status;
+  int n_tokens, H, HQ, D, rot;
+  uint8_t axis_of[128];
+};
+cudaError_t launch_rope(const RopeParams& p, int dtype, int interleaved, cudaStream_t stream);
+
+// --------------------------------------------------------------- attention
+struct PagedParams {
+  CUtensorMap kmap;  // pools as 2-D tensors [slot * H * 64][D], 64 x 64 boxes, 128-byte swizzle
+  CUtensorMap vmap;
+  const uint16_t* q;
+  void* o;
+  float* lse;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* begin;  // decode: first token attended, or null
+  const int32_t* q_off;  // cross: where each request's query rows begin; null: decode
+  const int32_t* range;  // cross: [n_q][2] or null
+  int64_t* prefix;       // workspace: pages of work before each request
+  float* part_ml;        // workspace: [slot][16] running maximum, then [slot][16] sum
+  float* part_o;         // workspace: [slot][16][D], not normalised
+  int* status;
+  int64_t q_stride, o_stride, kv_slots;
+  uint64_t wait_ns;
+  float qscale;  // sm_scale * log2(e)
+  int n_req, n_q, max_pages, H, G, o_f32;
+};
+
+constexpr int kPagedMaxBlocks = 512;  // blocks of a split launch; each owns two partial slots
+constexpr int kRowTile = 16;          // query rows of a split unit
+cudaError_t launch_paged_split(const PagedParams& p, int D, int dtype, cudaStream_t stream);
+
+// ------------------------------------------------------------------- types
+struct Bf16 {
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+struct F16 {
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return __half22float2(*reinterpret_cast<__half2*>(&w));
+  }
+  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Request b's attended tokens [lo, hi), cut into what its table row can hold.
+__device__ __forceinline__ void request_span(const PagedParams& p, int b, int& lo, int& hi) {
+  const int cap = p.max_pages * 64;
+  const int n = p.lens[b];
+  hi = min(max(n, 0), cap);
+  lo = 0;
+  bool bad = n != hi;
+  if (p.begin) {
+    const int a = p.begin[b];
+    lo = min(max(a, 0), cap);
+    bad |= a != lo;
+  }
+  if (bad) atomicOr(p.status, kStatusBadSlot);
+}
+
+// Request b's query rows: tokens [first, first + count) of q.
+__device__ __forceinline__ void request_rows(const PagedParams& p, int b, int& first, int& count) {
+  if (!p.q_off) {
+    first = b;
+    count = 1;
+    return;
+  }
+  first = min(max(p.q_off[b], 0), p.n_q);
+  count = max(min(max(p.q_off[b + 1], 0), p.n_q) - first, 0);
+}
+
+}  // namespace tpk
