@@ -2,6 +2,7 @@
 // and launches.  Lengths, tables and slot maps stay on the device, so what can be
 // checked here is shapes, strides, alignment and sizes; the kernels clamp or skip the
 // rest and report it in the device status word.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -100,6 +101,31 @@ void place_ws(PagedParams& p, int n_req, void* ws) {
   p.part_o = reinterpret_cast<float*>(w);
 }
 
+// How cross attention of n_q tokens is cut: `groups` bounds the row-tile blocks of one
+// KV head (whole ones, and one per request that is not), `splits` parts of the keys
+// fill the device where those are few; groups = 0: few rows per request, the split
+// kernel's 16-row units fit them better.
+struct CrossPlan {
+  int groups, splits;
+};
+CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
+  const int64_t rows = (int64_t)n_q * s->group;
+  if (rows <= (int64_t)kRowTile * n_req) return {0, 1};
+  const int R = tile_rows(s->head_dim);
+  const int64_t groups = rows / R + n_req;
+  const int64_t blocks = groups * s->kv_heads;
+  const int64_t splits = std::min<int64_t>(kTileBlocks / blocks, (s->max_pages + 3) / 4);  // two key tiles a part
+  return {(int)groups, (int)std::max<int64_t>(splits, 1)};
+}
+
+size_t cross_ws_bytes(const tpk_paged_shape* s, int n_req, int n_q) {
+  const CrossPlan c = cross_plan(s, n_req, n_q);
+  if (c.groups == 0) return split_ws_bytes(s, n_req);
+  if (c.splits == 1) return 256;
+  const size_t rows = (size_t)c.groups * s->kv_heads * c.splits * tile_rows(s->head_dim);
+  return align256(rows * 8) + rows * s->head_dim * 4;
+}
+
 bool sized(const tpk_paged_shape* s, int n_req) {
   return s && n_req >= 1 && n_req <= kMaxPagedReq && (s->head_dim == 64 || s->head_dim == 128 || s->head_dim == 256);
 }
@@ -140,7 +166,6 @@ tpk_status begin_attention(PagedParams& p, const tpk_paged_shape* s, int n_req, 
   p.max_pages = s->max_pages;
   p.H = s->kv_heads;
   p.G = s->group;
-  place_ws(p, n_req, ws);
   return TPK_OK;
 }
 
@@ -265,6 +290,7 @@ tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const 
   st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
                        tpk_decode_paged_workspace_bytes(shape, n_req));
   if (st != TPK_OK) return st;
+  place_ws(p, n_req, ws);
   p.begin = tok_begin;
   p.o_f32 = o_f32;
   p.n_q = n_req;
@@ -273,7 +299,7 @@ tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const 
 }
 
 size_t tpk_cross_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_q) {
-  return sized(shape, n_req) && n_q >= 0 ? split_ws_bytes(shape, n_req) : 0;
+  return sized(shape, n_req) && n_q >= 0 && shape->kv_heads > 0 && shape->group > 0 ? cross_ws_bytes(shape, n_req, n_q) : 0;
 }
 
 tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q, const void* q, int64_t q_stride,
@@ -293,7 +319,20 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
   p.q_off = q_off;
   p.range = kv_range;
   p.n_q = n_q;
-  const cudaError_t e = launch_paged_split(p, shape->head_dim, shape->dtype, reinterpret_cast<cudaStream_t>(stream));
+  const CrossPlan plan = cross_plan(shape, n_req, n_q);
+  cudaError_t e;
+  if (plan.groups == 0) {
+    place_ws(p, n_req, ws);
+    e = launch_paged_split(p, shape->head_dim, shape->dtype, reinterpret_cast<cudaStream_t>(stream));
+  } else {
+    const size_t rows = (size_t)plan.groups * shape->kv_heads * plan.splits * tile_rows(shape->head_dim);
+    p.part_ml = static_cast<float*>(ws);
+    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(rows * 8));
+    if ((int64_t)plan.groups * shape->kv_heads * plan.splits * tile_rows(shape->head_dim) > 0x7fffffffLL)
+      return fail(TPK_ERR_UNSUPPORTED, "too many query rows");
+    e = launch_cross_tiles(p, shape->head_dim, shape->dtype, plan.groups, plan.splits,
+                           reinterpret_cast<cudaStream_t>(stream));
+  }
   return e == cudaSuccess ? TPK_OK : cuda_fail(e, "cross attention launch");
 }
 

@@ -74,6 +74,10 @@ constexpr int kPagedMaxBlocks = 512;  // blocks of a split launch; each owns two
 constexpr int kRowTile = 16;          // query rows of a split unit
 cudaError_t launch_paged_split(const PagedParams& p, int D, int dtype, cudaStream_t stream);
 
+constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row tiles aims at
+int tile_rows(int D);             // query rows of one of its blocks
+cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int groups, int splits, cudaStream_t stream);
+
 // ------------------------------------------------------------------- types
 struct Bf16 {
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
