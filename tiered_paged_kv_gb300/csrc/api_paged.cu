@@ -63,27 +63,29 @@ tpk_status check_stride(const char* what, int64_t stride, int64_t least) {
   return TPK_OK;
 }
 
-// Pools as 2-D tensors [slot * H * 64][D] with page-high boxes of 64 channels and the
-// 128-byte swizzle.
-tpk_status make_maps(PagedParams& p, const tpk_paged_shape* s, const void* k_pool, const void* v_pool) {
+// A tensor of 16-bit values with boxes of 64 channels and the 128-byte swizzle.
+tpk_status make_map(CUtensorMap* map, int dtype, int rank, const void* base, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* box) {
   typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
   EncodeFn fn = reinterpret_cast<EncodeFn>(tensor_map_encoder());
   if (!fn) return fail(TPK_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, dtype == TPK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? TPK_OK : fail(TPK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+// Pools as [slot * H * 64][D], page-high boxes.
+tpk_status make_maps(PagedParams& p, const tpk_paged_shape* s, const void* k_pool, const void* v_pool) {
   const cuuint64_t dims[2] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->kv_slots * s->kv_heads * kPageTokens};
   const cuuint64_t strides[1] = {(cuuint64_t)s->head_dim * 2};
-  const cuuint32_t box[2] = {64, kPageTokens}, estr[2] = {1, 1};
-  const void* pools[2] = {k_pool, v_pool};
-  CUtensorMap* maps[2] = {&p.kmap, &p.vmap};
-  for (int i = 0; i < 2; ++i) {
-    const CUresult r = fn(maps[i], s->dtype == TPK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                          2, const_cast<void*>(pools[i]), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(TPK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
-  }
-  return TPK_OK;
+  const cuuint32_t box[2] = {64, kPageTokens};
+  const tpk_status st = make_map(&p.kmap, s->dtype, 2, k_pool, dims, strides, box);
+  return st == TPK_OK ? make_map(&p.vmap, s->dtype, 2, v_pool, dims, strides, box) : st;
 }
 
 // Workspace of a split launch: the numbering table, then the partials.
@@ -101,28 +103,33 @@ void place_ws(PagedParams& p, int n_req, void* ws) {
   p.part_o = reinterpret_cast<float*>(w);
 }
 
-// How cross attention of n_q tokens is cut: `groups` bounds the row-tile blocks of one
+// How cross attention of n_q tokens is cut: `groups` bounds the row-tile groups of one
 // KV head (whole ones, and one per request that is not), `splits` parts of the keys
 // fill the device where those are few; groups = 0: few rows per request, the split
 // kernel's 16-row units fit them better.
 struct CrossPlan {
-  int groups, splits;
+  int tiles, groups, splits;
+  int64_t rows(const tpk_paged_shape* s) const {  // of all blocks
+    return (int64_t)groups * s->kv_heads * splits * tiles * kTileRows;
+  }
 };
 CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
   const int64_t rows = (int64_t)n_q * s->group;
-  if (rows <= (int64_t)kRowTile * n_req) return {0, 1};
-  const int R = tile_rows(s->head_dim);
-  const int64_t groups = rows / R + n_req;
+  if (rows <= (int64_t)kRowTile * n_req) return {0, 0, 1};
+  // two tiles share the keys and values, unless most of the second would be empty
+  const int64_t per_tile = kTileRows / s->group;
+  const int tiles = s->head_dim == 256 || n_q <= per_tile * n_req ? 1 : 2;
+  const int64_t groups = n_q / (tiles * per_tile) + n_req;
   const int64_t blocks = groups * s->kv_heads;
   const int64_t splits = std::min<int64_t>(kTileBlocks / blocks, (s->max_pages + 3) / 4);  // two key tiles a part
-  return {(int)groups, (int)std::max<int64_t>(splits, 1)};
+  return {tiles, (int)groups, (int)std::max<int64_t>(splits, 1)};
 }
 
 size_t cross_ws_bytes(const tpk_paged_shape* s, int n_req, int n_q) {
   const CrossPlan c = cross_plan(s, n_req, n_q);
   if (c.groups == 0) return split_ws_bytes(s, n_req);
   if (c.splits == 1) return 256;
-  const size_t rows = (size_t)c.groups * s->kv_heads * c.splits * tile_rows(s->head_dim);
+  const size_t rows = (size_t)c.rows(s);
   return align256(rows * 8) + rows * s->head_dim * 4;
 }
 
@@ -325,12 +332,16 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
     place_ws(p, n_req, ws);
     e = launch_paged_split(p, shape->head_dim, shape->dtype, reinterpret_cast<cudaStream_t>(stream));
   } else {
-    const size_t rows = (size_t)plan.groups * shape->kv_heads * plan.splits * tile_rows(shape->head_dim);
+    const int64_t rows = plan.rows(shape);
+    if (rows > 0x7fffffffLL) return fail(TPK_ERR_UNSUPPORTED, "too many query rows");
+    const cuuint64_t dims[3] = {(cuuint64_t)shape->head_dim, (cuuint64_t)shape->kv_heads * shape->group, (cuuint64_t)n_q};
+    const cuuint64_t strides[2] = {(cuuint64_t)shape->head_dim * 2, (cuuint64_t)q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)shape->group, (cuuint32_t)(kTileRows / shape->group)};
+    st = make_map(&p.qmap, shape->dtype, 3, q, dims, strides, box);
+    if (st != TPK_OK) return st;
     p.part_ml = static_cast<float*>(ws);
-    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(rows * 8));
-    if ((int64_t)plan.groups * shape->kv_heads * plan.splits * tile_rows(shape->head_dim) > 0x7fffffffLL)
-      return fail(TPK_ERR_UNSUPPORTED, "too many query rows");
-    e = launch_cross_tiles(p, shape->head_dim, shape->dtype, plan.groups, plan.splits,
+    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256((size_t)rows * 8));
+    e = launch_cross_tiles(p, shape->head_dim, shape->dtype, plan.tiles, plan.groups, plan.splits,
                            reinterpret_cast<cudaStream_t>(stream));
   }
   return e == cudaSuccess ? TPK_OK : cuda_fail(e, "cross attention launch");

@@ -1,17 +1,25 @@
 // Cross attention of many query rows on the fifth-generation tensor cores.
 //
-// A thread block takes 128-row tiles of one (request, KV head), rows being packed
-// (query token, head) pairs: two tiles for D <= 128, one for D = 256 or where the rows
-// end.  The keys and values pass once, 128 tokens (two pages) at a time, through a ring
-// of shared-memory slots filled by TMA.  Per key tile S = Q K^T goes to TMEM, one thread
-// per row turns its 128 scores into weights (online softmax in base 2), writes them over
-// S in the input type, and O += P V runs with P read from TMEM as the A operand.
+// An item is one or two 128-row tiles of one (request, KV head), rows being packed (query
+// token, head) pairs: two tiles share the keys and values for D <= 128, unless the
+// requests have fewer rows; TMEM holds one for D = 256.  The keys and values pass once,
+// 128 tokens (two pages) at a time, through a ring of shared-memory slots filled by TMA.
+// Per key tile S = Q K^T goes to TMEM, two threads per row turn 64 scores each into
+// weights (online softmax in base 2), write them over S in the input type, and O += P V
+// runs with P read from TMEM as the A operand.
 //
-// The steps are numbered so that the tensor core always has work while a softmax runs:
-// step i uses score buffer i mod 2 and is (tile i mod 2, keys i / 2) with two tiles, or
-// keys i with one; the issuing thread runs QK(0), QK(1), then PV(i), QK(i + 2), ...  The
-// matrix instructions of one thread execute in order, so QK(i + 2) may overwrite the
-// buffer that PV(i) reads its weights from.
+// Roles: a loader warp finds the items (the block's own, then blocks not started that it
+// takes over from the launch queue, longest requests first), describes them to the
+// others and loads keys and values; two warps copy the queries; one thread issues the
+// matrix instructions; 8 or 16 warps do the softmax and write the rows.  All of them run
+// ahead into the next item as far as their buffers let them, so that its start hides
+// behind the end of the one before.
+//
+// The tensor core is kept busy while a softmax runs by a second score buffer: of the
+// other row tile with two, of the next keys with one.  The issuing thread runs
+// QK(0), QK(1), then PV(i), QK(i + 2), ...  The matrix instructions of one thread execute
+// in order, so QK(i + 2) may overwrite the buffer that PV(i) reads its weights from.
+// PV(i) starts on half of each row's weights while the other half is being formed.
 //
 // The reference maximum of a row moves only when the running maximum has grown by more
 // than 2^8 (weights then stay below 256, exact in range for both types), so the pass that
@@ -20,7 +28,7 @@
 // rounding of a weight is of the size of the output's own.
 //
 // Few query rows leave the device empty, so the keys can be split into `splits` parts
-// per tile; parts leave (maximum, sum, O) in the workspace and a fold joins them in part
+// per item; parts leave (maximum, sum, O) in the workspace and a fold joins them in part
 // order.  Bound: the tensor cores (4 D operations per score) and, for D = 64, the
 // exponentials.
 #include "paged.cuh"
@@ -30,30 +38,46 @@ namespace tpk {
 constexpr float kNone = -__builtin_huge_valf();
 constexpr float kSlack = 8.f;  // log2 of the largest weight
 constexpr int kKeys = 128;     // tokens of a key tile
-constexpr int kTileRows = 128;
 constexpr uint32_t kTmemCols = 512;
 
-template <int D>
+template <int D, int kT>
 struct TileCfg {
-  static constexpr int kTiles = D == 256 ? 1 : 2;
+  static constexpr int kTiles = kT;
   static constexpr int kRows = kTiles * kTileRows;
   static constexpr int kSlotChannels = D < 128 ? D : 128;
   static constexpr int kSlotBytes = kKeys * kSlotChannels * 2;
   static constexpr int kParts = D / kSlotChannels;  // slots per key (or value) tile
-  static constexpr int kSlots = D == 64 ? 8 : 5;
+  static constexpr int kSlots = D == 64 ? 8 : D == 128 && kT == 1 ? 6 : 5;
   static constexpr int kQBytes = kTileRows * D * 2;  // one tile
-  static constexpr int kSmem = 1024 + kTiles * kQBytes + kSlots * kSlotBytes;
-  static constexpr int kThreads = kTiles * 128 + 64;
+  static constexpr int kSharedBytes = 3072;          // TileShared, to the next 1024
+  static constexpr int kSmem = kSharedBytes + kTiles * kQBytes + kSlots * kSlotBytes;
+  static constexpr int kSoftWarps = kTiles * 8;  // softmax: two threads per row
+  static constexpr int kMma = kSoftWarps, kLoad = kMma + 1, kQuery = kLoad + 1;
+  static constexpr int kThreads = (kQuery + 1) * 32;
+};
+
+// One tile group of one (request, KV head), or one part of its keys.
+struct Item {
+  int id;       // its block number; -1: no more
+  int first;    // its first query token
+  int tokens;   // and how many of them it has: `per_tile` fill a row tile
+  int h, len, b;
+  int page0, page_end, nk;  // key tiles [0, nk) begin at page page0
+  int last;     // 16-token groups of the last key tile that hold any token
 };
 
 struct TileShared {
-  uint64_t full[8], empty[8];
-  uint64_t s_full[2], p_full[2];  // scores written, weights written (by score buffer)
-  uint64_t pv_done[2], o_full[2]; // a product ended, the last one (by tile)
-  uint64_t q_full, tail, drain;
+  uint4 next;                      // the work taken over from a block not started
+  uint64_t full[8], empty[8];      // ring of key and value slots
+  uint64_t s_full[2];              // scores written (by score buffer)
+  uint64_t p_half[2], p_full[2];   // weights of half of each row's pieces written, of all
+  uint64_t pv_done, o_full[2], o_empty[2];  // a product ended (one tile), the last one; o read (by tile)
+  uint64_t q_full, q_empty, tail, drain, taken;
+  uint64_t item_full[2], item_empty[2];
+  Item item[2];
   uint32_t tmem;
-  int b, tile, clo, chi;
-  int scan[12];
+  int fine[2][8][2];               // [item parity][pair of warps][half]: waits met so far
+  float half[4 * kTileRows];       // what the two threads of a row tell each other
 };
 
 // ------------------------------------------------------------ tcgen05 wrappers
@@ -127,18 +151,56 @@ __device__ __forceinline__ void tc_loaded(float (&r)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
 }
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 32 bytes, aligned to 32.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// Shared-memory operand descriptor, 128-byte swizzle: 8-row groups of 1024 bytes are
-// `stride` apart; 64-channel chunks `leading` apart (read only where the channels are
-// not the reduced dimension).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uint32_t stride) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-         1ull << 46 | 2ull << 61;
+// Shared-memory operand descriptor, 128-byte swizzle: 8-row groups of 1024 bytes follow
+// each other; 64-channel chunks are `leading` apart (read only where the channels are not
+// the reduced dimension).  A later 16-byte piece is the descriptor plus one.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading) {
+  const uint32_t lo = (addr & 0x3ffff) >> 4 | (leading >> 4) << 16;
+  return (uint64_t)((1024 >> 4) | 1u << 14 | 2u << 29) << 32 | lo;
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// One lane of a converged warp, which the compiler then knows to be alone.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 // Instruction descriptor: float32 accumulator, both inputs of one type, M = 128.
 __device__ __forceinline__ constexpr uint32_t instruction(bool bf16, bool b_rows_reduced, int n) {
@@ -155,42 +217,119 @@ struct IsBf16<Bf16> {
   static constexpr bool value = true;
 };
 
-__device__ __forceinline__ int tiles_of(const PagedParams& p, int b, int rows) {
-  int first, count;
-  request_rows(p, b, first, count);
-  return (int)(((int64_t)count * p.G + rows - 1) / rows);
+// Takes over a block that has not started: its number arrives at S.next and completes the
+// barrier; or the news that none is left.
+__device__ __forceinline__ void take_block(uint4* dst, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(dst)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ int taken_block(const uint4* src) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(src))
+      : "memory");
+  return got ? (int)x : -1;
+}
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
-    tile_kernel(const __grid_constant__ PagedParams p, int splits) {
-  using C = TileCfg<D>;
-  constexpr int kSoft = C::kTiles * 128;  // softmax threads
-  extern __shared__ uint8_t raw[];
-  uint8_t* qs = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  uint8_t* slots = qs + C::kTiles * C::kQBytes;
-  __shared__ TileShared S;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int part = blockIdx.x % splits;
-  const int h = blockIdx.x / splits % p.H;
-  const int want = blockIdx.x / splits / p.H;  // tile group among all requests'
+// Finds the request of a tile group.  Lane i of the warp holds requests base + i and
+// base + 32 + i: their query rows, lengths, groups, and the groups before them.
+struct Requests {
+  int per_group;           // query tokens of a group
+  int base = -64, begin = 0, end = 0;  // groups [begin, end) are those of the 64 held
+  int first[2], count[2], len[2], groups[2], before[2];
 
-  // ---- which request holds it
-  const int each = (p.n_req + C::kThreads - 1) / C::kThreads;
-  const int b0 = min(tid * each, p.n_req), b1 = min(b0 + each, p.n_req);
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tiles_of(p, b, C::kRows);
-  int inc = mine;
+  __device__ __forceinline__ void load(const PagedParams& p, int lane) {
+    int sum = 0;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += up;
+    for (int x = 0; x < 2; ++x) {
+      const int b = base + 32 * x + lane;
+      int lo;
+      first[x] = count[x] = len[x] = 0;
+      if (b < p.n_req) {
+        request_rows(p, b, first[x], count[x]);
+        request_span(p, b, lo, len[x]);
+      }
+      groups[x] = (count[x] + per_group - 1) / per_group;
+      int inc = groups[x];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += up;
+      }
+      before[x] = begin + sum + inc - groups[x];
+      sum += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    end = begin + sum;
   }
-  if (lane == 31) S.scan[warp] = inc;
+  // Longest first: blocks start in index order, so the last ones to run are short.  (With
+  // more than 64 requests their lengths even out.)
+  __device__ __forceinline__ void sort(const PagedParams& p, int lane) {
+    int b2[2] = {0, 0};
+    for (int y = 0; y < p.n_req; ++y) {
+      const int n = __shfl_sync(0xffffffffu, y < 32 ? len[0] : len[1], y & 31);
+      const int g = __shfl_sync(0xffffffffu, y < 32 ? groups[0] : groups[1], y & 31);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (n > len[x] || (n == len[x] && y < 32 * x + lane)) b2[x] += g;
+    }
+    before[0] = b2[0];
+    before[1] = b2[1];
+  }
+  // Fills in the request of group `want`; false past the last one.
+  __device__ __forceinline__ bool find(const PagedParams& p, int lane, bool sorted, int want, Item& it) {
+    if (base < 0 || want < begin) {
+      base = begin = 0;
+      load(p, lane);
+      if (sorted) sort(p, lane);
+    }
+    while (want >= end) {
+      if (base + 64 >= p.n_req) return false;
+      base += 64;
+      begin = end;
+      load(p, lane);
+    }
+    const uint32_t m0 = __ballot_sync(0xffffffffu, want >= before[0] && want < before[0] + groups[0]);
+    const uint32_t m1 = __ballot_sync(0xffffffffu, want >= before[1] && want < before[1] + groups[1]);
+    const int src = (m0 ? __ffs(m0) : __ffs(m1)) - 1;
+    const bool second = m0 == 0;
+    it.b = base + (second ? 32 : 0) + src;
+    const int t = (want - __shfl_sync(0xffffffffu, second ? before[1] : before[0], src)) * per_group;
+    it.first = __shfl_sync(0xffffffffu, second ? first[1] : first[0], src) + t;
+    it.tokens = min(__shfl_sync(0xffffffffu, second ? count[1] : count[0], src) - t, per_group);
+    it.len = __shfl_sync(0xffffffffu, second ? len[1] : len[0], src);
+    return true;
+  }
+};
+
+template <typename T, int D, int kT>
+__global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
+    tile_kernel(const __grid_constant__ PagedParams p, int splits) {
+  using C = TileCfg<D, kT>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  static_assert(sizeof(TileShared) <= C::kSharedBytes, "TileShared");
+  TileShared& S = *reinterpret_cast<TileShared*>(raw);
+  uint8_t* qs = raw + C::kSharedBytes;
+  uint8_t* slots = qs + C::kTiles * C::kQBytes;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (smem_u32(raw) & 1023) {  // the swizzle counts on it
+    if (tid == 0) atomicOr(p.status, kStatusTimeout);
+    return;
+  }
   if (tid == 0) {
-    S.b = -1;
-    S.clo = 0x7fffffff;
-    S.chi = 0;
 #pragma unroll
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&S.full[i], 1);
@@ -199,329 +338,510 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i], 128);
-      mbar_init(&S.pv_done[i], 1);
+      mbar_init(&S.p_half[i], 256);
+      mbar_init(&S.p_full[i], 256);
       mbar_init(&S.o_full[i], 1);
+      mbar_init(&S.o_empty[i], 256);
+      mbar_init(&S.item_full[i], 1);
+      mbar_init(&S.item_empty[i], C::kSoftWarps + 2);
     }
-    mbar_init(&S.q_full, kSoft);
+    mbar_init(&S.pv_done, 1);
+    mbar_init(&S.q_full, 1);
+    mbar_init(&S.q_empty, 1);
     mbar_init(&S.tail, 1);
     mbar_init(&S.drain, 1);
+    mbar_init(&S.taken, 1);
     fence_mbar_init();
   }
-  __syncthreads();
-  int before = inc - mine;
-  for (int w = 0; w < warp; ++w) before += S.scan[w];
-  if (want >= before && want < before + mine) {
-    for (int b = b0; b < b1; ++b) {
-      const int n = tiles_of(p, b, C::kRows);
-      if (want < before + n) {
-        S.b = b;
-        S.tile = want - before;
-        break;
-      }
-      before += n;
-    }
+  if (tid == C::kLoad * 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.vmap) : "memory");
   }
-  __syncthreads();
-  const int b = S.b;
-  if (b < 0) return;  // past the last request's rows
-  int first, count, tok_lo, tok_hi;
-  request_rows(p, b, first, count);
-  request_span(p, b, tok_lo, tok_hi);
-  const int64_t row0 = (int64_t)S.tile * C::kRows;
-  const int64_t rows = (int64_t)count * p.G - row0;  // of this block, if fewer than C::kRows
-  const int nt = C::kTiles == 2 && rows > kTileRows ? 2 : 1;
-
-  // ---- what each row sees, and what the block has to pass over
-  int see_lo = 0, see_hi = 0, token = 0, head = 0;
-  bool live = false;
-  if (tid < kSoft) {
-    live = tid < rows;
-    if (live) {
-      const int64_t i = row0 + tid;
-      const int t = (int)(i / p.G);
-      token = first + t;
-      head = h * p.G + (int)(i - (int64_t)t * p.G);
-      see_hi = tok_hi;
-      if (p.range) {
-        see_lo = max(0, p.range[2 * (int64_t)token]);
-        see_hi = min(tok_hi, p.range[2 * (int64_t)token + 1]);
-        if (see_hi > see_lo) {
-          atomicMin(&S.clo, see_lo);
-          atomicMax(&S.chi, see_hi);
-        } else {
-          see_lo = see_hi = 0;
-        }
-      }
-    }
-  }
-  if (warp == kSoft / 32) tmem_alloc(&S.tmem);
+  if (warp == C::kMma) tmem_alloc(&S.tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const int clo = p.range ? S.clo : 0, chi = p.range ? S.chi : tok_hi;
-  int page0 = chi > clo ? clo >> 6 : 0;
-  const int page_end = (chi + 63) >> 6;
-  int nk = chi > clo ? (page_end - page0 + 1) >> 1 : 0;  // key tiles
-  {
-    const int k0 = (int)((int64_t)nk * part / splits), k1 = (int)((int64_t)nk * (part + 1) / splits);
-    page0 += 2 * k0;
-    nk = k1 - k0;
-  }
-  const int steps = nt * nk;
   const uint32_t tmem = S.tmem;
-  const int32_t* table = p.table + (int64_t)b * p.max_pages;
-  // the ring holds the key and value tiles in the order the tensor core takes them
-  auto k_item = [&](int j) { return C::kParts * (nt == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1)); };
-  auto v_item = [&](int j) { return C::kParts * (nt == 2 ? 2 * j + 1 : (j < nk - 1 ? 2 * j + 2 : 2 * j + 1)); };
+  const int G = p.G, per_tile = kTileRows / G;  // query tokens of a row tile (rows past them are not used)
+  // the next item for a whole warp; false if it did not come in time
+  auto next_item = [&](int k, Item& it) {
+    const bool ok =
+        __all_sync(0xffffffffu, mbar_wait(&S.item_full[k & 1], k >> 1 & 1, p.status, p.wait_ns)) != 0;
+    if (ok) it = S.item[k & 1];
+    __syncwarp();
+    if (ok && lane == 0) mbar_arrive(&S.item_empty[k & 1]);
+    return ok;
+  };
 
-  if (warp == kSoft / 32) {
+  if (warp == C::kMma) {
     // ------------------------------------------------------------ matrix issue
-    if (lane == 0 && steps > 0) {
+    // One elected lane runs all of it: nothing to keep the warp together for.  The key
+    // and value tiles lie in the ring in the order they are taken here:
+    // K0 V0 K1 V1 ... with two row tiles, K0 K1 V0 K2 V1 ... with one.
+    if (elect_one()) {
       constexpr bool bf16 = IsBf16<T>::value;
       constexpr uint32_t id_qk = instruction(bf16, false, kKeys);
       constexpr uint32_t id_pv = instruction(bf16, true, C::kSlotChannels);
-      bool ok = mbar_wait(&S.q_full, 0, p.status, p.wait_ns);
-      tc_fence_after();
-      auto wait_item = [&](int item) {
-        for (int c = 0; c < C::kParts && ok; ++c)
-          ok = mbar_wait(&S.full[(item + c) % C::kSlots], ((item + c) / C::kSlots) & 1, p.status, p.wait_ns);
-        tc_fence_after();
-      };
-      auto free_item = [&](int item) {
-        for (int c = 0; c < C::kParts; ++c) tc_commit(&S.empty[(item + c) % C::kSlots]);
-      };
-      auto qk = [&](int i) {
-        const int tile = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i, item = k_item(j);
-        if (tile == 0) wait_item(item);
-        if (!ok) return;
-        const uint32_t q = smem_u32(qs) + tile * C::kQBytes;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const int part_of = c * 64 / C::kSlotChannels;
-          const uint32_t k = smem_u32(slots) + (item + part_of) % C::kSlots * C::kSlotBytes +
-                             (c * 64 % C::kSlotChannels) / 64 * (kKeys * 128);
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            tc_mma_ss(tmem + (i & 1) * kKeys, operand(q + c * (kTileRows * 128) + x * 32, 16, 1024),
-                      operand(k + x * 32, 16, 1024), id_qk, c > 0 || x > 0);
-        }
-        tc_commit(&S.s_full[i & 1]);
-        if (nt == 1 || tile == 1) free_item(item);
-      };
-      qk(0);
-      if (steps > 1) qk(1);
-      for (int i = 0; i < steps && ok; ++i) {
-        const int tile = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i, item = v_item(j);
-        ok = mbar_wait(&S.p_full[i & 1], (i >> 1) & 1, p.status, p.wait_ns);
-        if (ok && tile == 0) wait_item(item);
-        if (!ok) break;
-        tc_fence_after();
+      const uint32_t empty = smem_u32(S.empty), s_full = smem_u32(S.s_full), o_full = smem_u32(S.o_full);
+      const uint32_t q_empty = smem_u32(&S.q_empty), pv_done = smem_u32(&S.pv_done);
+      const uint64_t q_op = operand(smem_u32(qs), 16);
+      const uint64_t k_op = operand(smem_u32(slots), 16), v_op = operand(smem_u32(slots), kKeys * 128);
+      constexpr uint64_t kSlotStep = C::kSlotBytes >> 4;
+      int next = 0, phase = 0;        // ring position of the next tile
+      int items = 0;                  // with work, so far
+      int used[2] = {0, 0};           // items of each row tile so far
+      int step[2] = {0, 0};           // steps of each score buffer so far
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) { ok = ok && mbar_wait(bar, parity & 1, p.status, p.wait_ns); };
+      // the first slot of the next tile, once it has landed
+      auto take = [&] {
+        const int at = next;
 #pragma unroll
         for (int c = 0; c < C::kParts; ++c) {
-          const uint32_t v = smem_u32(slots) + (item + c) % C::kSlots * C::kSlotBytes;
-#pragma unroll
-          for (int x = 0; x < kKeys / 16; ++x)
-            tc_mma_ts(tmem + 256 + tile * 128 + c * 128, tmem + (i & 1) * kKeys + x * 8,
-                      operand(v + x * 2048, kKeys * 128, 1024), id_pv, j > 0 || x > 0);
+          wait(&S.full[next], phase);
+          if (++next == C::kSlots) {
+            next = 0;
+            phase ^= 1;
+          }
         }
-        tc_commit(&S.pv_done[tile]);
-        if (j == nk - 1) tc_commit(&S.o_full[tile]);
-        if (nt == 1 || tile == 1) free_item(item);
-        if (i + 2 < steps) qk(i + 2);
+        return at;
+      };
+      auto nth = [&](int at, int c) { return at + c < C::kSlots ? at + c : at + c - C::kSlots; };
+      // scores of row tile x with the keys at `at`, into score buffer `buf`
+      auto qk = [&](int x, int buf, int at, bool last) {
+        const uint64_t q = q_op + x * (C::kQBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < C::kParts; ++c) {
+          const uint64_t k = k_op + nth(at, c) * kSlotStep;
+#pragma unroll
+          for (int i = 0; i < C::kSlotChannels / 16; ++i)  // 64-channel chunks of 16 KB, 32 bytes a step
+            tc_mma_ss(tmem + buf * kKeys, q + (c * (C::kSlotChannels / 64) + i / 4) * (kTileRows * 8) + i % 4 * 2,
+                      k + i / 4 * (kKeys * 8) + i % 4 * 2, id_qk, c > 0 || i > 0);
+          if (last) tc_commit(empty + 8 * nth(at, c));
+        }
+        tc_commit(s_full + 8 * buf);
+      };
+      // o of row tile x += weights in buffer `buf` times the values at `at`: the first
+      // halves of the rows' pieces as soon as they are there; `last`: no other row tile
+      // needs the values; `groups`: 16-token groups that hold any token
+      auto pv = [&](int x, int buf, int at, bool more, bool last, int groups) {
+        if (!more) {  // o of the item before has been read
+          if (used[x] > 0) wait(&S.o_empty[x], used[x] - 1);
+          ++used[x];
+        }
+        const int n = step[buf]++;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          wait(s == 0 ? &S.p_half[buf] : &S.p_full[buf], n);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < C::kParts; ++c) {
+            const uint64_t v = v_op + nth(at, c) * kSlotStep;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int i = (y >> 1) * 4 + 2 * s + (y & 1);  // 16 tokens: two 8-row groups
+              if (i < groups)
+                tc_mma_ts(tmem + 256 + x * 128 + c * 128, tmem + buf * kKeys + i / 4 * (kKeys / 2) + i % 4 * 8,
+                          v + i * 128, id_pv, more || s > 0 || y > 0);
+            }
+            if (last && s == 1) tc_commit(empty + 8 * nth(at, c));
+          }
+        }
+      };
+      for (int k = 0; ok; ++k) {
+        wait(&S.item_full[k & 1], k >> 1);
+        if (!ok) break;
+        const int id = S.item[k & 1].id, nk = S.item[k & 1].nk, tail = S.item[k & 1].last;
+        const bool two = C::kTiles == 2 && S.item[k & 1].tokens > per_tile;
+        mbar_arrive(&S.item_empty[k & 1]);
+        if (id < 0) break;
+        if (nk == 0) continue;
+        wait(&S.q_full, items++);
+        tc_fence_after();
+        int ka = take();
+        if (!ok) break;
+        if (C::kTiles == 2) {
+          qk(0, 0, ka, !two);
+          if (two) qk(1, 1, ka, true);
+          if (nk == 1) tc_commit(q_empty);
+          for (int j = 0; j < nk && ok; ++j) {
+            const int va = take();
+            const bool more = j + 1 < nk;
+            if (more) ka = take();
+            if (!ok) break;
+            pv(0, 0, va, j > 0, !two, more ? 8 : tail);
+            if (!ok) break;
+            if (more) qk(0, 0, ka, !two); else tc_commit(o_full);
+            if (two) {
+              pv(1, 1, va, j > 0, true, more ? 8 : tail);
+              if (!ok) break;
+              if (more) qk(1, 1, ka, true); else tc_commit(o_full + 8);
+            }
+            if (j + 2 == nk) tc_commit(q_empty);
+          }
+        } else {
+          const int b0 = (step[0] + step[1]) & 1;  // score buffer of the first step
+          qk(0, b0, ka, true);
+          if (nk > 1) {
+            ka = take();
+            if (!ok) break;
+            qk(0, b0 ^ 1, ka, true);
+          }
+          if (nk <= 2) tc_commit(q_empty);
+          for (int j = 0; j < nk && ok; ++j) {
+            const int va = take();
+            const bool more = j + 2 < nk;
+            if (more) ka = take();
+            if (!ok) break;
+            pv(0, b0 ^ (j & 1), va, j > 0, true, j + 1 < nk ? 8 : tail);
+            if (!ok) break;
+            tc_commit(pv_done);
+            if (j + 1 == nk) tc_commit(o_full);
+            if (more) {
+              qk(0, b0 ^ (j & 1), ka, true);
+              if (j + 3 == nk) tc_commit(q_empty);
+            }
+          }
+        }
       }
-      tc_commit(&S.drain);
+      tc_commit(smem_u32(&S.drain));
       mbar_wait(&S.drain, 0, p.status, p.wait_ns);
     }
     __syncwarp();
-  } else if (warp == kSoft / 32 + 1) {
-    // ------------------------------------------------------------------ loader
-    int item = 0;
+  } else if (warp == C::kLoad) {
+    // -------------------------------------------- items, and their keys and values
+    const bool sorted = splits == 1 && p.n_req <= 64;
+    Requests requests;
+    requests.per_group = C::kTiles * per_tile;
+    int item = 0, tails = 0;
+    int st = 0, lap = 0;  // the ring slot to fill, times round the ring
     bool ok = true;
-    int32_t near = 0, far = 0;  // table entries of this window of 16 key tiles, and of the one before
-    int window = -1;
-    int tails = 0;
-    // one key (or value) tile: two pages, kParts slots
-    auto load = [&](int j, bool values) {
-      if (j / 16 > window) {
-        window = j / 16;
-        far = near;
-        const int pg = page0 + 32 * window + lane;
-        near = pg < page_end ? table[pg] : -1;
-      }
-      const int32_t from = j / 16 == window ? near : far;
-      int64_t slot[2];
-      bool there[2];
-      int n = 0;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        slot[x] = __shfl_sync(0xffffffffu, from, (2 * j + x) & 31);
-        there[x] = slot[x] >= 0 && slot[x] < p.kv_slots;
-        if (!there[x] && page0 + 2 * j + x < page_end && lane == 0) atomicOr(p.status, kStatusBadSlot);
-        n += there[x];
-      }
-      const int k0 = (page0 + 2 * j) * kPageTokens;
-      const bool clear = values && (n < 2 || k0 + kKeys > tok_hi);  // rows that must not be read as they are
-      for (int c = 0; c < C::kParts && ok; ++c, ++item) {
-        const int st = item % C::kSlots;
-        if (item >= C::kSlots)
-          ok = __all_sync(0xffffffffu, mbar_wait(&S.empty[st], (item / C::kSlots - 1) & 1, p.status, p.wait_ns));
-        if (!ok) break;
-        uint8_t* dst = slots + st * C::kSlotBytes;
-        uint64_t* bar = clear ? &S.tail : &S.full[st];
+    auto wait = [&](uint64_t* bar, int parity) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, p.status, p.wait_ns)) != 0;
+    };
+    int id = blockIdx.x;
+    int asked = 0;
+    for (int k = 0; ok; ++asked) {
+      // Asked for near the end of an item's loads: asked earlier, a block would commit
+      // itself to an item that another is free for first.
+      bool open = true;
+      auto ask = [&] {
         if (lane == 0) {
-          if (n > 0) mbar_arrive_expect_tx(bar, n * (C::kSlotBytes / 2));
-          else mbar_arrive(bar);
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (there[x])
-#pragma unroll
-              for (int ch = 0; ch < C::kSlotChannels; ch += 64)
-                tma_load_2d(dst + ch / 64 * (kKeys * 128) + x * (kPageTokens * 128), values ? &p.vmap : &p.kmap,
-                            c * C::kSlotChannels + ch, (int)((slot[x] * p.H + h) * kPageTokens), bar);
+          mbar_arrive_expect_tx(&S.taken, 16);
+          take_block(&S.next, &S.taken);
+        }
+        open = false;
+      };
+      // ---- what the item is
+      Item it;
+      const int part = id % splits;
+      it.id = id;
+      it.h = id / splits % p.H;
+      if (requests.find(p, lane, sorted, id / splits / p.H, it)) {
+        int clo = 0, chi = it.len;
+        if (p.range) {  // what any of its rows sees
+          clo = 0x7fffffff;
+          chi = 0;
+          for (int t = it.first + lane; t < it.first + it.tokens; t += 32) {
+            const int a = max(0, p.range[2 * (int64_t)t]), e = min(it.len, p.range[2 * (int64_t)t + 1]);
+            if (e > a) {
+              clo = min(clo, a);
+              chi = max(chi, e);
+            }
+          }
+          clo = __reduce_min_sync(0xffffffffu, clo);
+          chi = __reduce_max_sync(0xffffffffu, chi);
+        }
+        it.page0 = chi > clo ? clo >> 6 : 0;
+        it.page_end = (chi + 63) >> 6;
+        const int nk = chi > clo ? (it.page_end - it.page0 + 1) >> 1 : 0;
+        const int k0 = (int)((unsigned)nk * (unsigned)part / (unsigned)splits);  // splits <= kTileBlocks, nk < 2^24
+        const int k1 = (int)((unsigned)nk * (unsigned)(part + 1) / (unsigned)splits);
+        it.page0 += 2 * k0;
+        it.nk = k1 - k0;
+        it.last = min(8, (min(it.len, it.page_end * kPageTokens) - (it.page0 + 2 * (it.nk - 1)) * kPageTokens + 15) >> 4);
+        if (k >= 2) wait(&S.item_empty[k & 1], (k >> 1) - 1);
+        if (ok && lane == 0) {
+          S.item[k & 1] = it;
+          mbar_arrive(&S.item_full[k & 1]);
         }
         __syncwarp();
-        if (clear) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&S.tail, tails & 1, p.status, p.wait_ns));
-          ++tails;
-          for (int i = lane; i < kKeys * (C::kSlotChannels / 8); i += 32) {
-            const int r = i / (C::kSlotChannels / 8), piece = i % (C::kSlotChannels / 8);
-            if (!there[r >> 6] || k0 + r >= tok_hi)
-              *reinterpret_cast<uint4*>(dst + (piece >> 3) * (kKeys * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) =
-                  make_uint4(0, 0, 0, 0);
+        ++k;
+        const int page0 = it.page0, page_end = it.page_end, nk_ = it.nk, h = it.h, tok_hi = it.len;
+        const int32_t* table = p.table + (int64_t)it.b * p.max_pages;
+        int32_t near = 0, far = 0;  // table entries of this window of 16 key tiles, and of the one before
+        int window = -1;
+        const int n_slots = (int)p.kv_slots, H = p.H;
+        // one key (or value) tile: two pages, kParts slots
+        auto load = [&](int j, bool values) {
+          if (j >> 4 > window) {
+            window = j >> 4;
+            far = near;
+            const int pg = page0 + 32 * window + lane;
+            near = pg < page_end ? table[pg] : -1;
           }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.full[st]);
+          const int32_t from = j >> 4 == window ? near : far;
+          const int slot0 = __shfl_sync(0xffffffffu, from, 2 * j & 31), slot1 = __shfl_sync(0xffffffffu, from, (2 * j & 31) + 1);
+          const bool there0 = (unsigned)slot0 < (unsigned)n_slots, there1 = (unsigned)slot1 < (unsigned)n_slots;
+          const int n = there0 + there1;
+          const bool second = page0 + 2 * j + 1 < page_end;  // the tile has a second page
+          const int tok0 = (page0 + 2 * j) * kPageTokens;
+          const bool bad = !there0 || (!there1 && second);
+          if (bad && lane == 0) atomicOr(p.status, kStatusBadSlot);
+          // values whose weight is 0 must not be NaN: rows past the last token in its
+          // 16-token group (later groups are not multiplied), and pages not there
+          const bool clear = values && (bad || (tok0 + kKeys > tok_hi && (tok_hi & 15)));
+          const int y0 = (slot0 * H + h) * kPageTokens, y1 = (slot1 * H + h) * kPageTokens;
+#pragma unroll
+          for (int c = 0; c < C::kParts; ++c) {
+            if (lap > 0) wait(&S.empty[st], lap - 1);
+            if (!ok) break;
+            uint8_t* dst = slots + st * C::kSlotBytes;
+            uint64_t* bar = clear ? &S.tail : &S.full[st];
+            const CUtensorMap* map = values ? &p.vmap : &p.kmap;
+            if (elect_one()) {
+              if (n > 0) mbar_arrive_expect_tx(bar, n * (C::kSlotBytes / 2));
+              else mbar_arrive(bar);
+#pragma unroll
+              for (int ch = 0; ch < C::kSlotChannels; ch += 64) {
+                uint8_t* to = dst + ch / 64 * (kKeys * 128);
+                if (there0) tma_load_2d(to, map, c * C::kSlotChannels + ch, y0, bar);
+                if (there1) tma_load_2d(to + kPageTokens * 128, map, c * C::kSlotChannels + ch, y1, bar);
+              }
+            }
+            __syncwarp();
+            if (clear) {
+              wait(&S.tail, tails++);
+              constexpr int kPieces = C::kSlotChannels / 8;
+              const int piece = lane % kPieces;
+              const int end = min(kKeys, max(0, tok_hi - tok0));  // rows that hold tokens
+              const int last = bad ? kKeys : (end + 15) & ~15;
+              for (int r = bad ? lane / kPieces : end + lane / kPieces; r < last; r += 32 / kPieces)
+                if (r >= end || !(r < kPageTokens ? there0 : there1))
+                  *reinterpret_cast<uint4*>(dst + (piece >> 3) * (kKeys * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) =
+                      make_uint4(0, 0, 0, 0);
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&S.full[st]);
+            }
+            ++item;
+            if (++st == C::kSlots) {
+              st = 0;
+              ++lap;
+            }
+          }
+        };
+        for (int j = 0; j < nk_ && ok; ++j) {
+          if (j + 4 == nk_) ask();
+          if (C::kTiles == 2) {
+            load(j, false);
+          } else {
+            if (j == 0) load(0, false);
+            if (j + 1 < nk_) load(j + 1, false);
+          }
+          load(j, true);
         }
       }
-    };
-    if (nt == 2) {
-      for (int j = 0; j < nk && ok; ++j) {
-        load(j, false);
-        load(j, true);
-      }
-    } else {
-      for (int j = 0; j < nk && ok; ++j) {
-        if (j == 0) load(0, false);
-        if (j + 1 < nk) load(j + 1, false);
-        load(j, true);
+      if (open) ask();
+      wait(&S.taken, asked);
+      if (!ok) break;
+      id = taken_block(&S.next);
+      fence_async_smem();  // read before the next answer is written
+      __syncwarp();
+      if (id < 0) {
+        if (k >= 2) wait(&S.item_empty[k & 1], (k >> 1) - 1);
+        if (ok && lane == 0) {
+          S.item[k & 1].id = -1;
+          mbar_arrive(&S.item_full[k & 1]);
+        }
+        break;
       }
     }
-    if (!ok)  // let the copies in flight land before the block ends
+    if (!ok) {  // let what is in flight land before the block ends
+      mbar_wait(&S.taken, asked & 1, p.status, p.wait_ns);
       for (int i = max(0, item - C::kSlots); i < item; ++i)
         mbar_wait(&S.full[i % C::kSlots], (i / C::kSlots) & 1, p.status, p.wait_ns);
+    }
+    __syncwarp();
+  } else if (warp == C::kQuery) {
+    // ----------------------------------------------------------------- queries
+    int items = 0;
+    Item it;
+    for (int k = 0; next_item(k, it) && it.id >= 0; ++k) {
+      if (it.nk == 0) continue;
+      if (items > 0 &&
+          !__all_sync(0xffffffffu, mbar_wait(&S.q_empty, (items - 1) & 1, p.status, p.wait_ns)))
+        break;
+      ++items;
+      // rows (token, head) of each tile; tokens past the request's are someone else's or,
+      // past the last, zero: no row of theirs is written
+      const int tiles = it.tokens > per_tile ? 2 : 1;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&S.q_full, tiles * per_tile * G * D * 2);
+        for (int x = 0; x < tiles; ++x)
+#pragma unroll
+          for (int c = 0; c < D; c += 64)
+            tma_load_3d(qs + x * C::kQBytes + c / 64 * (kTileRows * 128), &p.qmap, c, it.h * G,
+                        it.first + x * per_tile, &S.q_full);
+      }
+      __syncwarp();
+    }
+    if (items > 0) mbar_wait(&S.q_full, (items - 1) & 1, p.status, p.wait_ns);  // none in flight at the end
   } else {
     // ----------------------------------------------------------------- softmax
-    const int tile = warp >> 2;
-    const float qscale = fabsf(p.qscale);  // its sign goes into q
-    if (steps > 0) {
-      const uint32_t flip = p.qscale < 0.f ? 0x80008000u : 0u;
-      for (int i = tid; i < nt * kTileRows * (D / 8); i += kSoft) {
-        const int r = i / (D / 8), piece = i % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
-          const int64_t x = row0 + r;
-          const int t = (int)(x / p.G);
-          v = *reinterpret_cast<const uint4*>(p.q + (int64_t)(first + t) * p.q_stride +
-                                              (int64_t)(h * p.G + (int)(x - (int64_t)t * p.G)) * D + piece * 8);
-          v.x ^= flip;
-          v.y ^= flip;
-          v.z ^= flip;
-          v.w ^= flip;
-        }
-        const int rr = r & (kTileRows - 1);
-        *reinterpret_cast<uint4*>(qs + (r >> 7) * C::kQBytes + (piece >> 3) * (kTileRows * 128) + rr * 128 +
-                                  (((piece & 7) ^ (rr & 7)) << 4)) = v;
-      }
-      fence_async_smem();
-      mbar_arrive(&S.q_full);
-    }
-    float m = kNone, l = 0.f;
-    bool ok = true;
-    uint32_t pages_ok = 0;
+    // Warp w has rows 32 (w mod 4) .. of tile w / 8 (a warp reaches the TMEM rows of its
+    // number mod 4 only) and keys 64 (w / 4 mod 2) .. of each key tile.
+    const int tile = warp >> 3, half = warp >> 2 & 1, row = (warp & 3) * 32 + lane, hrow = tile * kTileRows + row;
+    const float qscale = fabsf(p.qscale);  // its sign goes to the scores
+    constexpr int kMine = kKeys / 2;       // keys of this thread's half
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's TMEM rows
-    const uint32_t o_addr = tmem + 256 + tile * 128 + lanes;
-    const int n_mine = tile < nt ? nk : 0;
-    for (int n = 0; n < n_mine && ok; ++n) {
-      const int i = nt == 2 ? 2 * n + tile : n;
-      if ((n & 15) == 0) {
-        const int pg = page0 + 2 * n + lane;
-        const int32_t e = pg < page_end ? table[pg] : -1;
-        pages_ok = __ballot_sync(0xffffffffu, e >= 0 && e < p.kv_slots);
-      }
-      const int k0 = (page0 + 2 * n) * kPageTokens;
-      const uint32_t halves = pages_ok >> (2 * (n & 15)) & 3;
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[i & 1], (i >> 1) & 1, p.status, p.wait_ns));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t s_addr = tmem + (i & 1) * kKeys + lanes;
-      float x[kKeys];
-#pragma unroll
-      for (int c = 0; c < kKeys; c += 32) tc_ld32(x + c, s_addr + c);
-      tc_wait_ld();
-      tc_loaded(x);
-      const int lo = see_lo - k0, hi = see_hi - k0;
-      if (!__all_sync(0xffffffffu, lo <= 0 && hi >= kKeys && halves == 3)) {
-#pragma unroll
-        for (int c = 0; c < kKeys; ++c)
-          if (c < lo || c >= hi || !(halves >> (c >> 6) & 1)) x[c] = kNone;
-      }
-      float top[4] = {kNone, kNone, kNone, kNone};
-#pragma unroll
-      for (int c = 0; c < kKeys; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
-      const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * qscale;
-      const bool grow = mt > m + kSlack || (m == kNone && mt > kNone);
-      if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? ex2(m - mt) : 1.f;
-        l *= f;
-        if (grow) m = mt;
-        if (n > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&S.pv_done[tile], (n - 1) & 1, p.status, p.wait_ns));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tc_ld32(o, o_addr + c);
-            tc_wait_ld();
-            tc_loaded(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tc_st32(o_addr + c, o);
-          }
-          tc_wait_st();
-        }
-      }
-      const float ref = m == kNone ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < kKeys; c += 32) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float a = ex2(fmaf(x[c + e], qscale, -ref)), d = ex2(fmaf(x[c + e + 1], qscale, -ref));
-          sum[e & 2] += a;
-          sum[(e & 2) + 1] += d;
-          w[e >> 1] = T::pack(a, d);
-        }
-        tc_st16(s_addr + (c >> 1), w);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(&S.p_full[i & 1]);
-    }
-    // ---- the rows' results
-    if (n_mine > 0 && ok) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[tile], 0, p.status, p.wait_ns));
-      tc_fence_after();
-    }
-    if (ok && tile < nt) {
-      const int HQ = p.H * p.G;
-      const int64_t at = ((int64_t)blockIdx.x * C::kRows + tid);  // this part's row in the workspace
-      const float inv = splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+    const uint32_t o_addr = tmem + 256 + tile * 128 + half * (D / 2) + lanes;
+    const int pair = tile * 4 + (warp & 3);  // the two warps of the same rows
+    const int HQ = p.H * G;
+    const int t_row = row / G, g_row = row - t_row * G;  // token and head of this row in its tile
+    const bool neg = p.qscale < 0.f;
+    const bool sectors = ((reinterpret_cast<uintptr_t>(p.o) | (uintptr_t)p.o_stride * 2) & 31) == 0;
+    int step = 0, items = 0;  // steps and items of this row tile so far
+    bool ok = true;
+    // The exchange of a step.  With one row tile the next step may begin while the other
+    // thread still reads: two places in turn.  With two it begins with scores that wait
+    // for both threads' weights.
+    auto told = [&](int s, int which) -> float& {
+      return S.half[C::kTiles == 2 ? which * (2 * kTileRows) + hrow
+                                   : (s & 1) * (2 * kTileRows) + which * kTileRows + row];
+    };
+    for (int k = 0;; ++k) {
+      Item it;
+      it.id = -1;
+      ok = ok && next_item(k, it);
+      // a wait that ran out ends both warps of a pair at the same place
+      if (lane == 0) S.fine[k & 1][pair][half] = ok;
+      named_barrier(1 + pair, 64);
+      if (!ok || !S.fine[k & 1][pair][half ^ 1] || it.id < 0) break;
+      if (tile * per_tile >= it.tokens) continue;  // no rows in this tile
+      const bool live = t_row < per_tile && tile * per_tile + t_row < it.tokens;
+      const int token = it.first + tile * per_tile + t_row, head = it.h * G + g_row;
+      int see_lo = 0, see_hi = 0x7fffffff;  // a row that is not written need not be masked
       if (live) {
+        see_hi = it.len;
+        if (p.range) {
+          see_lo = max(0, p.range[2 * (int64_t)token]);
+          see_hi = min(see_hi, p.range[2 * (int64_t)token + 1]);
+        }
+      }
+      const int32_t* table = p.table + (int64_t)it.b * p.max_pages;
+      const int nk = it.nk;
+      float m = kNone, l = 0.f;
+      uint32_t pages_ok = 0;
+      for (int n = 0; n < nk; ++n, ++step) {
+        const int buf = C::kTiles == 2 ? tile : step & 1, parity = (C::kTiles == 2 ? step : step >> 1) & 1;
+        if ((n & 15) == 0) {
+          const int pg = it.page0 + 2 * n + lane;
+          const int32_t e = pg < it.page_end ? table[pg] : -1;
+          pages_ok = __ballot_sync(0xffffffffu, e >= 0 && e < p.kv_slots);
+        }
+        const int k0 = (it.page0 + 2 * n + half) * kPageTokens;
+        const bool there = pages_ok >> (2 * (n & 15) + half) & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[buf], parity, p.status, p.wait_ns)) != 0;
+        tc_fence_after();
+        const uint32_t s_addr = tmem + buf * kKeys + half * kMine + lanes;
+        const int lo = see_lo - k0, hi = see_hi - k0;
+        const bool plain = !neg && __all_sync(0xffffffffu, lo <= 0 && hi >= kMine && there);
+        // scores [c, c + 32) of this half; they are read twice, which takes half the
+        // registers and next to no time.  (The loops over them are not unrolled: the
+        // kernel's roles share an instruction cache.)
+        auto scores = [&](float(&x)[32], int c) {
+          tc_ld32(x, s_addr + c);
+          tc_wait_ld();
+          tc_loaded(x);
+          if (!plain) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              x[e] = neg ? -x[e] : x[e];
+              if (c + e < lo || c + e >= hi || !there) x[e] = kNone;
+            }
+          }
+        };
+        float top[4] = {kNone, kNone, kNone, kNone};
+#pragma unroll 1
+        for (int c = 0; c < kMine; c += 32) {
+          float x[32];
+          scores(x, c);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) top[e >> 1 & 3] = fmaxf(fmaxf(top[e >> 1 & 3], x[e]), x[e + 1]);
+        }
+        // the row's other half; both then take the same decisions (a wait that ran out
+        // is told as NaN, which no maximum is)
+        const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        told(step, half) = ok ? mine : __int_as_float(0x7fffffff);
+        named_barrier(1 + pair, 64);
+        const float other = told(step, half ^ 1);
+        ok = ok && !__any_sync(0xffffffffu, other != other);
+        if (!ok) break;
+        const float mt = fmaxf(mine, other) * qscale;
+        const bool grow = mt > m + kSlack || (m == kNone && mt > kNone);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2(m - mt) : 1.f;
+          l *= f;
+          if (grow) m = mt;
+          if (n > 0) {
+            // the product before these weights has ended: with two tiles it came before
+            // the scores just read
+            bool done = true;
+            if (C::kTiles == 1) done = __all_sync(0xffffffffu, mbar_wait(&S.pv_done, (step - 1) & 1, p.status, p.wait_ns)) != 0;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 2 && done; c += 32) {
+              float o[32];
+              tc_ld32(o, o_addr + c);
+              tc_wait_ld();
+              tc_loaded(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tc_st32(o_addr + c, o);
+            }
+            tc_wait_st();
+          }
+        }
+        const float ref = m == kNone ? 0.f : m;
+        const uint64_t q2 = ::tpk::pair(qscale, qscale), ref2 = ::tpk::pair(-ref, -ref);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+        for (int c = 0; c < kMine; c += 32) {
+          float x[32];
+          uint32_t w[16];
+          scores(x, c);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float2 v = unpair(fma2(::tpk::pair(x[e], x[e + 1]), q2, ref2));
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], ::tpk::pair(v.x, v.y));
+            w[e >> 1] = T::pack(v.x, v.y);
+          }
+          tc_st16(s_addr + (c >> 1), w);  // over scores of this half already used
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive(c == 0 ? &S.p_half[buf] : &S.p_full[buf]);
+        }
+        const float2 both = unpair(add2(sum[0], sum[1]));
+        l += both.x + both.y;
+      }
+      if (!ok) continue;
+      // ---- the rows' results
+      if (nk > 0) {
+        named_barrier(1 + pair, 64);
+        told(0, half) = l;
+        named_barrier(1 + pair, 64);
+        l += told(0, half ^ 1);
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[tile], items++ & 1, p.status, p.wait_ns)) != 0;
+        tc_fence_after();
+      }
+      const int64_t at = (int64_t)it.id * C::kRows + hrow;  // this part's row in the workspace
+      const float inv = splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const bool write = live && ok && !(splits > 1 && m == kNone);  // the fold does not read an empty part
+      if (live && ok && half == 0) {
         if (splits > 1) {
           p.part_ml[2 * at] = m;
           p.part_ml[2 * at + 1] = l;
@@ -530,63 +850,71 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
         }
       }
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < D / 2; c += 32) {
         float o[32];
         __syncwarp();
-        if (n_mine > 0) {
+        if (nk > 0) {
           tc_ld32(o, o_addr + c);
           tc_wait_ld();
           tc_loaded(o);
+          if (c + 32 == D / 2) {
+            tc_fence_before();
+            mbar_arrive(&S.o_empty[tile]);
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if (!live) continue;
-        if (splits > 1) {
-          if (m == kNone) continue;  // the fold does not read an empty part
-          float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + c);
+        const int ch = half * (D / 2) + c;
+        if (write && splits > 1) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + ch);
 #pragma unroll
           for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (int64_t)token * p.o_stride +
-                                                (int64_t)head * D + c);
+        } else if (write) {
+          uint16_t* dst = static_cast<uint16_t*>(p.o) + (int64_t)token * p.o_stride + (int64_t)head * D + ch;
+          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(T::pack(o[8 * e] * inv, o[8 * e + 1] * inv), T::pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                T::pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                T::pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          for (int e = 0; e < 16; ++e) w[e] = T::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+          if (sectors) {  // whole 32-byte sectors
+            store32(dst, w);
+            store32(dst + 16, w + 8);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<uint4*>(dst)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          }
         }
       }
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kSoft / 32) {
+  if (warp == C::kMma) {
     tc_fence_after();
     tmem_dealloc(tmem);
   }
 }
 
 // Joins the parts of a split launch, one warp per row of a tile group.
-template <typename T, int D>
+template <typename T, int D, int kT>
 __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ PagedParams p, int splits) {
-  using C = TileCfg<D>;
-  const int lane = threadIdx.x & 31;
+  using C = TileCfg<D, kT>;
+  const int lane = threadIdx.x & 31, per_tile = kTileRows / p.G;
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int r = (int)(w % C::kRows);
   const int h = (int)(w / C::kRows % p.H);
-  int want = (int)(w / C::kRows / p.H), b = 0;
+  int want = (int)(w / C::kRows / p.H), b = 0, first = 0, count = 0;
   for (; b < p.n_req; ++b) {
-    const int n = tiles_of(p, b, C::kRows);
+    request_rows(p, b, first, count);
+    const int n = (count + C::kTiles * per_tile - 1) / (C::kTiles * per_tile);
     if (want < n) break;
     want -= n;
   }
   if (b == p.n_req) return;
-  int first, count;
-  request_rows(p, b, first, count);
-  const int64_t i = (int64_t)want * C::kRows + r;
-  if (i >= (int64_t)count * p.G) return;
-  const int t = (int)(i / p.G), token = first + t, head = h * p.G + (int)(i - (int64_t)t * p.G);
+  const int x = r % kTileRows / p.G;
+  const int t = (want * C::kTiles + r / kTileRows) * per_tile + x;
+  if (x >= per_tile || t >= count) return;
+  const int token = first + t, head = h * p.G + r % kTileRows - x * p.G;
   const int64_t group = w / C::kRows;  // (tile group, head)
   auto at = [&](int k) { return (group * splits + k) * C::kRows + r; };
   float M = kNone;
@@ -615,32 +943,34 @@ __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ 
 
 int device_sms();
 
-template <typename T, int D>
+template <typename T, int D, int kT>
 static cudaError_t launch_t(const PagedParams& p, int groups, int splits, cudaStream_t stream) {
-  using C = TileCfg<D>;
+  using C = TileCfg<D, kT>;
   static DeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(tile_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return cudaFuncSetAttribute(tile_kernel<T, D, kT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  tile_kernel<T, D><<<groups * p.H * splits, C::kThreads, C::kSmem, stream>>>(p, splits);
+  tile_kernel<T, D, kT><<<groups * p.H * splits, C::kThreads, C::kSmem, stream>>>(p, splits);
   e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
-  tile_fold_kernel<T, D><<<groups * p.H * (C::kRows / 8), 256, 0, stream>>>(p, splits);
+  tile_fold_kernel<T, D, kT><<<groups * p.H * (C::kRows / 8), 256, 0, stream>>>(p, splits);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, int kT>
 static cudaError_t launch_type(const PagedParams& p, int dtype, int groups, int splits, cudaStream_t stream) {
-  return dtype == 0 ? launch_t<Bf16, D>(p, groups, splits, stream) : launch_t<F16, D>(p, groups, splits, stream);
+  return dtype == 0 ? launch_t<Bf16, D, kT>(p, groups, splits, stream) : launch_t<F16, D, kT>(p, groups, splits, stream);
 }
 
-int tile_rows(int D) { return D == 256 ? TileCfg<256>::kRows : TileCfg<128>::kRows; }
-
-cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int groups, int splits, cudaStream_t stream) {
-  return D == 64    ? launch_type<64>(p, dtype, groups, splits, stream)
-         : D == 128 ? launch_type<128>(p, dtype, groups, splits, stream)
-                    : launch_type<256>(p, dtype, groups, splits, stream);
+cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
+                               cudaStream_t stream) {
+  if (D == 256) return launch_type<256, 1>(p, dtype, groups, splits, stream);
+  if (D == 128)
+    return tiles == 1 ? launch_type<128, 1>(p, dtype, groups, splits, stream)
+                      : launch_type<128, 2>(p, dtype, groups, splits, stream);
+  return tiles == 1 ? launch_type<64, 1>(p, dtype, groups, splits, stream)
+                    : launch_type<64, 2>(p, dtype, groups, splits, stream);
 }
 
 }  // namespace tpk

@@ -52,6 +52,7 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, int interleaved, cudaStr
 struct PagedParams {
   CUtensorMap kmap;  // pools as 2-D tensors [slot * H * 64][D], 64 x 64 boxes, 128-byte swizzle
   CUtensorMap vmap;
+  CUtensorMap qmap;  // row tiles only: q as [n_q][H * G][D], boxes of 64 channels of a KV head's rows in a tile
   const uint16_t* q;
   void* o;
   float* lse;
@@ -75,8 +76,9 @@ constexpr int kRowTile = 16;          // query rows of a split unit
 cudaError_t launch_paged_split(const PagedParams& p, int D, int dtype, cudaStream_t stream);
 
 constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row tiles aims at
-int tile_rows(int D);             // query rows of one of its blocks
-cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int groups, int splits, cudaStream_t stream);
+constexpr int kTileRows = 128;    // query rows of a tile; a block takes `tiles` (1 or 2) of them
+cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
+                               cudaStream_t stream);
 
 // ------------------------------------------------------------------- types
 struct Bf16 {
