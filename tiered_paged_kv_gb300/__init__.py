@@ -157,10 +157,12 @@ def lib():
 def _ptr(x):
     if x is None:
         return None
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     raise TypeError(f"cannot take a device pointer from {type(x)}")
 
 
@@ -295,12 +297,12 @@ def kv_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, posit
     pages (see tpk_kv_rope_append).  axis_of is a host array of rot_dim / 2 axis
     numbers (None: axis 0); q and q_out, or k, v and the pools, may be None."""
     if axis_of is not None:
-        axis_of = np.ascontiguousarray(axis_of, np.uint8)
-        if axis_of.shape != (rot_dim // 2,):
-            raise ValueError(f"axis_of has shape {axis_of.shape}, not ({rot_dim // 2},)")
+        axis_of = np.asarray(axis_of, np.uint8).tobytes()
+        if len(axis_of) != rot_dim // 2:
+            raise ValueError(f"axis_of has {len(axis_of)} entries, not {rot_dim // 2}")
     _check(lib().tpk_kv_rope_append(ctypes.byref(shape), n_tokens, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
                                     v_stride, _ptr(positions), n_axes,
-                                    None if axis_of is None else axis_of.ctypes.data, _ptr(inv_freq), rot_dim,
+                                    axis_of, _ptr(inv_freq), rot_dim,
                                     int(interleaved), _ptr(slot_map), _ptr(q_out), q_out_stride, _ptr(k_pool),
                                     _ptr(v_pool), _stream(stream)))
 

@@ -2,10 +2,11 @@
 // device: one new token per request, or a handful of query tokens per request.
 //
 // A run is 16 query rows of one (request, KV head): the G heads of a new token, or
-// (token, head) pairs of cross attention.  Every run of a request reads the same pages,
-// so request b costs pages_b * runs_b, and its pages of work are numbered request by
-// request, run by run.  Each of the N blocks of the launch takes an equal range of
-// those numbers, whatever the lengths: the device stays evenly loaded and the split
+// (token, head) pairs of cross attention.  Every run of a request reads the same pages
+// and costs that many units and kRunCost more (its queries and its join), so request b
+// costs (pages_b + kRunCost) * runs_b; the units are numbered request by request, run by
+// run, a run's own cost first.  Each of the N blocks of the launch takes an equal range
+// of those numbers, whatever the lengths: the device stays evenly loaded and the split
 // needs no host-side lengths.  A run inside one block's range is written out at once;
 // one that crosses ranges leaves a partial (running maximum, sum, unnormalised o) in
 // the block's two workspace slots -- slot 0: a run entered in the middle, slot 1: one
@@ -32,11 +33,14 @@ template <int D>
 struct SplitCfg {
   static constexpr int kPageBytes = kPageTokens * D * 2;   // keys or values of one page
   static constexpr int kStageBytes = 2 * kPageBytes;
-  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 3 : 4;
+  static constexpr int kStages = D == 64 ? 4 : 3;
   static constexpr int kBlocksPerSm = D == 256 ? 1 : D == 128 ? 2 : 3;
-  static constexpr int kRowStride = D + 8;  // floats: spreads the rows of the joined o over the banks
+  static constexpr int kRowStride = 64 + 8;  // floats: spreads the rows of the joined o over the banks
   static constexpr int kJoinBytes = kConsumers * 8 * kRowStride * 4;
-  static constexpr int kSmem = 1024 + kStages * kStageBytes + kJoinBytes;
+  static constexpr int kSharedBytes = 768;  // SplitShared
+  static constexpr int kSmem = kStages * kStageBytes + kJoinBytes + kSharedBytes;
+  // shared memory of an SM, less what each block takes besides
+  static_assert(kBlocksPerSm * (kSmem + 1024) <= 228 * 1024, "blocks per SM");
 };
 
 struct SplitShared {
@@ -64,7 +68,17 @@ __device__ __forceinline__ int request_pages(const PagedParams& p, int b, int& p
   page0 = lo >> 6;
   return hi > lo ? ((hi + 63) >> 6) - page0 : 0;
 }
-__device__ __forceinline__ int64_t per_block(int64_t total, int blocks) { return (total + blocks - 1) / blocks; }
+constexpr int kRunCost = 3;
+// Units of request b.
+__device__ __forceinline__ int64_t request_units(const PagedParams& p, int b) {
+  int page0;
+  const int pages = request_pages(p, b, page0);
+  return pages > 0 ? (int64_t)(pages + kRunCost) * request_runs(p, b) : 0;
+}
+__device__ __forceinline__ int64_t per_block(int64_t total, int blocks) {
+  const int64_t per = (total + blocks - 1) / blocks;
+  return per < kRunCost + 1 ? kRunCost + 1 : per;
+}
 
 // One stretch of pages of one run.
 struct Segment {
@@ -77,21 +91,26 @@ struct Walk {
   int64_t at, end, base;
   int b;
   __device__ __forceinline__ bool next(const PagedParams& p, Segment& s) {
-    if (at >= end) return false;
-    for (;;) {
+    while (at < end) {
       s.pages = request_pages(p, b, s.page0);
-      const int64_t work = (int64_t)s.pages * request_runs(p, b);
-      if (at < base + work) break;
-      base += work;
-      ++b;
+      const int units = s.pages + kRunCost;
+      const int64_t work = s.pages > 0 ? (int64_t)units * request_runs(p, b) : 0;
+      if (at >= base + work) {
+        base += work;
+        ++b;
+        continue;
+      }
+      const int64_t local = at - base;
+      s.b = b;
+      s.run = (int)(local / units);
+      const int from = (int)(local - (int64_t)s.run * units);
+      const int to = (int)min((int64_t)units, end - at + from);
+      at += to - from;
+      s.page = max(from - kRunCost, 0);
+      s.count = to - kRunCost - s.page;
+      if (s.count > 0) return true;  // else the range ends within the run's own cost
     }
-    const int64_t local = at - base;
-    s.b = b;
-    s.run = (int)(local / s.pages);
-    s.page = (int)(local - (int64_t)s.run * s.pages);
-    s.count = (int)min((int64_t)(s.pages - s.page), end - at);
-    at += s.count;
-    return true;
+    return false;
   }
 };
 
@@ -116,11 +135,15 @@ __device__ __forceinline__ bool run_row(const PagedParams& p, int first, int cou
 template <typename T, int D, bool kSmall>  // kSmall: runs have at most 8 rows
 __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_constant__ PagedParams p) {
   using C = SplitCfg<D>;
-  extern __shared__ uint8_t raw[];
-  uint8_t* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) uint8_t stages[];
   float* join = reinterpret_cast<float*>(stages + C::kStages * C::kStageBytes);
-  __shared__ SplitShared S;
+  static_assert(sizeof(SplitShared) <= C::kSharedBytes, "SplitShared");
+  SplitShared& S = *reinterpret_cast<SplitShared*>(stages + C::kStages * C::kStageBytes + C::kJoinBytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (smem_u32(stages) & 1023) {  // the swizzle counts on it
+    if (tid == 0) atomicOr(p.status, kStatusTimeout);
+    return;
+  }
 
   // ---- the numbering: this block's range, and (block 0) the table for the fold
   if (tid < C::kStages) {
@@ -128,19 +151,41 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
     mbar_init(&S.empty[tid], kConsumers);
     fence_mbar_init();
   }
+  Walk walk;
+  if (p.whole) {
+    // a block per run: nothing to number, nothing to join
+    __syncthreads();
+    int page0, first, count;
+    const int runs = request_runs(p, 0);  // the same for every request
+    walk.b = blockIdx.x / runs;
+    const int run = blockIdx.x - walk.b * runs;
+    const int pages = request_pages(p, walk.b, page0);
+    walk.base = 0;
+    walk.at = (int64_t)run * (pages + kRunCost);
+    walk.end = walk.at + pages + kRunCost;
+    if (pages == 0) {
+      request_rows(p, walk.b, first, count);
+      const int tiles = runs / p.H, h = run / tiles;
+      for (int i = tid; i < kRowTile * (D / 2); i += kPagedThreads) {
+        int token, head;
+        if (!run_row(p, first, count, h, run - h * tiles, i / (D / 2), token, head)) continue;
+        store_pair<T>(p, token, head, D, i % (D / 2) * 2, 0.f, 0.f);
+        if (i % (D / 2) == 0) p.lse[(int64_t)token * p.H * p.G + head] = kEmpty;
+      }
+      return;
+    }
+  } else {
   const int each = (p.n_req + kPagedThreads - 1) / kPagedThreads;
   const int b0 = min(tid * each, p.n_req), b1 = min(b0 + each, p.n_req);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    int page0;
-    mine += (int64_t)request_pages(p, b, page0) * request_runs(p, b);
-  }
+  for (int b = b0; b < b1; ++b) mine += request_units(p, b);
   int64_t inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t up = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += up;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 31) S.scan[warp] = inc;
   if (tid == 0) S.first = -1;
   __syncthreads();
@@ -155,8 +200,7 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
   if ((lo < hi && lo >= before && lo < before + mine) || blockIdx.x == 0) {
     int64_t at = before;
     for (int b = b0; b < b1; ++b) {
-      int page0;
-      const int64_t work = (int64_t)request_pages(p, b, page0) * request_runs(p, b);
+      const int64_t work = request_units(p, b);
       if (lo < hi && lo >= at && lo < at + work) {
         S.first = b;
         S.base = at;
@@ -181,8 +225,9 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
     for (int64_t i = tid; i < (int64_t)count * HQ; i += kPagedThreads) p.lse[(int64_t)first * HQ + i] = kEmpty;
   }
   if (lo >= hi) return;
+  walk = Walk{lo, hi, S.base, S.first};
+  }
 
-  Walk walk{lo, hi, S.base, S.first};
   Segment s;
   if (warp == kConsumers) {
     // ------------------------------------------------------------- producer
@@ -418,14 +463,6 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, S.m[w][g + 8 * half]);
       const float f = m[half] == kEmpty ? 0.f : exp2f(m[half] - top);
-      float* dst = join + (warp * 8 + g) * C::kRowStride + 2 * t;
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        const float x = kSmall ? acc[n][0] + acc[n][2] : acc[n][2 * half];
-        const float y = kSmall ? acc[n][1] + acc[n][3] : acc[n][2 * half + 1];
-        *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(x * f, y * f);
-      }
-      named_barrier(1, kConsumers * 32);
       // 16 threads per row
       const int row = tid >> 4, r = row + 8 * half;
       float M = kEmpty, L = 0.f;
@@ -435,38 +472,63 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
       for (int w = 0; w < kConsumers; ++w)
         if (S.m[w][r] != kEmpty) L += exp2f(S.m[w][r] - M) * S.l[w][r];
       int token, head;
-      if (run_row(p, first, count, h, tile, r, token, head) && !dead) {
-        const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
-        for (int c = (tid & 15) * 2; c < D; c += 32) {
-          float x = 0.f, y = 0.f;
-#pragma unroll
-          for (int w = 0; w < kConsumers; ++w) {
-            const float2 v = *reinterpret_cast<const float2*>(join + (w * 8 + row) * C::kRowStride + c);
-            x += v.x;
-            y += v.y;
-          }
-          if (whole) store_pair<T>(p, token, head, D, c, x * inv, y * inv);
-          else *reinterpret_cast<float2*>(p.part_o + (slot * kRowTile + r) * D + c) = make_float2(x, y);
-        }
-        if ((tid & 15) == 0) {
-          if (whole) {
-            p.lse[(int64_t)token * HQ + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
-          } else {
-            p.part_ml[slot * kRowTile + r] = M;
-            p.part_ml[(2 * (int64_t)gridDim.x + slot) * kRowTile + r] = L;
-          }
+      const bool write = run_row(p, first, count, h, tile, r, token, head) && !dead;
+      const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+      if (write && (tid & 15) == 0) {
+        if (whole) {
+          p.lse[(int64_t)token * HQ + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
+        } else {
+          p.part_ml[slot * kRowTile + r] = M;
+          p.part_ml[(2 * (int64_t)gridDim.x + slot) * kRowTile + r] = L;
         }
       }
-      named_barrier(1, kConsumers * 32);
+      float* dst = join + (warp * 8 + g) * C::kRowStride + 2 * t;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 64) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float* a = acc[c0 / 8 + n];
+          const float x = kSmall ? a[0] + a[2] : a[2 * half];
+          const float y = kSmall ? a[1] + a[3] : a[2 * half + 1];
+          *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(x * f, y * f);
+        }
+        named_barrier(1, kConsumers * 32);
+        if (write) {
+          const int c = (tid & 15) * 4;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kConsumers; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(join + (w * 8 + row) * C::kRowStride + c);
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+          }
+          if (whole) {
+            store_pair<T>(p, token, head, D, c0 + c, o.x * inv, o.y * inv);
+            store_pair<T>(p, token, head, D, c0 + c + 2, o.z * inv, o.w * inv);
+          } else {
+            *reinterpret_cast<float4*>(p.part_o + (slot * kRowTile + r) * D + c0 + c) = o;
+          }
+        }
+        named_barrier(1, kConsumers * 32);
+      }
     }
   }
 }
 
 // Joins the partials of the runs that cross block ranges: block (i, r) takes row r of
-// the run that holds the first number of range i + 1, if range i is the run's first.
+// the run that holds the first number of range i + 1, if the run's first page is in range
+// i.  The
+// partials' maxima are read at once, one a thread; then every thread sums its four
+// channels over the partials in block order, eight loads in flight.
+constexpr int kFoldParts = 64;  // weights held at a time
 template <typename T, int D>
-__global__ void __launch_bounds__(D / 4) fold_paged_kernel(const __grid_constant__ PagedParams p, int blocks, int rows) {
-  const int i = blockIdx.x / rows, r = blockIdx.x % rows, c = threadIdx.x * 4;
+__global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ PagedParams p, int blocks, int rows) {
+  __shared__ float weight[kFoldParts];
+  __shared__ float red[2];
+  const int i = blockIdx.x / rows, r = blockIdx.x % rows, tid = threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t total = p.prefix[p.n_req];
   const int64_t per = per_block(total, blocks);
   const int64_t cut = per * (i + 1);
@@ -478,11 +540,11 @@ __global__ void __launch_bounds__(D / 4) fold_paged_kernel(const __grid_constant
   }
   const int b = lo;
   int page0, first, count, token, head;
-  const int pages = request_pages(p, b, page0);
+  const int units = request_pages(p, b, page0) + kRunCost;
   const int64_t base = p.prefix[b];
-  const int run = (int)((cut - base) / pages);
-  const int64_t start = base + (int64_t)run * pages, end = start + pages;
-  if (start == cut || start < per * i) return;  // not crossed here, or joined at an earlier cut
+  const int run = (int)((cut - base) / units);
+  const int64_t end = base + (int64_t)(run + 1) * units, start = end - units + kRunCost;  // its pages
+  if (start >= cut || start < per * i) return;  // not crossed here, or joined at an earlier cut
   request_rows(p, b, first, count);
   const int tiles = request_runs(p, b) / p.H;
   const int h = run / tiles;
@@ -492,26 +554,58 @@ __global__ void __launch_bounds__(D / 4) fold_paged_kernel(const __grid_constant
   auto slot = [&](int k) { return (2 * (int64_t)(i + k) + (k == 0 ? 1 : 0)) * kRowTile + r; };
   const float* part_l = p.part_ml + 2 * (int64_t)blocks * kRowTile;
   float M = kEmpty;
-  for (int k = 0; k < n; ++k) M = fmaxf(M, p.part_ml[slot(k)]);
+  for (int k = tid; k < n; k += 64) M = fmaxf(M, p.part_ml[slot(k)]);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  if ((tid & 31) == 0) red[tid >> 5] = M;
+  __syncthreads();
+  M = fmaxf(red[0], red[1]);
+  const float ref = M == kEmpty ? 0.f : M;
   float L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (M != kEmpty) {
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const int64_t at = slot(k);
-      const float w = exp2f(p.part_ml[at] - M);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + c);
-      L += w * part_l[at];
-      o.x += w * v.x;
-      o.y += w * v.y;
-      o.z += w * v.z;
-      o.w += w * v.w;
+  constexpr int kVec = D >= 256 ? 4 : D / 64;  // channels of a thread
+  float o[kVec];
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) o[e] = 0.f;
+  const int c = tid * kVec;
+  for (int k0 = 0; k0 < n; k0 += kFoldParts) {
+    const int cnt = min(kFoldParts, n - k0);
+    __syncthreads();
+    if (tid < cnt) weight[tid] = exp2f(p.part_ml[slot(k0 + tid)] - ref);
+    float mine = tid < cnt ? weight[tid] * part_l[slot(k0 + tid)] : 0.f;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = mine;
+    __syncthreads();
+    L += red[0] + red[1];
+    for (int j0 = 0; j0 < cnt; j0 += 8) {
+      float v[8][kVec];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < cnt) {
+          const float* src = p.part_o + slot(k0 + j0 + j) * D + c;
+          if constexpr (kVec == 4) *reinterpret_cast<float4*>(v[j]) = *reinterpret_cast<const float4*>(src);
+          else if constexpr (kVec == 2) *reinterpret_cast<float2*>(v[j]) = *reinterpret_cast<const float2*>(src);
+          else v[j][0] = *src;
+        }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < cnt) {
+          const float w = weight[j0 + j];
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) o[e] += w * v[j][e];
+        }
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  store_pair<T>(p, token, head, D, c, o.x * inv, o.y * inv);
-  store_pair<T>(p, token, head, D, c + 2, o.z * inv, o.w * inv);
-  if (c == 0) p.lse[(int64_t)token * p.H * p.G + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
+  if constexpr (kVec == 1) {
+    const float x = o[0] * inv, y = __shfl_down_sync(0xffffffffu, x, 1);
+    if ((tid & 1) == 0) store_pair<T>(p, token, head, D, c, x, y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kVec; e += 2) store_pair<T>(p, token, head, D, c + e, o[e] * inv, o[e + 1] * inv);
+  }
+  if (tid == 0) p.lse[(int64_t)token * p.H * p.G + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
 }
 
 int device_sms();
@@ -524,13 +618,24 @@ static cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
     return cudaFuncSetAttribute(split_kernel<T, D, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  const int blocks = min(device_sms() * C::kBlocksPerSm, kPagedMaxBlocks);
+  const int runs = p.H * ((p.G + kRowTile - 1) / kRowTile);  // of a decode request
+  const int blocks = p.whole ? p.n_req * runs : min(device_sms() * C::kBlocksPerSm, kPagedMaxBlocks);
   split_kernel<T, D, kSmall><<<blocks, kPagedThreads, C::kSmem, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || blocks == 1) return e;
+  if (e != cudaSuccess || p.whole || blocks == 1) return e;
+  // the fold's blocks may start while the last ranges still run: they wait for them
   const int rows = p.q_off ? kRowTile : min(p.G, kRowTile);
-  fold_paged_kernel<T, D><<<(blocks - 1) * rows, D / 4, 0, stream>>>(p, blocks, rows);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((blocks - 1) * rows);
+  cfg.blockDim = dim3(64);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, fold_paged_kernel<T, D>, p, blocks, rows);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, int D>
@@ -544,7 +649,12 @@ static cudaError_t launch_dim(const PagedParams& p, int D, cudaStream_t stream) 
                                                             : launch_rows<T, 256>(p, stream);
 }
 
-cudaError_t launch_paged_split(const PagedParams& p, int D, int dtype, cudaStream_t stream) {
+// Histories of at most this many pages are not split: a block per run walks its pages
+// in less time than the numbering and the join take.
+constexpr int kWholePages = 8;
+
+cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream) {
+  p.whole = !p.q_off && p.max_pages <= kWholePages;
   return dtype == 0 ? launch_dim<Bf16>(p, D, stream) : launch_dim<F16>(p, D, stream);
 }
 

@@ -8,15 +8,18 @@
 // 32-bit position it is off by at most 2^-33 turns, where a float32 product is off by
 // 10^-2 radians at 128K.  Its upper 32 bits, signed, go through sincospif.
 //
-// A block takes `per` tokens: their angles go to shared memory once and serve every
-// head.  A task is 16 channels of one head (8 pairs, or 16 channels copied), two
-// 16-byte loads and stores.  Bound: HBM, (2 HQ + 4 H) D * 2 bytes per token.
+// A thread keeps one piece of every token's row -- 16 channels of one head: 8 pairs, or
+// 16 channels copied; two 16-byte loads and stores -- so all index arithmetic is done
+// once, and passes over the block's tokens, four in flight.  The tokens' angles go to
+// shared memory once per block and serve every head.  Bound: HBM, (2 HQ + 4 H) D * 2
+// bytes per token.
 #include "paged.cuh"
 
 namespace tpk {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopePairs = 256;  // angles a block holds: per * rot / 2
+constexpr int kRopeThreads = 256;  // at most
+constexpr int kRopePairs = 1024;   // angles a block holds: tokens * rot / 2
+constexpr int kRopeTokens = 8;     // tokens of a block, at most (4: 39.1 us, 8: 36.5, 16: 40.9 at 8200 tokens)
 constexpr int kRopeUnroll = 4;
 
 // frac(f / (2 pi)) in units of 2^-64 turns.
@@ -35,128 +38,110 @@ __device__ __forceinline__ uint64_t turns64(float f) {
   return (w >> 31) ? 0 - t : t;
 }
 
-struct Two {
-  uint4 a, b;
-};
-
 template <typename T, bool kPairs>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p, int per, int tasks,
-                                                            int blocks16) {
-  __shared__ float2 turn[kRopePairs];  // (cos, sin) of [token][pair]
+                                                            int passes) {
+  // (cos, sin) of two pairs, [token][pair / 2 mod 4][pair / 8]: the lanes of a head read
+  // neighbours
+  __shared__ float4 turn[kRopePairs / 2];
+  __shared__ int64_t place[kRopeTokens];
   const int tid = threadIdx.x;
-  const int t0 = blockIdx.x * per, nt = min(per, p.n_tokens - t0);
-  const int half = p.rot >> 1, rot16 = p.rot >> 4;
+  const int t0 = blockIdx.x / passes * per, nt = min(per, p.n_tokens - t0);
+  const int half = p.rot >> 1, pieces = p.D >> 4;
   const int kheads = p.k ? p.H : 0;
-  const int total = nt * tasks;
 
-  // task -> token (within the block), head, and its two 8-channel pieces
-  auto split = [&](int i, int& t, int& head, int& j, int& ca, int& cb) {
-    t = i / tasks;
-    const int r = i - t * tasks;
-    head = r / blocks16;
-    j = r - head * blocks16;
-    const bool turned = j < rot16 && head < p.HQ + kheads;
-    ca = (kPairs || !turned) ? 16 * j : 8 * j;
-    cb = (kPairs || !turned) ? 16 * j + 8 : half + 8 * j;
-    return turned;
-  };
-  auto load = [&](int i) {
-    Two v;
-    int t, head, j, ca, cb;
-    split(i, t, head, j, ca, cb);
-    const int64_t row = t0 + t;
-    const uint16_t* src = head < p.HQ ? p.q + row * p.q_stride + head * p.D
-                          : head < p.HQ + kheads ? p.k + row * p.k_stride + (head - p.HQ) * p.D
-                                                 : p.v + row * p.v_stride + (head - p.HQ - kheads) * p.D;
-    v.a = *reinterpret_cast<const uint4*>(src + ca);
-    v.b = *reinterpret_cast<const uint4*>(src + cb);
-    return v;
-  };
-
-  Two v[kRopeUnroll];
+  // ---- this thread's piece
+  const int task = blockIdx.x % passes * blockDim.x + tid;
+  const bool mine = task < tasks;
+  const int head = task / pieces, j = task - head * pieces;
+  const bool query = head < p.HQ, key = !query && head < p.HQ + kheads;
+  const bool turned = (query || key) && 16 * j < p.rot;
+  const int ca = (kPairs || !turned) ? 16 * j : 8 * j;
+  const int cb = (kPairs || !turned) ? 16 * j + 8 : half + 8 * j;
+  const int h = query ? head : key ? head - p.HQ : head - p.HQ - kheads;
+  const int64_t stride = query ? p.q_stride : key ? p.k_stride : p.v_stride;
+  const uint16_t* src = (query ? p.q : key ? p.k : p.v) + (mine ? t0 * stride + h * p.D : 0);
+  uint4 a[kRopeUnroll], b[kRopeUnroll];
+  auto load = [&](int t) {
 #pragma unroll
-  for (int u = 0; u < kRopeUnroll; ++u)
-    if (tid + u * kRopeThreads < total) v[u] = load(tid + u * kRopeThreads);
-  for (int i = tid; i < nt * half; i += kRopeThreads) {
-    const int t = i / half, j = i - t * half;
-    const int64_t x = p.positions[(int64_t)p.axis_of[j] * p.n_tokens + t0 + t];
-    const uint64_t a = turns64(p.inv_freq[j]) * (uint64_t)x;
+    for (int u = 0; u < kRopeUnroll; ++u)
+      if (mine && t + u < nt) {
+        a[u] = *reinterpret_cast<const uint4*>(src + (t + u) * stride + ca);
+        b[u] = *reinterpret_cast<const uint4*>(src + (t + u) * stride + cb);
+      }
+  };
+  load(0);
+
+  // ---- the tokens' angles and places
+  for (int i = tid; i < nt * half; i += blockDim.x) {
+    const int t = i / half, x = i - t * half;
+    const int64_t pos = p.positions[(int64_t)p.axis_of[x] * p.n_tokens + t0 + t];
+    const uint64_t angle = turns64(p.inv_freq[x]) * (uint64_t)pos;
     float s, c;
-    sincospif((float)(int32_t)((a + 0x80000000u) >> 32) * 0x1p-31f, &s, &c);  // of pi * (2 * turns)
-    turn[i] = make_float2(c, s);
+    sincospif((float)(int32_t)((angle + 0x80000000u) >> 32) * 0x1p-31f, &s, &c);  // of pi * (2 * turns)
+    reinterpret_cast<float2*>(turn + t * (half >> 1) + (x >> 1 & 3) * (half >> 3) + (x >> 3))[x & 1] = make_float2(c, s);
+  }
+  if (tid < nt) {
+    const int64_t slot = p.slot_map ? p.slot_map[t0 + tid] : 0;
+    const bool past = p.slot_map && slot >= p.slot_limit;
+    if (past) atomicOr(p.status, kStatusBadSlot);
+    place[tid] = past ? -1 : slot;
   }
   __syncthreads();
+  if (!mine) return;
 
-  for (int i0 = tid; i0 < total; i0 += kRopeUnroll * kRopeThreads) {
-    if (i0 != tid) {
-#pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u)
-        if (i0 + u * kRopeThreads < total) v[u] = load(i0 + u * kRopeThreads);
-    }
+  uint16_t* const dst = query ? p.q_out + t0 * p.q_out_stride + h * p.D : key ? p.k_pool : p.v_pool;
+  for (int t = 0; t < nt; t += kRopeUnroll) {
+    if (t > 0) load(t);
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
-      const int i = i0 + u * kRopeThreads;
-      if (i >= total) break;
-      int t, head, j, ca, cb;
-      const bool turned = split(i, t, head, j, ca, cb);
-      const int64_t slot = p.slot_map ? p.slot_map[t0 + t] : 0;
+      if (t + u >= nt) break;
+      const int64_t slot = place[t + u];
       if (slot < 0) continue;  // padding
-      if (p.slot_map && slot >= p.slot_limit) {
-        atomicOr(p.status, kStatusBadSlot);
-        continue;
-      }
-      uint4 a = v[u].a, b = v[u].b;
       if (turned) {
-        uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
-        uint32_t* wb = reinterpret_cast<uint32_t*>(&b);
-        const float2* cs = turn + t * half + 8 * j;
-        if (kPairs) {
+        uint32_t* wa = reinterpret_cast<uint32_t*>(&a[u]);
+        uint32_t* wb = reinterpret_cast<uint32_t*>(&b[u]);
+        const float4* cs = turn + (t + u) * (half >> 1) + j;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 4; ++k) {
+          const float4 e = cs[k * (half >> 3)];  // pairs 8 j + 2 k and the next
+          if (kPairs) {
+            uint32_t* w = k < 2 ? wa + 2 * k : wb + 2 * k - 4;
+            const float2 x = T::unpack(w[0]), y = T::unpack(w[1]);
+            w[0] = T::pack(x.x * e.x - x.y * e.y, x.y * e.x + x.x * e.y);
+            w[1] = T::pack(y.x * e.z - y.y * e.w, y.y * e.z + y.x * e.w);
+          } else {
             const float2 x = T::unpack(wa[k]), y = T::unpack(wb[k]);
-            const float2 e = cs[k], f = cs[k + 4];
-            wa[k] = T::pack(x.x * e.x - x.y * e.y, x.y * e.x + x.x * e.y);
-            wb[k] = T::pack(y.x * f.x - y.y * f.y, y.y * f.x + y.x * f.y);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 x = T::unpack(wa[k]), y = T::unpack(wb[k]);
-            const float2 e = cs[2 * k], f = cs[2 * k + 1];
-            wa[k] = T::pack(x.x * e.x - y.x * e.y, x.y * f.x - y.y * f.y);
-            wb[k] = T::pack(y.x * e.x + x.x * e.y, y.y * f.x + x.y * f.y);
+            wa[k] = T::pack(x.x * e.x - y.x * e.y, x.y * e.z - y.y * e.w);
+            wb[k] = T::pack(y.x * e.x + x.x * e.y, y.y * e.z + x.y * e.w);
           }
         }
       }
-      uint16_t* dst;
-      if (head < p.HQ) {
-        dst = p.q_out + (t0 + t) * p.q_out_stride + head * p.D;
-      } else {
-        const bool key = head < p.HQ + kheads;
-        const int h = head - p.HQ - (key ? 0 : kheads);
-        dst = (key ? p.k_pool : p.v_pool) + (((slot >> 6) * p.H + h) * kPageTokens + (slot & 63)) * (int64_t)p.D;
-      }
-      *reinterpret_cast<uint4*>(dst + ca) = a;
-      *reinterpret_cast<uint4*>(dst + cb) = b;
+      uint16_t* to = query ? dst + (t + u) * p.q_out_stride
+                           : dst + (((slot >> 6) * p.H + h) * kPageTokens + (slot & 63)) * (int64_t)p.D;
+      *reinterpret_cast<uint4*>(to + ca) = a[u];
+      *reinterpret_cast<uint4*>(to + cb) = b[u];
     }
   }
 }
 
 cudaError_t launch_rope(const RopeParams& p, int dtype, int interleaved, cudaStream_t stream) {
-  const int blocks16 = p.D / 16;
-  const int tasks = (p.HQ + (p.k ? 2 * p.H : 0)) * blocks16;
-  // tokens per block: six tasks per thread where there are many tokens (loads in
-  // flight), one where the tokens hardly fill the device
-  int per = max(1, min(8, 6 * kRopeThreads / tasks));
+  const int tasks = (p.HQ + (p.k ? 2 * p.H : 0)) * (p.D / 16);
+  // equal passes over a row's pieces, in whole warps
+  const int passes = (tasks + kRopeThreads - 1) / kRopeThreads;
+  const int threads = ((tasks + passes - 1) / passes + 31) / 32 * 32;
+  // tokens of a block: as many as keep every SM at eight blocks, up to what shared memory
+  // holds; one where the tokens hardly fill the device
+  int per = min(kRopeTokens, p.n_tokens * passes / (8 * 152));
   if (p.rot > 0) per = min(per, 2 * kRopePairs / p.rot);
-  per = max(1, min(per, p.n_tokens / 304));
-  const int blocks = (p.n_tokens + per - 1) / per;
+  per = max(1, per);
+  const int blocks = (p.n_tokens + per - 1) / per * passes;
   if (dtype == 0) {
-    if (interleaved) rope_kernel<Bf16, true><<<blocks, kRopeThreads, 0, stream>>>(p, per, tasks, blocks16);
-    else rope_kernel<Bf16, false><<<blocks, kRopeThreads, 0, stream>>>(p, per, tasks, blocks16);
+    if (interleaved) rope_kernel<Bf16, true><<<blocks, threads, 0, stream>>>(p, per, tasks, passes);
+    else rope_kernel<Bf16, false><<<blocks, threads, 0, stream>>>(p, per, tasks, passes);
   } else {
-    if (interleaved) rope_kernel<F16, true><<<blocks, kRopeThreads, 0, stream>>>(p, per, tasks, blocks16);
-    else rope_kernel<F16, false><<<blocks, kRopeThreads, 0, stream>>>(p, per, tasks, blocks16);
+    if (interleaved) rope_kernel<F16, true><<<blocks, threads, 0, stream>>>(p, per, tasks, passes);
+    else rope_kernel<F16, false><<<blocks, threads, 0, stream>>>(p, per, tasks, passes);
   }
   return cudaGetLastError();
 }

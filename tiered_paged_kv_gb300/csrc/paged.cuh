@@ -69,11 +69,12 @@ struct PagedParams {
   uint64_t wait_ns;
   float qscale;  // sm_scale * log2(e)
   int n_req, n_q, max_pages, H, G, o_f32;
+  int whole;  // a block per run (set at launch)
 };
 
 constexpr int kPagedMaxBlocks = 512;  // blocks of a split launch; each owns two partial slots
 constexpr int kRowTile = 16;          // query rows of a split unit
-cudaError_t launch_paged_split(const PagedParams& p, int D, int dtype, cudaStream_t stream);
+cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream);
 
 constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row tiles aims at
 constexpr int kTileRows = 128;    // query rows of a tile; a block takes `tiles` (1 or 2) of them
