@@ -50,10 +50,8 @@ struct SplitShared {
   float m[kConsumers][kRowTile];
   float l[kConsumers][kRowTile];
   int64_t scan[kPagedThreads / 32];
-  int64_t total;
-  int64_t lo;       // this block's range starts here
-  int64_t base;     // first number of the request it starts in
-  int first;        // that request
+  int64_t base;  // more than kScanned requests: first unit of the one the block starts in
+  int first;     // that request
 };
 
 // Runs and pages of request b.
@@ -79,6 +77,46 @@ __device__ __forceinline__ int64_t per_block(int64_t total, int blocks) {
   const int64_t per = (total + blocks - 1) / blocks;
   return per < kRunCost + 1 ? kRunCost + 1 : per;
 }
+
+// The numbering of up to kScanned requests by one warp: lane i has requests 4 i .. 4 i + 3.
+constexpr int kScanned = 128;
+struct Numbers {
+  int64_t total, before;  // all units; those before this lane's requests
+  int64_t units[4];
+  __device__ __forceinline__ void load(const PagedParams& p) {
+    const int lane = threadIdx.x & 31;
+    int64_t mine = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      units[x] = 4 * lane + x < p.n_req ? request_units(p, 4 * lane + x) : 0;
+      mine += units[x];
+    }
+    int64_t inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += up;
+    }
+    before = inc - mine;
+    total = __shfl_sync(0xffffffffu, inc, 31);
+  }
+  // The request that holds unit `at` (below total) and the units before it.
+  __device__ __forceinline__ void find(int64_t at, int& b, int64_t& base) const {
+    int64_t begin = before, here = -1;
+    int mine = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (at >= begin && at < begin + units[x]) {
+        here = begin;
+        mine = 4 * (threadIdx.x & 31) + x;
+      }
+      begin += units[x];
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, here >= 0)) - 1;
+    b = __shfl_sync(0xffffffffu, mine, src);
+    base = __shfl_sync(0xffffffffu, here, src);
+  }
+};
 
 // One stretch of pages of one run.
 struct Segment {
@@ -146,6 +184,10 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
   }
 
   // ---- the numbering: this block's range, and (block 0) the table for the fold
+  if (tid == kConsumers * 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.vmap) : "memory");
+  }
   if (tid < C::kStages) {
     mbar_init(&S.full[tid], 1);
     mbar_init(&S.empty[tid], kConsumers);
@@ -175,42 +217,57 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
       return;
     }
   } else {
-  const int each = (p.n_req + kPagedThreads - 1) / kPagedThreads;
-  const int b0 = min(tid * each, p.n_req), b1 = min(b0 + each, p.n_req);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += request_units(p, b);
-  int64_t inc = mine;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int64_t lo, hi;
+    if (p.n_req <= kScanned) {
+      Numbers numbers;
+      numbers.load(p);
+      const int64_t per = per_block(numbers.total, gridDim.x);
+      lo = min(per * blockIdx.x, numbers.total);
+      hi = min(lo + per, numbers.total);
+      if (lo < hi) numbers.find(lo, walk.b, walk.base);
+      __syncthreads();
+    } else {
+      const int each = (p.n_req + kPagedThreads - 1) / kPagedThreads;
+      const int b0 = min(tid * each, p.n_req), b1 = min(b0 + each, p.n_req);
+      int64_t mine = 0;
+      for (int b = b0; b < b1; ++b) mine += request_units(p, b);
+      int64_t inc = mine;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += up;
-  }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (lane == 31) S.scan[warp] = inc;
-  if (tid == 0) S.first = -1;
-  __syncthreads();
-  int64_t total = 0, before = inc - mine;
-#pragma unroll
-  for (int w = 0; w < kPagedThreads / 32; ++w) {
-    if (w < warp) before += S.scan[w];
-    total += S.scan[w];
-  }
-  const int64_t per = per_block(total, gridDim.x);
-  const int64_t lo = min(per * blockIdx.x, total), hi = min(lo + per, total);
-  if ((lo < hi && lo >= before && lo < before + mine) || blockIdx.x == 0) {
-    int64_t at = before;
-    for (int b = b0; b < b1; ++b) {
-      const int64_t work = request_units(p, b);
-      if (lo < hi && lo >= at && lo < at + work) {
-        S.first = b;
-        S.base = at;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += up;
       }
-      if (blockIdx.x == 0) p.prefix[b] = at;
-      at += work;
+      if (lane == 31) S.scan[warp] = inc;
+      __syncthreads();
+      int64_t total = 0, before = inc - mine;
+#pragma unroll
+      for (int w = 0; w < kPagedThreads / 32; ++w) {
+        if (w < warp) before += S.scan[w];
+        total += S.scan[w];
+      }
+      const int64_t per = per_block(total, gridDim.x);
+      lo = min(per * blockIdx.x, total);
+      hi = min(lo + per, total);
+      if ((lo < hi && lo >= before && lo < before + mine) || blockIdx.x == 0) {
+        int64_t at = before;
+        for (int b = b0; b < b1; ++b) {
+          const int64_t work = request_units(p, b);
+          if (lo < hi && lo >= at && lo < at + work) {
+            S.first = b;
+            S.base = at;
+          }
+          if (blockIdx.x == 0) p.prefix[b] = at;
+          at += work;
+        }
+      }
+      if (blockIdx.x == 0 && tid == 0) p.prefix[p.n_req] = total;
+      __syncthreads();
+      walk.b = S.first;
+      walk.base = S.base;
     }
-  }
-  if (blockIdx.x == 0 && tid == 0) p.prefix[p.n_req] = total;
-  __syncthreads();
+    walk.at = lo;
+    walk.end = hi;
 
   // ---- requests that attend nothing
   for (int b = blockIdx.x; b < p.n_req; b += gridDim.x) {
@@ -224,8 +281,7 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
     }
     for (int64_t i = tid; i < (int64_t)count * HQ; i += kPagedThreads) p.lse[(int64_t)first * HQ + i] = kEmpty;
   }
-  if (lo >= hi) return;
-  walk = Walk{lo, hi, S.base, S.first};
+    if (lo >= hi) return;
   }
 
   Segment s;
@@ -528,28 +584,48 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
   __shared__ float weight[kFoldParts];
   __shared__ float red[2];
   const int i = blockIdx.x / rows, r = blockIdx.x % rows, tid = threadIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t total = p.prefix[p.n_req];
+  // ---- which run: from the lengths where they are few, before the partials are there
+  int64_t total, base = 0;
+  int b = 0;
+  Numbers numbers;
+  if (p.n_req <= kScanned) {
+    numbers.load(p);
+    total = numbers.total;
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    total = p.prefix[p.n_req];
+  }
   const int64_t per = per_block(total, blocks);
   const int64_t cut = per * (i + 1);
-  if (cut >= total) return;
-  int lo = 0, hi = p.n_req - 1;
-  while (lo < hi) {  // the request that holds number `cut`
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.prefix[mid] <= cut) lo = mid; else hi = mid - 1;
+  bool mine = cut < total;
+  int n = 0, token = 0, head = 0;
+  if (mine) {
+    if (p.n_req <= kScanned) {
+      numbers.find(cut, b, base);
+    } else {
+      int lo = 0, hi = p.n_req - 1;
+      while (lo < hi) {  // the request that holds number `cut`
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.prefix[mid] <= cut) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
+      base = p.prefix[b];
+    }
+    int page0, first, count;
+    const int units = request_pages(p, b, page0) + kRunCost;
+    const int run = (int)((cut - base) / units);
+    const int64_t end = base + (int64_t)(run + 1) * units, start = end - units + kRunCost;  // its pages
+    mine = start < cut && start >= per * i;  // crossed here, and not joined at an earlier cut
+    request_rows(p, b, first, count);
+    const int tiles = request_runs(p, b) / p.H;
+    const int h = run / tiles;
+    mine = mine && run_row(p, first, count, h, run - h * tiles, r, token, head);
+    n = (int)((end - 1) / per) - i + 1;  // blocks i .. i + n - 1 hold a piece
   }
-  const int b = lo;
-  int page0, first, count, token, head;
-  const int units = request_pages(p, b, page0) + kRunCost;
-  const int64_t base = p.prefix[b];
-  const int run = (int)((cut - base) / units);
-  const int64_t end = base + (int64_t)(run + 1) * units, start = end - units + kRunCost;  // its pages
-  if (start >= cut || start < per * i) return;  // not crossed here, or joined at an earlier cut
-  request_rows(p, b, first, count);
-  const int tiles = request_runs(p, b) / p.H;
-  const int h = run / tiles;
-  if (!run_row(p, first, count, h, run - h * tiles, r, token, head)) return;
-  const int n = (int)((end - 1) / per) - i + 1;  // blocks i .. i + n - 1 hold a piece
+  // every block waits, whether it has a row or not: the launch must not end before the
+  // one whose partials it joins
+  if (p.n_req <= kScanned) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!mine) return;
   // block i left the run before its end, the others entered it in the middle
   auto slot = [&](int k) { return (2 * (int64_t)(i + k) + (k == 0 ? 1 : 0)) * kRowTile + r; };
   const float* part_l = p.part_ml + 2 * (int64_t)blocks * kRowTile;
