@@ -135,6 +135,25 @@ def test_bad_lengths_and_offsets_are_clamped():
     assert tpk.get_device_status(reset=True) == (4, 1)
 
 
+@pytest.mark.parametrize("n", [9, 300])
+def test_extreme_ranges(n):
+    """Range bounds at the ends of int32: cut to the states, empty where they cross."""
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    r = [[(lo, hi), (0, lo), (hi, hi), (lo, 5), (300, hi), (hi, lo), (lo, lo), (64, 65)][i % 8] for i in range(n)]
+    run([n], [700], 1, 2, 128, "bf16", ranges=r)
+
+
+def test_short_wait_limit_alone_changes_nothing():
+    c = Cross(Pages([3000, 900], 2, 128, "bf16", 4), [400, 300], 2)
+    tpk.set_test_wait(50_000_000, -1)
+    try:
+        c.call()
+        c.check()
+    finally:
+        tpk.set_test_wait()
+    assert tpk.get_device_status(reset=True) == (0, 0)
+
+
 def test_no_queries():
     run([0, 0], [100, 5], 1, 1, 64, "bf16")
 

@@ -109,3 +109,41 @@ def test_replayed_steps_of_a_growing_batch():
                                     torch.ones(1, k.shape[0], dtype=torch.bool), D ** -0.5)
                     check_attention(o1[b, j:j + 1].cpu(), l1[b, j:j + 1].cpu(), ref, D, k.shape[0], dt)
     assert tpk.get_device_status(reset=True) == (0, 0)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 elements, the history in its last slots: stored there by
+    the rotary call, read back by both attention calls."""
+    H, G, D, n = 4, 2, 256, 150
+    slots = 2 ** 32 // (H * PAGE * D) + 8
+    dt = torch.bfloat16
+    kp, vp = (torch.empty(slots, H, PAGE, D, dtype=dt, device="cuda") for _ in range(2))
+    shape = tpk.PagedShape(H, G, D, kv_slots=slots, max_pages=12)
+    gen = torch.Generator().manual_seed(2)
+    x = torch.randn(2, n, H, D, generator=gen).to(dt)
+    table = torch.full((1, 12), -1, dtype=torch.int32)
+    table[0, :3] = torch.tensor([slots - 1, slots - 3, slots - 2])
+    t = torch.arange(n)
+    slot = table[0, t // PAGE].long() * PAGE + t % PAGE
+    d = x.cuda()
+    tpk.kv_rope_append(shape, n, None, 0, d[0], H * D, d[1], H * D, None, 1, None, None, 0, False, slot.cuda(), None, 0, kp, vp)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    ref = x.double()
+    for nq in (1, 200):
+        q = torch.randn(nq, H * G, D, generator=gen).to(dt)
+        o, lse = torch.zeros(nq, H * G, D, dtype=dt, device="cuda"), torch.zeros(nq, H * G, device="cuda")
+        w = H * G * D
+        if nq == 1:
+            nb = tpk.decode_paged_workspace_bytes(shape, 1)
+            ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+            tpk.decode_attn_paged(shape, 1, q.cuda(), w, kp, vp, table.cuda(), lens, None, o, w, False, lse, ws, nb)
+        else:
+            nb = tpk.cross_paged_workspace_bytes(shape, 1, nq)
+            ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+            off = torch.tensor([0, nq], dtype=torch.int32, device="cuda")
+            tpk.cross_attn_paged(shape, 1, nq, q.cuda(), w, off, kp, vp, table.cuda(), lens, None, o, w, lse, ws, nb)
+        torch.cuda.synchronize()
+        for j in range(H * G):
+            want = attention(q[:, j].double(), ref[0, :, j // G], ref[1, :, j // G], torch.ones(nq, n, dtype=torch.bool), D ** -0.5)
+            check_attention(o[:, j].cpu(), lse[:, j].cpu(), want, D, n, dt, one_plane=True, what=f"{nq} queries head {j}")
+    assert tpk.get_device_status(reset=True) == (0, 0)

@@ -103,26 +103,40 @@ void place_ws(PagedParams& p, int n_req, void* ws) {
   p.part_o = reinterpret_cast<float*>(w);
 }
 
-// How cross attention of n_q tokens is cut: `groups` bounds the row-tile groups of one
-// KV head (whole ones, and one per request that is not), `splits` parts of the keys
-// fill the device where those are few; groups = 0: few rows per request, the split
-// kernel's 16-row units fit them better.
+// How cross attention of n_q tokens is cut.  groups = 0: the split kernel's 16-row units.
+// Otherwise row-tile items of one or two 128-row tiles: `groups` bounds them for one KV
+// head (whole ones, and one per request that is not), `splits` parts of the keys fill
+// the device where they are few.  The rules go by what the host knows (lengths are on
+// the device): n_req, n_q and the table's width.
 struct CrossPlan {
-  int tiles, groups, splits;
+  int tiles;
+  int64_t groups, splits;
   int64_t rows(const tpk_paged_shape* s) const {  // of all blocks
-    return (int64_t)groups * s->kv_heads * splits * tiles * kTileRows;
+    return groups * s->kv_heads * splits * tiles * kTileRows;
   }
 };
 CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
-  const int64_t rows = (int64_t)n_q * s->group;
-  if (rows <= (int64_t)kRowTile * n_req) return {0, 0, 1};
-  // two tiles share the keys and values, unless most of the second would be empty
-  const int64_t per_tile = kTileRows / s->group;
-  const int tiles = s->head_dim == 256 || n_q <= per_tile * n_req ? 1 : 2;
+  const int64_t H = s->kv_heads, per_tile = kTileRows / s->group;
+  // The split kernel spreads single pages over the device and starts faster, the tiles
+  // read a page once for 128 rows: up to about six (page, 16 rows) units per SM the
+  // first wins (one request of 8 tokens, 6000 states, 4 x 8 heads of 256: 25 against 27
+  // us; of 1 token: 16 against 23; four of 1 token, 3000 states, 8 x 4 heads of 128, ten
+  // units per SM: 20 against 18; of 32 tokens: 57 against 28).
+  const int64_t units = ((int64_t)n_q * s->group / kRowTile + n_req) * H * s->max_pages;
+  if (units <= 6 * kTileBlocks) return {0, 0, 1};
+  // Two tiles share the keys and values and take about 1.5 times one tile's time, so one
+  // is better where it needs at most 1.5 times the waves (four requests of 128 tokens,
+  // 3000 states, 8 x 4 heads of 128: 34 us with one tile, 47 with two; sixteen of 128, 1000
+  // states, 8 x 2 heads of 64: 25 and 20).  Requests count as equally long.
+  const int64_t each = ((int64_t)n_q + n_req - 1) / n_req;
+  auto waves = [&](int tiles) {
+    const int64_t items = n_req * ((each + tiles * per_tile - 1) / (tiles * per_tile)) * H;
+    return (items + kTileBlocks - 1) / kTileBlocks;
+  };
+  const int tiles = s->head_dim == 256 || 2 * waves(1) <= 3 * waves(2) ? 1 : 2;  // 256: TMEM holds one
   const int64_t groups = n_q / (tiles * per_tile) + n_req;
-  const int64_t blocks = groups * s->kv_heads;
-  const int64_t splits = std::min<int64_t>(kTileBlocks / blocks, (s->max_pages + 3) / 4);  // two key tiles a part
-  return {tiles, (int)groups, (int)std::max<int64_t>(splits, 1)};
+  const int64_t splits = std::min<int64_t>(kTileBlocks / (groups * H), (s->max_pages + 3) / 4);  // two key tiles a part
+  return {tiles, groups, std::max<int64_t>(splits, 1)};
 }
 
 size_t cross_ws_bytes(const tpk_paged_shape* s, int n_req, int n_q) {
@@ -306,7 +320,7 @@ tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const 
 }
 
 size_t tpk_cross_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_q) {
-  return sized(shape, n_req) && n_q >= 0 && shape->kv_heads > 0 && shape->group > 0 ? cross_ws_bytes(shape, n_req, n_q) : 0;
+  return sized(shape, n_req) && n_q >= 0 && shape->kv_heads > 0 && shape->group > 0 && shape->group <= kMaxGroup ? cross_ws_bytes(shape, n_req, n_q) : 0;
 }
 
 tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q, const void* q, int64_t q_stride,
@@ -341,7 +355,7 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
     if (st != TPK_OK) return st;
     p.part_ml = static_cast<float*>(ws);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256((size_t)rows * 8));
-    e = launch_cross_tiles(p, shape->head_dim, shape->dtype, plan.tiles, plan.groups, plan.splits,
+    e = launch_cross_tiles(p, shape->head_dim, shape->dtype, plan.tiles, (int)plan.groups, (int)plan.splits,
                            reinterpret_cast<cudaStream_t>(stream));
   }
   return e == cudaSuccess ? TPK_OK : cuda_fail(e, "cross attention launch");

@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.kmap) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.vmap) : "memory");
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == C::kMma) tmem_alloc(&S.tmem);
   tc_fence_before();
   __syncthreads();
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         see_hi = it.len;
         if (p.range) {
           see_lo = max(0, p.range[2 * (int64_t)token]);
-          see_hi = min(see_hi, p.range[2 * (int64_t)token + 1]);
+          see_hi = max(0, min(see_hi, p.range[2 * (int64_t)token + 1]));
         }
       }
       const int32_t* table = p.table + (int64_t)it.b * p.max_pages;
@@ -749,8 +750,9 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         const int lo = see_lo - k0, hi = see_hi - k0;
         const bool plain = !neg && __all_sync(0xffffffffu, lo <= 0 && hi >= kMine && there);
         // scores [c, c + 32) of this half; they are read twice, which takes half the
-        // registers and next to no time.  (The loops over them are not unrolled: the
-        // kernel's roles share an instruction cache.)
+        // registers and next to no time.  (The roles share an instruction cache: of the
+        // loops over them only the first is unrolled, with two row tiles, 316 -> 302 us at
+        // eight prompts; with one tile that costs 4 %.)
         auto scores = [&](float(&x)[32], int c) {
           tc_ld32(x, s_addr + c);
           tc_wait_ld();
@@ -764,7 +766,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
           }
         };
         float top[4] = {kNone, kNone, kNone, kNone};
-#pragma unroll 1
+#pragma unroll (C::kTiles == 2 ? 2 : 1)
         for (int c = 0; c < kMine; c += 32) {
           float x[32];
           scores(x, c);
@@ -910,10 +912,12 @@ __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ 
     if (want < n) break;
     want -= n;
   }
-  if (b == p.n_req) return;
   const int x = r % kTileRows / p.G;
   const int t = (want * C::kTiles + r / kTileRows) * per_tile + x;
-  if (x >= per_tile || t >= count) return;
+  // every block waits, whether it has a row or not: the launch must not end before the
+  // one whose parts it joins
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (b == p.n_req || x >= per_tile || t >= count) return;
   const int token = first + t, head = h * p.G + r % kTileRows - x * p.G;
   const int64_t group = w / C::kRows;  // (tile group, head)
   auto at = [&](int k) { return (group * splits + k) * C::kRows + r; };
@@ -954,8 +958,18 @@ static cudaError_t launch_t(const PagedParams& p, int groups, int splits, cudaSt
   tile_kernel<T, D, kT><<<groups * p.H * splits, C::kThreads, C::kSmem, stream>>>(p, splits);
   e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
-  tile_fold_kernel<T, D, kT><<<groups * p.H * (C::kRows / 8), 256, 0, stream>>>(p, splits);
-  return cudaGetLastError();
+  // the fold's blocks may start while the last parts still run: they wait for them
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(groups * p.H * (C::kRows / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tile_fold_kernel<T, D, kT>, p, splits);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D, int kT>

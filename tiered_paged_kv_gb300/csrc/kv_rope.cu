@@ -130,9 +130,9 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, int interleaved, cudaStr
   // equal passes over a row's pieces, in whole warps
   const int passes = (tasks + kRopeThreads - 1) / kRopeThreads;
   const int threads = ((tasks + passes - 1) / passes + 31) / 32 * 32;
-  // tokens of a block: as many as keep every SM at eight blocks, up to what shared memory
+  // tokens of a block: as many as leave every SM eight blocks, up to what shared memory
   // holds; one where the tokens hardly fill the device
-  int per = min(kRopeTokens, p.n_tokens * passes / (8 * 152));
+  int per = (int)min((int64_t)kRopeTokens, (int64_t)p.n_tokens * passes / (8 * 152));
   if (p.rot > 0) per = min(per, 2 * kRopePairs / p.rot);
   per = max(1, per);
   const int blocks = (p.n_tokens + per - 1) / per * passes;
