@@ -10,7 +10,8 @@
 //
 // Roles: a loader warp finds the items (the block's own, then blocks not started that it
 // takes over from the launch queue, longest requests first), describes them to the
-// others and loads keys and values; two warps copy the queries; one thread issues the
+// others and loads keys and values (at D = 256 a warp of its own loads the values); one
+// warp loads queries; one thread issues the
 // matrix instructions; 8 or 16 warps do the softmax and write the rows.  All of them run
 // ahead into the next item as far as their buffers let them, so that its start hides
 // behind the end of the one before.
@@ -53,7 +54,11 @@ struct TileCfg {
   static constexpr int kSmem = kSharedBytes + kTiles * kQBytes + kSlots * kSlotBytes;
   static constexpr int kSoftWarps = kTiles * 8;  // softmax: two threads per row
   static constexpr int kMma = kSoftWarps, kLoad = kMma + 1, kQuery = kLoad + 1;
-  static constexpr int kThreads = (kQuery + 1) * 32;
+  // At D = 256 one loader issues more slowly than the tensor core takes the tiles, and the
+  // values get a warp of their own (72 -> 70 us at the clips); at 128 it costs 2 %.
+  static constexpr bool kTwoLoaders = kParts == 2;
+  static constexpr int kValues = kQuery + 1;
+  static constexpr int kThreads = (kQuery + 1 + kTwoLoaders) * 32;
 };
 
 // One tile group of one (request, KV head), or one part of its keys.
@@ -245,6 +250,18 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+struct Keys {
+  static constexpr bool value = false;
+};
+struct Values {
+  static constexpr bool value = true;
+};
+// Page-table entries of 16 key tiles, one a lane.
+struct TableWindow {
+  int32_t entry = -1;
+  int window = -1;
+};
+
 // Finds the request of a tile group.  Lane i of the warp holds requests base + i and
 // base + 32 + i: their query rows, lengths, groups, and the groups before them.
 struct Requests {
@@ -343,7 +360,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       mbar_init(&S.o_full[i], 1);
       mbar_init(&S.o_empty[i], 256);
       mbar_init(&S.item_full[i], 1);
-      mbar_init(&S.item_empty[i], C::kSoftWarps + 2);
+      mbar_init(&S.item_empty[i], C::kSoftWarps + 2 + C::kTwoLoaders);
     }
     mbar_init(&S.pv_done, 1);
     mbar_init(&S.q_full, 1);
@@ -372,6 +389,81 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
     __syncwarp();
     if (ok && lane == 0) mbar_arrive(&S.item_empty[k & 1]);
     return ok;
+  };
+
+  // One key (or value) tile, two pages, into the kParts ring slots from position `pos` on (a
+  // position is a slot and a lap)
+  auto load_tile = [&](auto kind, const Item& it, TableWindow& w, int j, int pos, int& tails, bool& ok) {
+    constexpr bool values = decltype(kind)::value;
+    auto wait = [&](uint64_t* bar, int parity) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, p.status, p.wait_ns)) != 0;
+    };
+    if (j >> 4 > w.window) {
+      w.window = j >> 4;
+      const int pg = it.page0 + 32 * w.window + lane;
+      w.entry = pg < it.page_end ? p.table[(int64_t)it.b * p.max_pages + pg] : -1;
+    }
+    const int slot0 = __shfl_sync(0xffffffffu, w.entry, 2 * j & 31);
+    const int slot1 = __shfl_sync(0xffffffffu, w.entry, (2 * j & 31) + 1);
+    const unsigned n_slots = (unsigned)p.kv_slots;
+    const bool there0 = (unsigned)slot0 < n_slots, there1 = (unsigned)slot1 < n_slots;
+    const int n = there0 + there1;
+    const bool second = it.page0 + 2 * j + 1 < it.page_end;  // the tile has a second page
+    const int tok0 = (it.page0 + 2 * j) * kPageTokens;
+    const bool bad = !there0 || (!there1 && second);
+    if (bad && lane == 0) atomicOr(p.status, kStatusBadSlot);
+    // values whose weight is 0 must not be NaN: rows past the last token in its 16-token
+    // group (later groups are not multiplied), and pages not there
+    const bool clear = values && (bad || (tok0 + kKeys > it.len && (it.len & 15)));
+    const int y0 = (slot0 * p.H + it.h) * kPageTokens, y1 = (slot1 * p.H + it.h) * kPageTokens;
+    const CUtensorMap* map = values ? &p.vmap : &p.kmap;
+#pragma unroll
+    for (int c = 0; c < C::kParts; ++c) {
+      const int st = (pos + c) % C::kSlots, lap = (pos + c) / C::kSlots;
+      if (lap > 0) wait(&S.empty[st], lap - 1);
+      if (!ok) return;
+      uint8_t* dst = slots + st * C::kSlotBytes;
+      uint64_t* bar = clear ? &S.tail : &S.full[st];
+      if (elect_one()) {
+        if (n > 0) mbar_arrive_expect_tx(bar, n * (C::kSlotBytes / 2));
+        else mbar_arrive(bar);
+#pragma unroll
+        for (int ch = 0; ch < C::kSlotChannels; ch += 64) {
+          uint8_t* to = dst + ch / 64 * (kKeys * 128);
+          if (there0) tma_load_2d(to, map, c * C::kSlotChannels + ch, y0, bar);
+          if (there1) tma_load_2d(to + kPageTokens * 128, map, c * C::kSlotChannels + ch, y1, bar);
+        }
+      }
+      __syncwarp();
+      if (clear) {
+        wait(&S.tail, tails++);
+        constexpr int kPieces = C::kSlotChannels / 8;
+        const int piece = lane % kPieces;
+        const int end = min(kKeys, max(0, it.len - tok0));  // rows that hold tokens
+        const int last = bad ? kKeys : (end + 15) & ~15;
+        for (int r = bad ? lane / kPieces : end + lane / kPieces; r < last; r += 32 / kPieces)
+          if (r >= end || !(r < kPageTokens ? there0 : there1))
+            *reinterpret_cast<uint4*>(dst + (piece >> 3) * (kKeys * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) =
+                make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.full[st]);
+      }
+    }
+  };
+  // ring positions of key and value tile j of an item whose first position is `base`, in
+  // the order the tensor core takes them
+  auto k_pos = [&](const Item& it, int base, int j) {
+    return base + C::kParts * (C::kTiles == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1);
+  };
+  auto v_pos = [&](const Item& it, int base, int j) {
+    return base + C::kParts * (C::kTiles == 2 || j + 1 == it.nk ? 2 * j + 1 : 2 * j + 2);
+  };
+  // a loader that gave up lets its latest copies land before the block ends
+  auto land = [&](int pos) {
+    if (pos < 0) return;
+    for (int c = 0; c < C::kParts; ++c)
+      mbar_wait(&S.full[(pos + c) % C::kSlots], (pos + c) / C::kSlots & 1, p.status, p.wait_ns);
   };
 
   if (warp == C::kMma) {
@@ -511,12 +603,11 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp == C::kLoad) {
-    // -------------------------------------------- items, and their keys and values
+    // -------------------------------------------------------- items, and their keys
     const bool sorted = splits == 1 && p.n_req <= 64;
     Requests requests;
     requests.per_group = C::kTiles * per_tile;
-    int item = 0, tails = 0;
-    int st = 0, lap = 0;  // the ring slot to fill, times round the ring
+    int base = 0, pos = -1, tails = 0;  // ring positions before this item; the latest one filled
     bool ok = true;
     auto wait = [&](uint64_t* bar, int parity) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, p.status, p.wait_ns)) != 0;
@@ -569,80 +660,20 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         }
         __syncwarp();
         ++k;
-        const int page0 = it.page0, page_end = it.page_end, nk_ = it.nk, h = it.h, tok_hi = it.len;
-        const int32_t* table = p.table + (int64_t)it.b * p.max_pages;
-        int32_t near = 0, far = 0;  // table entries of this window of 16 key tiles, and of the one before
-        int window = -1;
-        const int n_slots = (int)p.kv_slots, H = p.H;
-        // one key (or value) tile: two pages, kParts slots
-        auto load = [&](int j, bool values) {
-          if (j >> 4 > window) {
-            window = j >> 4;
-            far = near;
-            const int pg = page0 + 32 * window + lane;
-            near = pg < page_end ? table[pg] : -1;
+        TableWindow w, w2;  // with one row tile the keys are one tile ahead
+        for (int j = 0; j < it.nk && ok; ++j) {
+          if (j + 4 == it.nk) ask();
+          if (C::kTwoLoaders) {
+            pos = k_pos(it, base, j);
+            load_tile(Keys{}, it, w, j, pos, tails, ok);
+            continue;
           }
-          const int32_t from = j >> 4 == window ? near : far;
-          const int slot0 = __shfl_sync(0xffffffffu, from, 2 * j & 31), slot1 = __shfl_sync(0xffffffffu, from, (2 * j & 31) + 1);
-          const bool there0 = (unsigned)slot0 < (unsigned)n_slots, there1 = (unsigned)slot1 < (unsigned)n_slots;
-          const int n = there0 + there1;
-          const bool second = page0 + 2 * j + 1 < page_end;  // the tile has a second page
-          const int tok0 = (page0 + 2 * j) * kPageTokens;
-          const bool bad = !there0 || (!there1 && second);
-          if (bad && lane == 0) atomicOr(p.status, kStatusBadSlot);
-          // values whose weight is 0 must not be NaN: rows past the last token in its
-          // 16-token group (later groups are not multiplied), and pages not there
-          const bool clear = values && (bad || (tok0 + kKeys > tok_hi && (tok_hi & 15)));
-          const int y0 = (slot0 * H + h) * kPageTokens, y1 = (slot1 * H + h) * kPageTokens;
-#pragma unroll
-          for (int c = 0; c < C::kParts; ++c) {
-            if (lap > 0) wait(&S.empty[st], lap - 1);
-            if (!ok) break;
-            uint8_t* dst = slots + st * C::kSlotBytes;
-            uint64_t* bar = clear ? &S.tail : &S.full[st];
-            const CUtensorMap* map = values ? &p.vmap : &p.kmap;
-            if (elect_one()) {
-              if (n > 0) mbar_arrive_expect_tx(bar, n * (C::kSlotBytes / 2));
-              else mbar_arrive(bar);
-#pragma unroll
-              for (int ch = 0; ch < C::kSlotChannels; ch += 64) {
-                uint8_t* to = dst + ch / 64 * (kKeys * 128);
-                if (there0) tma_load_2d(to, map, c * C::kSlotChannels + ch, y0, bar);
-                if (there1) tma_load_2d(to + kPageTokens * 128, map, c * C::kSlotChannels + ch, y1, bar);
-              }
-            }
-            __syncwarp();
-            if (clear) {
-              wait(&S.tail, tails++);
-              constexpr int kPieces = C::kSlotChannels / 8;
-              const int piece = lane % kPieces;
-              const int end = min(kKeys, max(0, tok_hi - tok0));  // rows that hold tokens
-              const int last = bad ? kKeys : (end + 15) & ~15;
-              for (int r = bad ? lane / kPieces : end + lane / kPieces; r < last; r += 32 / kPieces)
-                if (r >= end || !(r < kPageTokens ? there0 : there1))
-                  *reinterpret_cast<uint4*>(dst + (piece >> 3) * (kKeys * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) =
-                      make_uint4(0, 0, 0, 0);
-              fence_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&S.full[st]);
-            }
-            ++item;
-            if (++st == C::kSlots) {
-              st = 0;
-              ++lap;
-            }
-          }
-        };
-        for (int j = 0; j < nk_ && ok; ++j) {
-          if (j + 4 == nk_) ask();
-          if (C::kTiles == 2) {
-            load(j, false);
-          } else {
-            if (j == 0) load(0, false);
-            if (j + 1 < nk_) load(j + 1, false);
-          }
-          load(j, true);
+          if (C::kTiles == 2 || j == 0) load_tile(Keys{}, it, w, j, k_pos(it, base, j), tails, ok);
+          if (C::kTiles == 1 && j + 1 < it.nk) load_tile(Keys{}, it, w2, j + 1, k_pos(it, base, j + 1), tails, ok);
+          pos = v_pos(it, base, j);
+          load_tile(Values{}, it, w, j, pos, tails, ok);
         }
+        base += 2 * C::kParts * it.nk;
       }
       if (open) ask();
       wait(&S.taken, asked);
@@ -659,11 +690,25 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         break;
       }
     }
-    if (!ok) {  // let what is in flight land before the block ends
+    if (!ok) {
       mbar_wait(&S.taken, asked & 1, p.status, p.wait_ns);
-      for (int i = max(0, item - C::kSlots); i < item; ++i)
-        mbar_wait(&S.full[i % C::kSlots], (i / C::kSlots) & 1, p.status, p.wait_ns);
+      land(pos);
     }
+    __syncwarp();
+  } else if (C::kTwoLoaders && warp == C::kValues) {
+    // ------------------------------------------------------------------ values
+    int base = 0, pos = -1, tails = 0;
+    bool ok = true;
+    Item it;
+    for (int k = 0; ok && next_item(k, it) && it.id >= 0; ++k) {
+      TableWindow w;
+      for (int j = 0; j < it.nk && ok; ++j) {
+        pos = v_pos(it, base, j);
+        load_tile(Values{}, it, w, j, pos, tails, ok);
+      }
+      base += 2 * C::kParts * it.nk;
+    }
+    if (!ok) land(pos);
     __syncwarp();
   } else if (warp == C::kQuery) {
     // ----------------------------------------------------------------- queries
