@@ -158,9 +158,10 @@ def test_no_queries():
     run([0, 0], [100, 5], 1, 1, 64, "bf16")
 
 
-def test_many_requests():
-    lens, nq = [(i * 37) % 100 for i in range(1000)], [(i * 13) % 5 for i in range(1000)]
-    run(nq, lens, 1, 1, 64, "bf16", seed=9)
+@pytest.mark.parametrize("n,most,queries", [(1000, 100, 5), (200, 250, 3), (100, 500, 2), (70, 600, 90), (65, 3000, 40)])
+def test_many_requests(n, most, queries):
+    """Row tiles and 16-row units, their requests sorted, numbered by a warp, by the block."""
+    run([(i * 13) % queries for i in range(n)], [(i * 37) % most for i in range(n)], 1, 1, 64, "bf16", seed=9)
 
 
 @pytest.mark.parametrize("nq", [[9, 5], [400, 300]])

@@ -114,14 +114,17 @@ def test_bad_lengths_are_clamped():
     assert tpk.get_device_status(reset=True) == (4, 1)
 
 
-def test_many_requests():
-    lens = [(i * 37) % 150 for i in range(4096)]
-    pg = Pages(lens, 1, 64, "bf16", 9)
+@pytest.mark.parametrize("n,most,max_pages", [(4096, 150, None), (129, 2000, None), (300, 130, 40), (600, 60, 33),
+                                              (130, 1500, 32), (128, 900, 33)])
+def test_many_requests(n, most, max_pages):
+    """Whole and split histories, numbered by a warp and by the block."""
+    lens = [(i * 37 + i // 7) % most for i in range(n)]
+    pg = Pages(lens, 1, 64, "bf16", 9, max_pages=max_pages)
     d = Decode(pg, 2)
     d.call()
     torch.cuda.synchronize()
     o, lse = d.o.cpu(), d.lse.cpu()
-    for b in list(range(0, 4096, 97)) + [0, 4095]:
+    for b in list(range(0, n, 97 if n > 1000 else 11)) + [0, n - 1]:
         want = attention(d.q[b].double().view(2, 64), pg.keys[b][:, 0], pg.values[b][:, 0],
                          torch.ones(2, lens[b], dtype=torch.bool), d.scale)
         check_attention(o[b].view(2, 64), lse[b], want, 64, lens[b], pg.dtype, what=f"request {b}")

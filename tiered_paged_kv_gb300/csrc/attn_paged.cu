@@ -725,12 +725,17 @@ static cudaError_t launch_dim(const PagedParams& p, int D, cudaStream_t stream) 
                                                             : launch_rows<T, 256>(p, stream);
 }
 
-// Histories of at most this many pages are not split: a block per run walks its pages
-// in less time than the numbering and the join take.
-constexpr int kWholePages = 8;
+// Short histories are not split: a block per run walks its pages in less time than the
+// numbering and the join take (one request of 4 pages, 8 x 8 heads of 128: 6.4 us whole, 9.4
+// split; of 8: 8.9 and 9.4; of 12: 11.0 and 9.5).  With a run for every SM the device is
+// busy either way, and splitting only costs (16 requests of 32 pages: 26.5 and 31.9); but
+// the lengths are not known here, and one long history among short ones must not be left
+// to one block for longer than that.
+constexpr int kWholePages = 8, kWholePagesBusy = 32, kBusyRuns = 128;
 
 cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream) {
-  p.whole = !p.q_off && p.max_pages <= kWholePages;
+  const int64_t runs = (int64_t)p.n_req * p.H * ((p.G + kRowTile - 1) / kRowTile);
+  p.whole = !p.q_off && p.max_pages <= (runs >= kBusyRuns ? kWholePagesBusy : kWholePages);
   return dtype == 0 ? launch_dim<Bf16>(p, D, stream) : launch_dim<F16>(p, D, stream);
 }
 
