@@ -130,3 +130,37 @@ def test_tables_model():
     table, free = [[0, -1], [1, -1]], [2, -1]
     n_free, length, granted, off, slot, pos, req = tables_model([64, 64], [65, 65], table, free, 1, 4)
     assert granted == [1, 0] and length == [65, 64] and slot == [128, -1, -1, -1] and n_free == 0
+
+
+def test_python_calls_marshal_and_refuse():
+    """The C module's conversions: pointers from ints, None and data_ptr(), errors as
+    exceptions, statuses as TpkError."""
+    class Ptr:
+        def data_ptr(self):
+            return 16
+
+    class Stream:
+        cuda_stream = 0
+
+    s = shape(head_dim=64, group=1, kv_heads=1)
+    x = Ptr()
+    axis = np.zeros(32, np.uint8)
+    good = dict(shape=s, n_tokens=0, q=x, q_stride=64, k=x, k_stride=64, v=x, v_stride=64, positions=x, n_axes=1,
+                axis_of=axis, inv_freq=x, rot_dim=64, interleaved=False, slot_map=x, q_out=x, q_out_stride=64, k_pool=x,
+                v_pool=16, stream=Stream())
+    tpk.kv_rope_append(**good)
+    tpk.kv_rope_append(**{**good, "axis_of": None, "stream": None})
+    tpk.kv_rope_append(**{**good, "axis_of": axis.tobytes(), "stream": 0})
+    for kw, exc in [({"q": "text"}, TypeError), ({"q": 1.5}, TypeError), ({"n_tokens": 1 << 40}, OverflowError),
+                    ({"q_stride": "64"}, TypeError), ({"shape": None}, tpk.TpkError), ({"shape": b"short"}, ValueError),
+                    ({"axis_of": axis[:31]}, ValueError), ({"axis_of": np.zeros(32, np.int32)}, ValueError),
+                    ({"stream": "s"}, AttributeError), ({"rot_dim": 8}, ValueError), ({"k": None}, tpk.TpkError),
+                    ({"q": -1}, Exception)]:
+        with pytest.raises(exc):
+            tpk.kv_rope_append(**{**good, **kw})
+    with pytest.raises(tpk.TpkError, match="n_req"):
+        tpk.decode_attn_paged(shape(), 0, x, 4096, x, x, x, x, None, x, 4096, False, x, x, BIG)
+    with pytest.raises(tpk.TpkError, match="workspace"):
+        tpk.cross_attn_paged(shape(), 1, 1, x, 4096, x, x, x, x, x, None, x, 4096, x, x, -1)
+    with pytest.raises(tpk.TpkError, match="n_req"):
+        tpk.kv_tables_update(0, 4, x, x, x, x, 8, x, x, x, x, x, x, x, x, 10)

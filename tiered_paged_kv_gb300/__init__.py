@@ -5,11 +5,15 @@ function here only marshals arguments: device buffers are passed as raw
 pointers (torch tensors are accepted and their ``data_ptr()`` is used), streams
 as ``torch.cuda.Stream`` or raw handles.  All computation runs in the library's
 CUDA kernels; there is no CPU fallback, and loading fails loudly when the
-library has not been built.
+library has not been built.  The calls of a serving step (kv_tables_update and
+those after it) go through a small C module (``csrc/binding.c``) instead of ctypes,
+whose conversions would take longer than their kernels.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import numpy as np
@@ -281,30 +285,47 @@ def hybrid_plan(shape, n_exact_tokens, n_int8_pages, resident_blocks=0):
     return se, s8, units.value
 
 
+_call = None
+
+
+def _calls():
+    """Load the C module of the serving step's calls (raises if it has not been built)."""
+    global _call
+    if _call is None:
+        lib()
+        path = _build_mod.CALL
+        if not os.path.exists(path):
+            raise RuntimeError(f"_tpk_call.so not built ({path}); run tiered_paged_kv_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_tpk_call", path)
+        spec = importlib.util.spec_from_file_location("_tpk_call", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _call = module
+    return _call
+
+
 def kv_tables_update(n_req, max_pages, len_old, len_new, page_table, free_slots, free_cap, n_free_in, n_free_out,
                      len_out, granted, tok_off, slot_map, positions, token_req, max_tokens, stream=None):
     """Page tables and slot maps on the GPU from old and new request lengths (see
     tpk_kv_tables_update); every array is a device buffer."""
-    _check(lib().tpk_kv_tables_update(n_req, max_pages, _ptr(len_old), _ptr(len_new), _ptr(page_table),
-                                      _ptr(free_slots), free_cap, _ptr(n_free_in), _ptr(n_free_out), _ptr(len_out),
-                                      _ptr(granted), _ptr(tok_off), _ptr(slot_map), _ptr(positions), _ptr(token_req),
-                                      max_tokens, _stream(stream)))
+    st = (_call or _calls()).kv_tables_update(n_req, max_pages, len_old, len_new, page_table, free_slots, free_cap,
+                                              n_free_in, n_free_out, len_out, granted, tok_off, slot_map, positions,
+                                              token_req, max_tokens, stream)
+    if st:
+        _check(st)
 
 
 def kv_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, positions, n_axes, axis_of, inv_freq,
                    rot_dim, interleaved, slot_map, q_out, q_out_stride, k_pool, v_pool, stream=None):
     """Rotate q and k at positions of up to four axes and store k and v into their
-    pages (see tpk_kv_rope_append).  axis_of is a host array of rot_dim / 2 axis
-    numbers (None: axis 0); q and q_out, or k, v and the pools, may be None."""
-    if axis_of is not None:
-        axis_of = np.asarray(axis_of, np.uint8).tobytes()
-        if len(axis_of) != rot_dim // 2:
-            raise ValueError(f"axis_of has {len(axis_of)} entries, not {rot_dim // 2}")
-    _check(lib().tpk_kv_rope_append(ctypes.byref(shape), n_tokens, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
-                                    v_stride, _ptr(positions), n_axes,
-                                    axis_of, _ptr(inv_freq), rot_dim,
-                                    int(interleaved), _ptr(slot_map), _ptr(q_out), q_out_stride, _ptr(k_pool),
-                                    _ptr(v_pool), _stream(stream)))
+    pages (see tpk_kv_rope_append).  axis_of is a host uint8 array (or bytes) of
+    rot_dim / 2 axis numbers (None: axis 0); q and q_out, or k, v and the pools, may be
+    None."""
+    st = (_call or _calls()).kv_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, positions, n_axes,
+                                            axis_of, inv_freq, rot_dim, interleaved, slot_map, q_out, q_out_stride,
+                                            k_pool, v_pool, stream)
+    if st:
+        _check(st)
 
 
 def decode_paged_workspace_bytes(shape, n_req):
@@ -315,9 +336,10 @@ def decode_attn_paged(shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_t
                       lse, ws, ws_bytes, stream=None):
     """One new token per request over a paged cache whose lengths are device arrays
     (see tpk_decode_attn_paged)."""
-    _check(lib().tpk_decode_attn_paged(ctypes.byref(shape), n_req, _ptr(q), q_stride, _ptr(k_pool), _ptr(v_pool),
-                                       _ptr(page_table), _ptr(n_tokens), _ptr(tok_begin), _ptr(o), o_stride,
-                                       int(o_f32), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
+    st = (_call or _calls()).decode_attn_paged(shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens,
+                                               tok_begin, o, o_stride, o_f32, lse, ws, ws_bytes, stream)
+    if st:
+        _check(st)
 
 
 def cross_paged_workspace_bytes(shape, n_req, n_q):
@@ -328,9 +350,10 @@ def cross_attn_paged(shape, n_req, n_q, q, q_stride, q_off, k_pool, v_pool, page
                      o_stride, lse, ws, ws_bytes, stream=None):
     """Ragged query tokens over paged states of another length (see
     tpk_cross_attn_paged)."""
-    _check(lib().tpk_cross_attn_paged(ctypes.byref(shape), n_req, n_q, _ptr(q), q_stride, _ptr(q_off), _ptr(k_pool),
-                                      _ptr(v_pool), _ptr(page_table), _ptr(n_tokens), _ptr(kv_range), _ptr(o),
-                                      o_stride, _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
+    st = (_call or _calls()).cross_attn_paged(shape, n_req, n_q, q, q_stride, q_off, k_pool, v_pool, page_table,
+                                              n_tokens, kv_range, o, o_stride, lse, ws, ws_bytes, stream)
+    if st:
+        _check(st)
 
 
 def set_decode_timing_events(before=None, after=None):

@@ -1,7 +1,8 @@
 """Build the tpk CUDA library (libtpk.so) for sm_103a with nvcc.
 
 Each translation unit is compiled in parallel, then linked into one shared
-library under ``_build/``.  No GPU is needed to build.
+library under ``_build/``, beside it the small C module that marshals the serving
+step's calls for Python (gcc).  No GPU is needed to build.
 """
 from __future__ import annotations
 
@@ -9,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libtpk.so")
+CALL = os.path.join(OUT_DIR, "_tpk_call.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -77,7 +80,21 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_call(force)
     return LIB
+
+
+def _build_call(force: bool) -> None:
+    src = os.path.join(CSRC, "binding.c")
+    if not force and not _stale(CALL, [src, LIB] + headers()):
+        return
+    tmp = CALL + f".tmp{os.getpid()}"
+    cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_path("include"), "-I", INCLUDE,
+           src, "-o", tmp, "-L", OUT_DIR, "-ltpk", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for binding.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
 
 
 if __name__ == "__main__":
