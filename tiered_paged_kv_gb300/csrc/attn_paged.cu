@@ -21,6 +21,10 @@
 // at most 8 query rows the planes are the two halves of one 16-row operand and cost
 // nothing.  A tensor tile of 128 rows would hold 8 or 16 useful ones; the few rows make
 // the kernel bound by HBM (4 H D bytes per attended token against 4 H G D operations).
+//
+// Measured: 16 requests of 32,000 tokens at head sizes 64, 128, 256: 6.5, 6.8, 6.8 TB/s; one
+// request of 131,072 tokens (4 x 8 heads of 256, 537 MB) 88.9 us, 6.0 TB/s; one of 200 tokens
+// 9.3 us.
 #include "paged.cuh"
 
 namespace tpk {

@@ -12,7 +12,8 @@
 // 16 channels copied; two 16-byte loads and stores -- so all index arithmetic is done
 // once, and passes over the block's tokens, four in flight.  The tokens' angles go to
 // shared memory once per block and serve every head.  Bound: HBM, (2 HQ + 4 H) D * 2
-// bytes per token.
+// bytes per token.  Measured: 8,200 tokens of 32 + 8 heads of 128 (202 MB) 36.5 us, 5.5
+// TB/s; 16 tokens of 32 + 4 heads of 256 2.5 us.
 #include "paged.cuh"
 
 namespace tpk {
