@@ -15,23 +15,22 @@
 // Within a block a producer warp walks the range and feeds a ring of page stages by TMA
 // (64 tokens of keys and of values, 128-byte swizzle); four consumer warps take 16 of
 // the 64 tokens each and keep their own online softmax, joined when a run ends.  Both
-// products run on mma.sync m16n8k16 with float32 accumulators.  The weights enter PV
-// as two 16-bit planes (the rounded weight and what the rounding left, about 16 bits in
-// bfloat16), so they add no error of their own next to the rounding of the output; with
-// at most 8 query rows the planes are the two halves of one 16-row operand and cost
-// nothing.  A tensor tile of 128 rows would hold 8 or 16 useful ones; the few rows make
-// the kernel bound by HBM (4 H D bytes per attended token against 4 H G D operations).
+// products run on mma.sync m16n8k16 with float32 accumulators (struct Rows).  The weights
+// enter PV as two 16-bit planes (the rounded weight and what the rounding left, about 16
+// bits in bfloat16), so they add no error of their own next to the rounding of the output.
+// A tensor tile of 128 rows would hold 8 or 16 useful ones; the few rows make the kernel
+// bound by HBM (4 H D bytes per attended token against 4 H G D operations).
 //
-// Measured: 16 requests of 32,000 tokens at head sizes 64, 128, 256: 6.5, 6.8, 6.8 TB/s; one
-// request of 131,072 tokens (4 x 8 heads of 256, 537 MB) 88.9 us, 6.0 TB/s; one of 200 tokens
-// 9.3 us.
+// Measured: 16 requests of 32,000 tokens at head sizes 64, 128, 256: 6.8, 6.9, 6.9 TB/s; one
+// request of 131,072 tokens (4 x 8 heads of 256, 537 MB) 86 us, 6.2 TB/s; one of 200 tokens
+// 7.6 us.
 #include "paged.cuh"
 
 namespace tpk {
 
+constexpr float kEmpty = -__builtin_huge_valf();
 constexpr int kConsumers = 4;
 constexpr int kPagedThreads = (kConsumers + 1) * 32;
-constexpr float kEmpty = -__builtin_huge_valf();
 
 template <int D>
 struct SplitCfg {
@@ -39,8 +38,11 @@ struct SplitCfg {
   static constexpr int kStageBytes = 2 * kPageBytes;
   static constexpr int kStages = D == 64 ? 4 : 3;
   static constexpr int kBlocksPerSm = D == 256 ? 1 : D == 128 ? 2 : 3;
-  static constexpr int kRowStride = 64 + 8;  // floats: spreads the rows of the joined o over the banks
-  static constexpr int kJoinBytes = kConsumers * 8 * kRowStride * 4;
+  static constexpr int kJoin = D == 256 ? 256 : 64;  // channels joined at a time
+  // floats a row, which spread the 8 rows (or the 4 lanes' row pairs) over the banks
+  template <bool kSmall>
+  static constexpr int kJoinStride = kJoin + (kSmall ? 4 : 8);
+  static constexpr int kJoinBytes = kConsumers * 8 * kJoinStride<false> * 4;
   static constexpr int kSharedBytes = 768;  // SplitShared
   static constexpr int kSmem = kStages * kStageBytes + kJoinBytes + kSharedBytes;
   // shared memory of an SM, less what each block takes besides
@@ -166,16 +168,210 @@ __device__ __forceinline__ void store_pair(const PagedParams& p, int64_t row, in
 // Row r of a run: its query token and query head; false past the run's last row.
 __device__ __forceinline__ bool run_row(const PagedParams& p, int first, int count, int h, int tile, int r, int& token,
                                         int& head) {
-  const int64_t i = (int64_t)tile * kRowTile + r;
-  if (i >= (int64_t)count * p.G) return false;
-  const int t = (int)(i / p.G);
-  token = first + t;
-  head = h * p.G + (int)(i - (int64_t)t * p.G);
+  // 32 bits do: 2^32 rows would be 512 GB of output
+  const uint32_t i = (uint32_t)tile * kRowTile + r;
+  if (i >= (uint32_t)count * (uint32_t)p.G) return false;
+  const uint32_t t = i / (uint32_t)p.G;
+  token = first + (int)t;
+  head = h * p.G + (int)(i - t * (uint32_t)p.G);
   return true;
 }
 
-template <typename T, int D, bool kSmall>  // kSmall: runs have at most 8 rows
-__global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_constant__ PagedParams p) {
+// One warp's share of a run, as 32 lanes (g, t) = (lane / 4, lane % 4) hold it: every lane has
+// two of the run's rows, row(0) and row(1), and of those some tokens' scores and some
+// channels' output.
+// Up to 8 rows are the narrow side of m16n8k16: S^T = K Q^T (16 tokens x 8 rows; rows 2t and
+// 2t + 1), O^T += V^T P^T (16 channels x 8 rows), P^T being S^T transposed in registers.  A
+// third fewer steps than 8 rows of 16, and half the accumulators: 400 requests of 200 to 300
+// tokens, 8 heads of 256: 171 us (207 as the wide side); one of 200 tokens 7.6 (9.0).
+// Up to 16 rows are the wide side: S = Q K^T, O += P V, rows g and g + 8; as two narrow tiles
+// 96 requests of 1000 tokens, 8 heads of 128, take 77 us instead of 73.
+template <typename T, int D, bool kSmall>
+struct Rows {
+  static constexpr int kAcc = kSmall ? D / 16 : D / 8;
+  uint32_t q[D / 16][kSmall ? 2 : 4];
+  int see_lo[2], see_hi[2];  // the tokens each row sees
+  float acc[kAcc][4];
+  float m[2], l[2];  // l: of this lane's tokens
+  int g, t, r8, i8;  // r8, i8: row r8 of matrix i8 in ldmatrix
+
+  __device__ __forceinline__ explicit Rows(int lane) : g(lane >> 2), t(lane & 3), r8(lane & 7), i8(lane >> 3) {}
+  __device__ __forceinline__ int row(int e) const { return kSmall ? 2 * t + e : g + 8 * e; }
+  // Joins x over the lanes that share this lane's rows.
+  template <typename F>
+  __device__ __forceinline__ static float over_lanes(float x, F f) {
+#pragma unroll
+    for (int d = kSmall ? 4 : 1; d < (kSmall ? 32 : 4); d <<= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+  }
+
+  __device__ __forceinline__ void start(const PagedParams& p, int first, int count, int h, int tile, int tok_lo,
+                                        int tok_hi) {
+    int token, head;
+#pragma unroll
+    for (int e = 0; e < (kSmall ? 1 : 2); ++e) {
+      const bool live = run_row(p, first, count, h, tile, g + 8 * e, token, head);
+      const uint32_t* src =
+          reinterpret_cast<const uint32_t*>(p.q + (live ? (int64_t)token * p.q_stride + (int64_t)head * D : 0));
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][e] = live ? src[8 * k + t] : 0;
+        q[k][e + (kSmall ? 1 : 2)] = live ? src[8 * k + t + 4] : 0;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const bool live = run_row(p, first, count, h, tile, row(e), token, head);
+      see_lo[e] = tok_lo;
+      see_hi[e] = live ? tok_hi : tok_lo;
+      if (live && p.range) {
+        see_lo[e] = max(tok_lo, p.range[2 * (int64_t)token]);
+        see_hi[e] = min(tok_hi, p.range[2 * (int64_t)token + 1]);
+      }
+      m[e] = kEmpty;
+      l[e] = 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < kAcc; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
+  }
+
+  // Folds in 16 tokens from tok0 on, whose keys and values start at ks and vs.
+  __device__ __forceinline__ void tokens(const PagedParams& p, uint32_t ks, uint32_t vs, int tok0) {
+    // ---- scores, two chains of matrix steps a tile
+    constexpr int kTiles = kSmall ? 1 : 2;  // of 8 tokens, in the wide form
+    float sc[kTiles][2][4];
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][x][e] = 0.f;
+    const int k_half = kSmall ? i8 & 1 : i8 >> 1, k_piece = kSmall ? i8 >> 1 : i8 & 1;
+    const uint32_t krow = ks + (k_half * 8 + r8) * 128;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t kf[4];
+      const int c = 2 * k + k_piece;  // 16-byte piece of the row
+      ldmatrix_x4(kf, krow + (c >> 3) * 8192 + (((c & 7) ^ r8) << 4));
+      if constexpr (kSmall) {
+        T::mma(sc[0][k & 1], kf, q[k][0], q[k][1]);
+      } else {
+        T::mma(sc[0][k & 1], q[k], kf[0], kf[1]);
+        T::mma(sc[1][k & 1], q[k], kf[2], kf[3]);
+      }
+    }
+    // ---- online softmax in base 2, each row for itself
+    constexpr int kMine = kSmall ? 2 : 4;  // tokens of a row in this lane
+    float x[2][kMine];
+    bool grows = false;  // beyond the maximum so far
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int y = 0; y < kMine; ++y) {
+        const int tok = tok0 + (kSmall ? g + 8 * y : 8 * (y >> 1) + 2 * t + (y & 1));
+        const int n = kSmall ? 0 : y >> 1, at = kSmall ? 2 * y + e : 2 * e + (y & 1);
+        const bool seen = tok >= see_lo[e] && tok < see_hi[e];
+        x[e][y] = seen ? (sc[n][0][at] + sc[n][1][at]) * p.qscale : kEmpty;
+        grows = grows || x[e][y] > m[e];
+      }
+    // Three steps over 8 lanes wait for the vote, two over 4 do not.
+    const bool scaled = __any_sync(0xffffffffu, grows);
+    float scale[2];
+    if (!kSmall || scaled) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = m[e];
+#pragma unroll
+        for (int y = 0; y < kMine; ++y) top = fmaxf(top, x[e][y]);
+        top = over_lanes(top, [](float a, float b) { return fmaxf(a, b); });
+        scale[e] = m[e] == kEmpty ? 0.f : exp2f(m[e] - top);
+        m[e] = top;
+        l[e] *= scale[e];
+      }
+    }
+    if (scaled) {
+#pragma unroll
+      for (int c = 0; c < kAcc; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[c][e] *= scale[kSmall ? e & 1 : e >> 1];
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float ref = m[e] == kEmpty ? 0.f : m[e];
+      float sum = 0.f;
+#pragma unroll
+      for (int y = 0; y < kMine; ++y) {
+        x[e][y] = exp2f(x[e][y] - ref);
+        sum += x[e][y];
+      }
+      l[e] += sum;
+    }
+    // ---- o += weights * values, in two planes: the rounded weights, and what that left
+    uint32_t hi[4], lw[4];
+#pragma unroll
+    for (int i = 0; i < (kSmall ? 2 : 4); ++i) {
+      float a, b;
+      if constexpr (kSmall) {
+        a = x[0][i];
+        b = x[1][i];
+      } else {
+        a = x[i & 1][i & 2];
+        b = x[i & 1][(i & 2) + 1];
+      }
+      hi[i] = T::pack(a, b);
+      const float2 back = T::unpack(hi[i]);
+      lw[i] = T::pack(a - back.x, b - back.y);
+      if constexpr (kSmall) {
+        hi[i] = transpose8(hi[i]);
+        lw[i] = transpose8(lw[i]);
+      }
+    }
+    const int v_half = kSmall ? i8 >> 1 : i8 & 1, v_piece = kSmall ? i8 & 1 : i8 >> 1;
+    const uint32_t vrow = vs + (v_half * 8 + r8) * 128;
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) {
+      uint32_t vf[4];
+      const int c = 2 * n + v_piece;
+      ldmatrix_x4_trans(vf, vrow + (c >> 3) * 8192 + (((c & 7) ^ r8) << 4));
+      if constexpr (kSmall) {
+        T::mma(acc[n], vf, hi[0], hi[1]);
+        T::mma(acc[n], vf, lw[0], lw[1]);
+      } else {
+        T::mma(acc[2 * n], hi, vf[0], vf[1]);
+        T::mma(acc[2 * n + 1], hi, vf[2], vf[3]);
+        T::mma(acc[2 * n], lw, vf[0], vf[1]);
+        T::mma(acc[2 * n + 1], lw, vf[2], vf[3]);
+      }
+    }
+  }
+
+  // Puts kJoin channels from c0 on, scaled, into `to` (8 rows of `stride` floats): the run's
+  // rows 8 pass .. 8 pass + 7.
+  template <int kJoin>
+  __device__ __forceinline__ void put(float* to, int stride, int c0, int pass, const float (&f)[2]) const {
+    if constexpr (kSmall) {
+#pragma unroll
+      for (int c = 0; c < kJoin / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          to[(2 * t + (e & 1)) * stride + 16 * c + 8 * (e >> 1) + g] = acc[c0 / 16 + c][e] * f[e & 1];
+    } else {
+#pragma unroll
+      for (int c = 0; c < kJoin / 8; ++c)
+        *reinterpret_cast<float2*>(to + g * stride + 8 * c + 2 * t) =
+            make_float2(acc[c0 / 8 + c][2 * pass] * f[pass], acc[c0 / 8 + c][2 * pass + 1] * f[pass]);
+    }
+  }
+};
+
+// The second bound asks for the registers of kBlocksPerSm blocks.  In the wide form at
+// D = 128 two fit without it (167 registers); with it the compiler spills (96 requests of
+// 1000 tokens, 16 rows: 73 us without, 80 with; asking for one block, which takes 214, 91).
+template <typename T, int D, bool kSmall>
+__global__ void __launch_bounds__(kPagedThreads, D == 256 ? 1 : D == 64 ? 3 : kSmall ? 2 : 0)
+    split_kernel(const __grid_constant__ PagedParams p) {
   using C = SplitCfg<D>;
   extern __shared__ __align__(1024) uint8_t stages[];
   float* join = reinterpret_cast<float*>(stages + C::kStages * C::kStageBytes);
@@ -310,7 +506,7 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
               break;
             }
           }
-          if (lane == 0) {
+          if (elect_one()) {
             const bool ok = slot >= 0 && slot < p.kv_slots;
             S.valid[st] = ok;
             if (ok) {
@@ -338,45 +534,16 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
   }
 
   // --------------------------------------------------------------- consumers
-  // Thread (g, t) = (lane / 4, lane % 4) owns query row g (and g + 8), and of each
-  // 8-token (8-channel) tile tokens (channels) 2t and 2t + 1.
-  const int g = lane >> 2, t = lane & 3;
-  const int r8 = lane & 7, i8 = lane >> 3;  // ldmatrix: row r8 of matrix i8
+  Rows<T, D, kSmall> rows(lane);
   bool dead = false;
-  int item = 0;
+  int item = 0;  // pages of this block so far
   while (walk.next(p, s)) {
     int first, count, tok_lo, tok_hi;
     request_rows(p, s.b, first, count);
     request_span(p, s.b, tok_lo, tok_hi);
     const int tiles = request_runs(p, s.b) / p.H;
     const int h = s.run / tiles, tile = s.run - h * tiles;
-    // ---- the query rows as A operands, and the tokens each row sees
-    uint32_t q[D / 16][kSmall ? 2 : 4];
-    int see_lo[2], see_hi[2];
-#pragma unroll
-    for (int half = 0; half < (kSmall ? 1 : 2); ++half) {
-      int token, head;
-      const bool live = run_row(p, first, count, h, tile, g + 8 * half, token, head);
-      see_lo[half] = tok_lo;
-      see_hi[half] = live ? tok_hi : tok_lo;
-      if (live && p.range) {
-        see_lo[half] = max(tok_lo, p.range[2 * (int64_t)token]);
-        see_hi[half] = min(tok_hi, p.range[2 * (int64_t)token + 1]);
-      }
-      const uint32_t* src =
-          reinterpret_cast<const uint32_t*>(p.q + (live ? (int64_t)token * p.q_stride + (int64_t)head * D : 0));
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        q[k][half] = live ? src[8 * k + t] : 0;
-        q[k][half + (kSmall ? 1 : 2)] = live ? src[8 * k + t + 4] : 0;
-      }
-    }
-    float acc[D / 8][4];
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-    float m[2] = {kEmpty, kEmpty}, l[2] = {0.f, 0.f};
+    rows.start(p, first, count, h, tile, tok_lo, tok_hi);
 
     for (int j = 0; j < s.count; ++j, ++item) {
       const int st = item % C::kStages;
@@ -385,146 +552,52 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
         dead = !__all_sync(0xffffffffu, ok);
       }
       if (!dead && S.valid[st]) {
-        uint8_t* ks = stages + st * C::kStageBytes;
+        uint8_t* ks = stages + st * C::kStageBytes + warp * 16 * 128;
         uint8_t* vs = ks + C::kPageBytes;
         const int tok0 = (s.page0 + s.page + j) * kPageTokens + warp * 16;  // this warp's first token
         // rows outside the request's span may hold NaN: their weight is 0, their
         // values are cleared
         if (tok0 < tok_lo || tok0 + 16 > tok_hi) {
-          for (int i = lane; i < 16 * (D / 8); i += 32) {
-            const int r = i / (D / 8), c = i % (D / 8);
+          for (int x = lane; x < 16 * (D / 8); x += 32) {
+            const int r = x / (D / 8), c = x % (D / 8);
             if (tok0 + r < tok_lo || tok0 + r >= tok_hi)
-              *reinterpret_cast<uint4*>(vs + (c >> 3) * 8192 + (warp * 16 + r) * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+              *reinterpret_cast<uint4*>(vs + (c >> 3) * 8192 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
                   make_uint4(0, 0, 0, 0);
           }
           fence_async_smem();  // the stage is filled by TMA again later
           __syncwarp();
         }
-        // ---- scores of 16 tokens: two 8-token tiles, two chains each
-        float sc[2][2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[n][x][e] = 0.f;
-        const uint32_t krow = smem_u32(ks) + (warp * 16 + (i8 >> 1) * 8 + r8) * 128;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t kb[4], a[4];
-          const int c = 2 * k + (i8 & 1);  // 16-byte piece of the row
-          ldmatrix_x4(kb, krow + (c >> 3) * 8192 + (((c & 7) ^ r8) << 4));
-          a[0] = q[k][0];
-          a[1] = kSmall ? 0 : q[k][1];
-          a[2] = q[k][kSmall ? 1 : 2];
-          a[3] = kSmall ? 0 : q[k][3];
-          T::mma(sc[0][k & 1], a, kb[0], kb[1]);
-          T::mma(sc[1][k & 1], a, kb[2], kb[3]);
-        }
-        // ---- online softmax in base 2
-        uint32_t hi[2][2], lw[2][2];  // [row half][token tile]: rounded weights, and what that left
-        float scale[2];
-        bool same = true;
-#pragma unroll
-        for (int half = 0; half < (kSmall ? 1 : 2); ++half) {
-          float x[4];
-          float top = kEmpty;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int n = e >> 1, w = 2 * half + (e & 1);
-            const int tok = tok0 + 8 * n + 2 * t + (e & 1);
-            const bool seen = tok >= see_lo[half] && tok < see_hi[half];
-            x[e] = seen ? (sc[n][0][w] + sc[n][1][w]) * p.qscale : kEmpty;
-            top = fmaxf(top, x[e]);
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float mn = fmaxf(m[half], top);
-          const float ref = mn == kEmpty ? 0.f : mn;
-          scale[half] = exp2f(m[half] - ref);  // 0 while nothing was seen
-          same = same && (mn == m[half]);
-          m[half] = mn;
-          float sum = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = exp2f(x[e] - ref);
-            sum += x[e];
-          }
-          l[half] = l[half] * scale[half] + sum;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            hi[half][n] = T::pack(x[2 * n], x[2 * n + 1]);
-            const float2 back = T::unpack(hi[half][n]);
-            lw[half][n] = T::pack(x[2 * n] - back.x, x[2 * n + 1] - back.y);
-          }
-        }
-        if (!__all_sync(0xffffffffu, same)) {
-          const float s0 = scale[0], s1 = kSmall ? scale[0] : scale[1];
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            acc[n][0] *= s0;
-            acc[n][1] *= s0;
-            acc[n][2] *= s1;
-            acc[n][3] *= s1;
-          }
-        }
-        // ---- o += weights * values (16 tokens: one k step)
-        uint32_t a[4], a2[4];
-        if (kSmall) {
-          a[0] = hi[0][0];
-          a[1] = lw[0][0];
-          a[2] = hi[0][1];
-          a[3] = lw[0][1];
-        } else {
-          a[0] = hi[0][0];
-          a[1] = hi[1][0];
-          a[2] = hi[0][1];
-          a[3] = hi[1][1];
-          a2[0] = lw[0][0];
-          a2[1] = lw[1][0];
-          a2[2] = lw[0][1];
-          a2[3] = lw[1][1];
-        }
-        const uint32_t vrow = smem_u32(vs) + (warp * 16 + (i8 & 1) * 8 + r8) * 128;
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t vb[4];
-          const int c = 2 * n + (i8 >> 1);
-          ldmatrix_x4_trans(vb, vrow + (c >> 3) * 8192 + (((c & 7) ^ r8) << 4));
-          T::mma(acc[2 * n], a, vb[0], vb[1]);
-          T::mma(acc[2 * n + 1], a, vb[2], vb[3]);
-          if (!kSmall) {
-            T::mma(acc[2 * n], a2, vb[0], vb[1]);
-            T::mma(acc[2 * n + 1], a2, vb[2], vb[3]);
-          }
-        }
+        rows.tokens(p, smem_u32(ks), smem_u32(vs), tok0);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.empty[st]);
     }
 
-    // ---- join the four warps' states
+    // ---- join the warps' states, 8 rows at a time by kPer threads each
 #pragma unroll
-    for (int half = 0; half < (kSmall ? 1 : 2); ++half) {
-      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-      if (t == 0) {
-        S.m[warp][g + 8 * half] = m[half];
-        S.l[warp][g + 8 * half] = l[half];
+    for (int e = 0; e < 2; ++e) {
+      const float l = rows.over_lanes(rows.l[e], [](float a, float b) { return a + b; });
+      if ((kSmall ? rows.g : rows.t) == 0) {
+        S.m[warp][rows.row(e)] = rows.m[e];
+        S.l[warp][rows.row(e)] = l;
       }
     }
     named_barrier(1, kConsumers * 32);
     const bool whole = s.count == s.pages;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (s.page == 0 ? 1 : 0);
     const int HQ = p.H * p.G;
+    float f[2];
 #pragma unroll
-    for (int half = 0; half < (kSmall ? 1 : 2); ++half) {
+    for (int e = 0; e < 2; ++e) {
       float top = kEmpty;
 #pragma unroll
-      for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, S.m[w][g + 8 * half]);
-      const float f = m[half] == kEmpty ? 0.f : exp2f(m[half] - top);
-      // 16 threads per row
-      const int row = tid >> 4, r = row + 8 * half;
+      for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, S.m[w][rows.row(e)]);
+      f[e] = rows.m[e] == kEmpty ? 0.f : exp2f(rows.m[e] - top);
+    }
+    constexpr int kPer = kConsumers * 4, kStride = C::template kJoinStride<kSmall>;
+#pragma unroll
+    for (int pass = 0; pass < (kSmall ? 1 : 2); ++pass) {
+      const int row = tid / kPer, r = row + 8 * pass;
       float M = kEmpty, L = 0.f;
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, S.m[w][r]);
@@ -534,7 +607,7 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
       int token, head;
       const bool write = run_row(p, first, count, h, tile, r, token, head) && !dead;
       const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
-      if (write && (tid & 15) == 0) {
+      if (write && tid % kPer == 0) {
         if (whole) {
           p.lse[(int64_t)token * HQ + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
         } else {
@@ -542,33 +615,28 @@ __global__ void __launch_bounds__(kPagedThreads) split_kernel(const __grid_const
           p.part_ml[(2 * (int64_t)gridDim.x + slot) * kRowTile + r] = L;
         }
       }
-      float* dst = join + (warp * 8 + g) * C::kRowStride + 2 * t;
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 64) {
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const float* a = acc[c0 / 8 + n];
-          const float x = kSmall ? a[0] + a[2] : a[2 * half];
-          const float y = kSmall ? a[1] + a[3] : a[2 * half + 1];
-          *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(x * f, y * f);
-        }
+      for (int c0 = 0; c0 < D; c0 += C::kJoin) {
+        rows.template put<C::kJoin>(join + warp * 8 * kStride, kStride, c0, pass, f);
         named_barrier(1, kConsumers * 32);
         if (write) {
-          const int c = (tid & 15) * 4;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int w = 0; w < kConsumers; ++w) {
-            const float4 v = *reinterpret_cast<const float4*>(join + (w * 8 + row) * C::kRowStride + c);
-            o.x += v.x;
-            o.y += v.y;
-            o.z += v.z;
-            o.w += v.w;
-          }
-          if (whole) {
-            store_pair<T>(p, token, head, D, c0 + c, o.x * inv, o.y * inv);
-            store_pair<T>(p, token, head, D, c0 + c + 2, o.z * inv, o.w * inv);
-          } else {
-            *reinterpret_cast<float4*>(p.part_o + (slot * kRowTile + r) * D + c0 + c) = o;
+          for (int c = (tid % kPer) * 4; c < C::kJoin; c += kPer * 4) {
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) {
+              const float4 v = *reinterpret_cast<const float4*>(join + (w * 8 + row) * kStride + c);
+              o.x += v.x;
+              o.y += v.y;
+              o.z += v.z;
+              o.w += v.w;
+            }
+            if (whole) {
+              store_pair<T>(p, token, head, D, c0 + c, o.x * inv, o.y * inv);
+              store_pair<T>(p, token, head, D, c0 + c + 2, o.z * inv, o.w * inv);
+            } else {
+              *reinterpret_cast<float4*>(p.part_o + (slot * kRowTile + r) * D + c0 + c) = o;
+            }
           }
         }
         named_barrier(1, kConsumers * 32);
@@ -730,9 +798,9 @@ static cudaError_t launch_dim(const PagedParams& p, int D, cudaStream_t stream) 
 }
 
 // Short histories are not split: a block per run walks its pages in less time than the
-// numbering and the join take (one request of 4 pages, 8 x 8 heads of 128: 6.4 us whole, 9.4
-// split; of 8: 8.9 and 9.4; of 12: 11.0 and 9.5).  With a run for every SM the device is
-// busy either way, and splitting only costs (16 requests of 32 pages: 26.5 and 31.9); but
+// numbering and the join take (one request of 4 pages, 8 x 8 heads of 128: 6.2 us whole, 9.1
+// split; of 8: 8.1 and 9.1; of 12: 10.2 and 9.2).  With a run for every SM the device is
+// busy either way, and splitting only costs (16 requests of 32 pages: 25.8 and 31.6); but
 // the lengths are not known here, and one long history among short ones must not be left
 // to one block for longer than that.
 constexpr int kWholePages = 8, kWholePagesBusy = 32, kBusyRuns = 128;

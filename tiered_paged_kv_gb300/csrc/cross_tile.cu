@@ -202,14 +202,6 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading) {
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// One lane of a converged warp, which the compiler then knows to be alone.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
 // Instruction descriptor: float32 accumulator, both inputs of one type, M = 128.
 __device__ __forceinline__ constexpr uint32_t instruction(bool bf16, bool b_rows_reduced, int n) {
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_rows_reduced ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
