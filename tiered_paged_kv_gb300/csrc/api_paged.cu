@@ -79,13 +79,16 @@ tpk_status make_map(CUtensorMap* map, int dtype, int rank, const void* base, con
   return r == CUDA_SUCCESS ? TPK_OK : fail(TPK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
 }
 
-// Pools as [slot * H * 64][D], page-high boxes.
-tpk_status make_maps(PagedParams& p, const tpk_paged_shape* s, const void* k_pool, const void* v_pool) {
-  const cuuint64_t dims[2] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->kv_slots * s->kv_heads * kPageTokens};
-  const cuuint64_t strides[1] = {(cuuint64_t)s->head_dim * 2};
-  const cuuint32_t box[2] = {64, kPageTokens};
-  const tpk_status st = make_map(&p.kmap, s->dtype, 2, k_pool, dims, strides, box);
-  return st == TPK_OK ? make_map(&p.vmap, s->dtype, 2, v_pool, dims, strides, box) : st;
+// The pools for the split kernel (whole: every channel in one box of kBoxRows rows), or for
+// the row tiles (boxes of a page's rows and 64 channels).
+tpk_status make_maps(PagedParams& p, const tpk_paged_shape* s, const void* k_pool, const void* v_pool, bool whole) {
+  const cuuint64_t D = s->head_dim, rows = (cuuint64_t)s->kv_slots * s->kv_heads * kPageTokens;
+  const cuuint64_t dims[3] = {whole ? 64 : D, rows, D / 64};
+  const cuuint64_t strides[2] = {D * 2, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(whole ? kBoxRows : kPageTokens), (cuuint32_t)(D / 64)};
+  const int rank = whole ? 3 : 2;
+  const tpk_status st = make_map(&p.kmap, s->dtype, rank, k_pool, dims, strides, box);
+  return st == TPK_OK ? make_map(&p.vmap, s->dtype, rank, v_pool, dims, strides, box) : st;
 }
 
 // Workspace of a split launch: the numbering table, then the partials.
@@ -170,8 +173,6 @@ tpk_status begin_attention(PagedParams& p, const tpk_paged_shape* s, int n_req, 
   std::memset(&p, 0, sizeof p);
   p.status = device_status_word();
   if (!p.status) return fail(TPK_ERR_CUDA, "cannot resolve the device status word");
-  st = make_maps(p, s, k_pool, v_pool);
-  if (st != TPK_OK) return st;
   p.q = static_cast<const uint16_t*>(q);
   p.o = o;
   p.lse = lse;
@@ -310,6 +311,7 @@ tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const 
   PagedParams p;
   st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
                        tpk_decode_paged_workspace_bytes(shape, n_req));
+  if (st == TPK_OK) st = make_maps(p, shape, k_pool, v_pool, true);
   if (st != TPK_OK) return st;
   place_ws(p, n_req, ws);
   p.begin = tok_begin;
@@ -341,6 +343,8 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
   p.range = kv_range;
   p.n_q = n_q;
   const CrossPlan plan = cross_plan(shape, n_req, n_q);
+  st = make_maps(p, shape, k_pool, v_pool, plan.groups == 0);
+  if (st != TPK_OK) return st;
   cudaError_t e;
   if (plan.groups == 0) {
     place_ws(p, n_req, ws);

@@ -49,8 +49,11 @@ struct RopeParams {
 cudaError_t launch_rope(const RopeParams& p, int dtype, int interleaved, cudaStream_t stream);
 
 // --------------------------------------------------------------- attention
+constexpr int kBoxRows = 16;  // rows of a page in one copy of the split kernel: one warp's
 struct PagedParams {
-  CUtensorMap kmap;  // pools as 2-D tensors [slot * H * 64][D], 64 x 64 boxes, 128-byte swizzle
+  // pools with the 128-byte swizzle.  Row tiles: [slot * H * 64][D], boxes of 64 rows x 64
+  // channels; split kernel: [D / 64][slot * H * 64][64], boxes of all channels of kBoxRows rows
+  CUtensorMap kmap;
   CUtensorMap vmap;
   CUtensorMap qmap;  // row tiles only: q as [n_q][H * G][D], boxes of 64 channels of a KV head's rows in a tile
   const uint16_t* q;
@@ -136,6 +139,13 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
+}
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void named_barrier(int id, int threads) {
