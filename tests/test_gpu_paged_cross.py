@@ -154,6 +154,20 @@ def test_short_wait_limit_alone_changes_nothing():
     assert tpk.get_device_status(reset=True) == (0, 0)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq,lens,pages,G", [([1], [1], 5, 1), ([1], [0], 5, 3), ([0], [5], 5, 1), ([70], [250], 4, 8),
+                                             ([4, 0, 1, 2], [300, 20, 0, 65], 8, 20), ([2], [3000], 47, 8),
+                                             ([2, 3], [20000, 129], 313, 4), ([30], [20000], 313, 8)],
+                         ids=lambda x: "-".join(map(str, x)) if isinstance(x, list) else str(x))
+def test_few_rows(nq, lens, pages, G, D):
+    """Tables wider than the lengths, on both sides of the choice of kernel."""
+    run(nq, lens, 1, G, D, "f16", seed=G, max_pages=pages, lead=1, tail=2)
+
+
+def test_few_rows_with_bad_pages():
+    run([4, 3], [1000, 64], 1, 2, 128, "bf16", mute=[(0, 0), (0, 7), (0, 15), (1, 0)], status=(4, 1))
+
+
 def test_no_queries():
     run([0, 0], [100, 5], 1, 1, 64, "bf16")
 

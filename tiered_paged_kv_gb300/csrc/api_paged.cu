@@ -120,13 +120,16 @@ struct CrossPlan {
 };
 CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
   const int64_t H = s->kv_heads, per_tile = kTileRows / s->group;
-  // The split kernel spreads single pages over the device and starts faster, the tiles
-  // read a page once for 128 rows: up to about six (page, 16 rows) units per SM the
-  // first wins (one request of 8 tokens, 6000 states, 4 x 8 heads of 256: 25 against 27
-  // us; of 1 token: 16 against 23; four of 1 token, 3000 states, 8 x 4 heads of 128, ten
-  // units per SM: 20 against 18; of 32 tokens: 57 against 28).
-  const int64_t units = ((int64_t)n_q * s->group / kRowTile + n_req) * H * s->max_pages;
-  if (units <= 6 * kTileBlocks) return {0, 0, 1};
+  // The split kernel spreads single pages over the device, the tiles read a page once for
+  // 128 rows.  Up to four pages the tiles need no fold (one request of 4 tokens, 100 states,
+  // 8 x 4 heads of 128: 7.3 us against 10.5).  Beyond that the split kernel wins with up to
+  // three (page, 16 rows) units per SM (one request of 16 tokens, 400 states, 4 x 8 heads
+  // of 256: 14.2 against 17.3; of 800, 3.1 units: 16.1 and 18.2; of 800, 8 x 4 of 128, 3.4
+  // units: 13.0 and 12.4), and with few runs up to fifty (one request of 4 tokens, 20,000
+  // states, 4 x 8 heads of 256, 12 runs: 38 against 50; of 8 tokens, 20 runs: 56 and 52; of
+  // 4 tokens, 60,000 states, 74 units: 78 and 73).
+  const int64_t runs = ((int64_t)n_q * s->group / kRowTile + n_req) * H, units = runs * s->max_pages;
+  if (s->max_pages > 4 && (units <= 3 * kTileBlocks || (runs <= 16 && units <= 50 * kTileBlocks))) return {0, 0, 1};
   // Two tiles share the keys and values and take about 1.5 times one tile's time, so one
   // is better where it needs at most 1.5 times the waves (four requests of 128 tokens,
   // 3000 states, 8 x 4 heads of 128: 34 us with one tile, 47 with two; sixteen of 128, 1000

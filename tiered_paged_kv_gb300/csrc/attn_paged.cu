@@ -17,12 +17,11 @@
 // warps take 16 of the 64 tokens each and keep their own online softmax, joined when a run
 // ends.  Boxes outside the request's span are neither copied nor computed: 96 windows of
 // 1000 tokens, 8 x 5 heads of 128, 66.9 -> 64.4 us.
-// Both
-// products run on mma.sync m16n8k16 with float32 accumulators (struct Rows).  The weights
-// enter PV as two 16-bit planes (the rounded weight and what the rounding left, about 16
-// bits in bfloat16), so they add no error of their own next to the rounding of the output.
-// A tensor tile of 128 rows would hold 8 or 16 useful ones; the few rows make the kernel
-// bound by HBM (4 H D bytes per attended token against 4 H G D operations).
+// Both products run on mma.sync m16n8k16 with float32 accumulators (struct Rows).  The
+// weights enter PV as two 16-bit planes (the rounded weight and what the rounding left,
+// about 16 bits in bfloat16), so they add no error of their own next to the rounding of the
+// output.  A tensor tile of 128 rows would hold 8 or 16 useful ones; the few rows make the
+// kernel bound by HBM (4 H D bytes per attended token against 4 H G D operations).
 //
 // Measured: 16 requests of 32,000 tokens at head sizes 64, 128, 256: 6.8, 6.9, 6.9 TB/s; one
 // request of 131,072 tokens (4 x 8 heads of 256, 537 MB) 86 us, 6.2 TB/s; one of 200 tokens
