@@ -136,7 +136,7 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, int interleaved, cudaStr
   int per = (int)min((int64_t)kRopeTokens, (int64_t)p.n_tokens * passes / (8 * 152));
   if (p.rot > 0) per = min(per, 2 * kRopePairs / p.rot);
   per = max(1, per);
-  const int blocks = (p.n_tokens + per - 1) / per * passes;
+  const int blocks = ((p.n_tokens - 1) / per + 1) * passes;
   if (dtype == 0) {
     if (interleaved) rope_kernel<Bf16, true><<<blocks, threads, 0, stream>>>(p, per, tasks, passes);
     else rope_kernel<Bf16, false><<<blocks, threads, 0, stream>>>(p, per, tasks, passes);
