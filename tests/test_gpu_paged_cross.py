@@ -164,6 +164,24 @@ def test_few_rows(nq, lens, pages, G, D):
     run(nq, lens, 1, G, D, "f16", seed=G, max_pages=pages, lead=1, tail=2)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,most,every,G", [(200, 700, 1, 1), (160, 130, 1, 8), (300, 90, 3, 3), (180, 400, 40, 1),
+                                            (40, 2500, 1, 4)])
+def test_rows_of_many_requests(n, most, every, G, D):
+    """About a token a request, spread evenly or gathered in every third or fortieth."""
+    run([every if i % every == 0 else 0 for i in range(n)], [(i * 37) % most for i in range(n)], 1, G, D, "bf16",
+        seed=G, tail=3)
+
+
+def test_sixteen_rows_of_many_requests():
+    run([(i * 7) % 33 for i in range(700)], [(i * 37) % 200 for i in range(700)], 1, 1, 64, "f16", seed=2)
+
+
+def test_rows_of_many_requests_see_ranges():
+    r = [(0, 0) if i % 5 == 0 else (i % 200, i % 200 + 65) for i in range(170)]
+    run([1] * 170, [(i * 37) % 300 for i in range(170)], 1, 2, 128, "bf16", ranges=r)
+
+
 def test_few_rows_with_bad_pages():
     run([4, 3], [1000, 64], 1, 2, 128, "bf16", mute=[(0, 0), (0, 7), (0, 15), (1, 0)], status=(4, 1))
 

@@ -121,15 +121,30 @@ struct CrossPlan {
 CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
   const int64_t H = s->kv_heads, per_tile = kTileRows / s->group;
   // The split kernel spreads single pages over the device, the tiles read a page once for
-  // 128 rows.  Up to four pages the tiles need no fold (one request of 4 tokens, 100 states,
-  // 8 x 4 heads of 128: 7.3 us against 10.5).  Beyond that the split kernel wins with up to
-  // three (page, 16 rows) units per SM (one request of 16 tokens, 400 states, 4 x 8 heads
-  // of 256: 14.2 against 17.3; of 800, 3.1 units: 16.1 and 18.2; of 800, 8 x 4 of 128, 3.4
-  // units: 13.0 and 12.4), and with few runs up to fifty (one request of 4 tokens, 20,000
-  // states, 4 x 8 heads of 256, 12 runs: 38 against 50; of 8 tokens, 20 runs: 56 and 52; of
-  // 4 tokens, 60,000 states, 74 units: 78 and 73).
-  const int64_t runs = ((int64_t)n_q * s->group / kRowTile + n_req) * H, units = runs * s->max_pages;
-  if (s->max_pages > 4 && (units <= 3 * kTileBlocks || (runs <= 16 && units <= 50 * kTileBlocks))) return {0, 0, 1};
+  // 128 rows.  With up to eight rows a request (its narrow form) the split kernel wins
+  // (1000 requests of a token, 250 states, 8 heads of 64: 109 us against 261; 256 of 1500
+  // states: 131 and 200; 64 of 1000, 4 x 8 heads of 256: 51 and 55) unless the tiles fill
+  // one wave of blocks and need no fold (16 of 1000, 8 heads of 128: 21 and 18; one of 100:
+  // 10.5 and 7.3), which the longest of long histories would hold up.
+  const int64_t rows = (int64_t)n_q * s->group, items = (n_q / per_tile + n_req) * H;
+  if (rows <= 8 * (int64_t)n_req) {
+    const bool folded = s->max_pages > 4 && 2 * items <= kTileBlocks;
+    if (items > kTileBlocks || folded || s->max_pages > 32) return {0, 0, 1};
+  } else {
+    // With up to 16, at head size 64 (small key tiles), in four waves of blocks or more: 1000
+    // requests of 16 tokens, 250 states, 8 heads: 153 and 263; 80 of 2 heads, 300 states: 19
+    // and 15.
+    if (rows <= 16 * (int64_t)n_req && s->head_dim == 64 && items > 4 * kTileBlocks) return {0, 0, 1};
+    // With more the split kernel wins with up to three (page, 16 rows) units per SM (one
+    // request of 16 tokens, 400 states, 4 x 8 heads of 256: 14.2 against 17.3; of 800, 3.1
+    // units: 16.1 and 18.2; of 800, 8 x 4 of 128, 3.4 units: 13.0 and 12.4), and with few
+    // runs up to fifty (one request of 4 tokens, 20,000 states, 4 x 8 heads of 256, 12 runs:
+    // 38 against 50; of 8 tokens, 20 runs: 56 and 52; of 4 tokens, 60,000 states, 74 units:
+    // 78 and 73), but not where the tiles need no fold (four pages: of 4 tokens, 100 states,
+    // 4 x 8 heads of 256: 12.8 and 9.3).
+    const int64_t runs = (rows / kRowTile + n_req) * H, units = runs * s->max_pages;
+    if (s->max_pages > 4 && (units <= 3 * kTileBlocks || (runs <= 16 && units <= 50 * kTileBlocks))) return {0, 0, 1};
+  }
   // Two tiles share the keys and values and take about 1.5 times one tile's time, so one
   // is better where it needs at most 1.5 times the waves (four requests of 128 tokens,
   // 3000 states, 8 x 4 heads of 128: 34 us with one tile, 47 with two; sixteen of 128, 1000

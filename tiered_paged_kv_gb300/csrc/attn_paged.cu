@@ -67,7 +67,7 @@ struct SplitShared {
 __device__ __forceinline__ int request_runs(const PagedParams& p, int b) {
   int first, count;
   request_rows(p, b, first, count);
-  return p.H * (int)(((int64_t)count * p.G + kRowTile - 1) / kRowTile);
+  return p.H * (int)(((int64_t)count * p.G + p.run_rows - 1) >> (p.run_rows == 8 ? 3 : 4));
 }
 __device__ __forceinline__ int request_pages(const PagedParams& p, int b, int& lo, int& hi) {
   request_span(p, b, lo, hi);
@@ -170,7 +170,7 @@ __device__ __forceinline__ void store_pair(const PagedParams& p, int64_t row, in
 __device__ __forceinline__ bool run_row(const PagedParams& p, int first, int count, int h, int tile, int r, int& token,
                                         int& head) {
   // 32 bits do: a call has at most 2^31 query rows
-  const uint32_t i = (uint32_t)tile * kRowTile + r;
+  const uint32_t i = (uint32_t)tile * p.run_rows + r;
   if (i >= (uint32_t)count * (uint32_t)p.G) return false;
   const uint32_t t = i / (uint32_t)p.G;
   token = first + (int)t;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 256 ? 1 : D == 64 ? 3 : kS
     if (pages == 0) {
       request_rows(p, walk.b, first, count);
       const int tiles = runs / p.H, h = run / tiles;
-      for (int i = tid; i < kRowTile * (D / 2); i += kPagedThreads) {
+      for (int i = tid; i < p.run_rows * (D / 2); i += kPagedThreads) {
         int token, head;
         if (!run_row(p, first, count, h, run - h * tiles, i / (D / 2), token, head)) continue;
         store_pair<T>(p, token, head, D, i % (D / 2) * 2, 0.f, 0.f);
@@ -771,13 +771,13 @@ static cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
     return cudaFuncSetAttribute(split_kernel<T, D, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  const int runs = p.H * ((p.G + kRowTile - 1) / kRowTile);  // of a decode request
+  const int runs = p.H * ((p.G + p.run_rows - 1) / p.run_rows);  // of a decode request
   const int blocks = p.whole ? p.n_req * runs : min(device_sms() * C::kBlocksPerSm, kPagedMaxBlocks);
   split_kernel<T, D, kSmall><<<blocks, kPagedThreads, C::kSmem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.whole || blocks == 1) return e;
   // the fold's blocks may start while the last ranges still run: they wait for them
-  const int rows = p.q_off ? kRowTile : min(p.G, kRowTile);
+  const int rows = p.q_off ? p.run_rows : min(p.G, p.run_rows);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -793,7 +793,7 @@ static cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
 
 template <typename T, int D>
 static cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
-  return !p.q_off && p.G <= 8 ? launch_t<T, D, true>(p, stream) : launch_t<T, D, false>(p, stream);
+  return p.run_rows == 8 ? launch_t<T, D, true>(p, stream) : launch_t<T, D, false>(p, stream);
 }
 
 template <typename T>
@@ -811,7 +811,8 @@ static cudaError_t launch_dim(const PagedParams& p, int D, cudaStream_t stream) 
 constexpr int kWholePages = 8, kWholePagesBusy = 32, kBusyRuns = 128;
 
 cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream) {
-  const int64_t runs = (int64_t)p.n_req * p.H * ((p.G + kRowTile - 1) / kRowTile);
+  p.run_rows = (int64_t)p.n_q * p.G <= 8 * (int64_t)p.n_req ? 8 : kRowTile;
+  const int64_t runs = (int64_t)p.n_req * p.H * ((p.G + p.run_rows - 1) / p.run_rows);
   p.whole = !p.q_off && p.max_pages <= (runs >= kBusyRuns ? kWholePagesBusy : kWholePages);
   return dtype == 0 ? launch_dim<Bf16>(p, D, stream) : launch_dim<F16>(p, D, stream);
 }

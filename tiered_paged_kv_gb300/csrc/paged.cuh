@@ -72,11 +72,12 @@ struct PagedParams {
   uint64_t wait_ns;
   float qscale;  // sm_scale * log2(e)
   int n_req, n_q, max_pages, H, G, o_f32;
-  int whole;  // a block per run (set at launch)
+  int run_rows;  // query rows of a run, 8 or 16 (set at launch)
+  int whole;     // a block per run (set at launch)
 };
 
 constexpr int kPagedMaxBlocks = 512;  // blocks of a split launch; each owns two partial slots
-constexpr int kRowTile = 16;          // query rows of a split unit
+constexpr int kRowTile = 16;          // query rows of a split run, at most
 cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream);
 
 constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row tiles aims at
