@@ -173,6 +173,15 @@ def test_rows_of_many_requests(n, most, every, G, D):
         seed=G, tail=3)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,most,q,pages,G", [(128, 500, 3, 8, 1), (128, 60, 5, 1, 4), (7, 300, 30, 6, 3), (100, 2000, 2, 32, 4),
+                                              (129, 400, 2, 7, 4), (3, 500, 70, 8, 2), (1, 64, 1, 1, 128)])
+def test_runs_not_cut(n, most, q, pages, G, D):
+    """A block per run: requests with no rows, no states, several runs."""
+    run([(i * 5) % (q + 1) if n > 1 else q for i in range(n)], [(i * 37 + 64) % (most + 1) for i in range(n)], 1, G, D,
+        "bf16", seed=q, lead=2, tail=5, max_pages=pages)
+
+
 def test_sixteen_rows_of_many_requests():
     run([(i * 7) % 33 for i in range(700)], [(i * 37) % 200 for i in range(700)], 1, 1, 64, "f16", seed=2)
 

@@ -86,16 +86,16 @@ __device__ __forceinline__ int64_t per_block(int64_t total, int blocks) {
 }
 
 // The numbering of up to kScanned requests by one warp: lane i has requests 4 i .. 4 i + 3.
-constexpr int kScanned = 128;
 struct Numbers {
   int64_t total, before;  // all units; those before this lane's requests
   int64_t units[4];
-  __device__ __forceinline__ void load(const PagedParams& p) {
+  template <typename F>
+  __device__ __forceinline__ void load(const PagedParams& p, F of_request) {
     const int lane = threadIdx.x & 31;
     int64_t mine = 0;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      units[x] = 4 * lane + x < p.n_req ? request_units(p, 4 * lane + x) : 0;
+      units[x] = 4 * lane + x < p.n_req ? of_request(p, 4 * lane + x) : 0;
       mine += units[x];
     }
     int64_t inc = mine;
@@ -397,22 +397,32 @@ __global__ void __launch_bounds__(kPagedThreads, D == 256 ? 1 : D == 64 ? 3 : kS
   }
   Walk walk;
   if (p.whole) {
-    // a block per run: nothing to number, nothing to join
+    // a block per run: nothing to join, and nothing to number if every request has as many
+    int64_t run;
+    if (p.q_off) {
+      Numbers numbers;
+      numbers.load(p, request_runs);
+      if (blockIdx.x >= numbers.total) return;  // the grid is an upper bound
+      numbers.find(blockIdx.x, walk.b, run);
+      run = blockIdx.x - run;
+    } else {
+      const int runs = request_runs(p, 0);
+      walk.b = blockIdx.x / runs;
+      run = blockIdx.x - walk.b * runs;
+    }
     __syncthreads();
     int lo, hi, first, count;
-    const int runs = request_runs(p, 0);  // the same for every request
-    walk.b = blockIdx.x / runs;
-    const int run = blockIdx.x - walk.b * runs;
+    const int runs = request_runs(p, walk.b);
     const int pages = request_pages(p, walk.b, lo, hi);
     walk.base = 0;
-    walk.at = (int64_t)run * (pages + kRunCost);
+    walk.at = run * (pages + kRunCost);
     walk.end = walk.at + pages + kRunCost;
     if (pages == 0) {
       request_rows(p, walk.b, first, count);
-      const int tiles = runs / p.H, h = run / tiles;
+      const int tiles = runs / p.H, h = (int)run / tiles;
       for (int i = tid; i < p.run_rows * (D / 2); i += kPagedThreads) {
         int token, head;
-        if (!run_row(p, first, count, h, run - h * tiles, i / (D / 2), token, head)) continue;
+        if (!run_row(p, first, count, h, (int)run - h * tiles, i / (D / 2), token, head)) continue;
         store_pair<T>(p, token, head, D, i % (D / 2) * 2, 0.f, 0.f);
         if (i % (D / 2) == 0) p.lse[(int64_t)token * p.H * p.G + head] = kEmpty;
       }
@@ -423,7 +433,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 256 ? 1 : D == 64 ? 3 : kS
     int64_t lo, hi;
     if (p.n_req <= kScanned) {
       Numbers numbers;
-      numbers.load(p);
+      numbers.load(p, request_units);
       const int64_t per = per_block(numbers.total, gridDim.x);
       lo = min(per * blockIdx.x, numbers.total);
       hi = min(lo + per, numbers.total);
@@ -666,7 +676,7 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
   int b = 0;
   Numbers numbers;
   if (p.n_req <= kScanned) {
-    numbers.load(p);
+    numbers.load(p, request_units);
     total = numbers.total;
   } else {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -763,6 +773,12 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
 
 int device_sms();
 
+// Runs of a launch: a decode's, an upper bound of cross attention's.
+static int64_t most_runs(const PagedParams& p) {
+  const int64_t each = (p.G + p.run_rows - 1) / p.run_rows;
+  return p.H * (p.q_off ? (int64_t)p.n_q * p.G / p.run_rows + p.n_req : p.n_req * each);
+}
+
 template <typename T, int D, bool kSmall>
 static cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
   using C = SplitCfg<D>;
@@ -771,8 +787,7 @@ static cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
     return cudaFuncSetAttribute(split_kernel<T, D, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  const int runs = p.H * ((p.G + p.run_rows - 1) / p.run_rows);  // of a decode request
-  const int blocks = p.whole ? p.n_req * runs : min(device_sms() * C::kBlocksPerSm, kPagedMaxBlocks);
+  const int blocks = p.whole ? (int)most_runs(p) : min(device_sms() * C::kBlocksPerSm, kPagedMaxBlocks);
   split_kernel<T, D, kSmall><<<blocks, kPagedThreads, C::kSmem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.whole || blocks == 1) return e;
@@ -802,18 +817,9 @@ static cudaError_t launch_dim(const PagedParams& p, int D, cudaStream_t stream) 
                                                             : launch_rows<T, 256>(p, stream);
 }
 
-// Short histories are not split: a block per run walks its pages in less time than the
-// numbering and the join take (one request of 4 pages, 8 x 8 heads of 128: 6.2 us whole, 9.1
-// split; of 8: 8.1 and 9.1; of 12: 10.2 and 9.2).  With a run for every SM the device is
-// busy either way, and splitting only costs (16 requests of 32 pages: 25.8 and 31.6); but
-// the lengths are not known here, and one long history among short ones must not be left
-// to one block for longer than that.
-constexpr int kWholePages = 8, kWholePagesBusy = 32, kBusyRuns = 128;
-
 cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream) {
   p.run_rows = (int64_t)p.n_q * p.G <= 8 * (int64_t)p.n_req ? 8 : kRowTile;
-  const int64_t runs = (int64_t)p.n_req * p.H * ((p.G + p.run_rows - 1) / p.run_rows);
-  p.whole = !p.q_off && p.max_pages <= (runs >= kBusyRuns ? kWholePagesBusy : kWholePages);
+  p.whole = split_whole(p.q_off, p.n_req, p.q_off ? (int64_t)p.n_req * p.H : most_runs(p), p.max_pages);
   return dtype == 0 ? launch_dim<Bf16>(p, D, stream) : launch_dim<F16>(p, D, stream);
 }
 

@@ -80,6 +80,19 @@ constexpr int kPagedMaxBlocks = 512;  // blocks of a split launch; each owns two
 constexpr int kRowTile = 16;          // query rows of a split run, at most
 cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream);
 
+constexpr int kScanned = 128;  // requests that one warp numbers: lane i has 4 i .. 4 i + 3
+// Short histories are not split: a block per run walks its pages in less time than the
+// numbering and the join take (one request of 4 pages, 8 x 8 heads of 128: 6.2 us whole, 9.1
+// split; of 8: 8.1 and 9.1; of 12: 10.2 and 9.2).  With a run for every SM the device is
+// busy either way, and splitting only costs (16 requests of 32 pages: 25.8 and 31.6); but
+// the lengths are not known here, and one long history among short ones must not be left
+// to one block for longer than that.  Cross attention counts one run a request and head, and
+// finds a block's run by a warp's scan.
+constexpr int kWholePages = 8, kWholePagesBusy = 32, kBusyRuns = 128;
+inline bool split_whole(bool cross, int n_req, int64_t runs, int max_pages) {
+  return max_pages <= (runs >= kBusyRuns ? kWholePagesBusy : kWholePages) && (!cross || n_req <= kScanned);
+}
+
 constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row tiles aims at
 constexpr int kTileRows = 128;    // query rows of a tile; a block takes `tiles` (1 or 2) of them
 cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
