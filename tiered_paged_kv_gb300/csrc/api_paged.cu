@@ -126,23 +126,26 @@ CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
   //   8 heads of 64: 109 us against 261; 120 of 1500: 68 and 102; one of 100, 8 x 4 of 128:
   //   5.5 and 7.3; four of 1000: 11.2 and 12.2; sixteen of 2000: 26.0 and 27.7);
   // - with up to sixteen, where it need not cut runs or there are many items (19 of 600, 8 of
-  //   64: 12.2 and 12.4; 64 of 500, 8 of 128: 33 and 38; 16 of 2000: 29.8 and 27.6; 1000 of
+  //   64: 10.7 and 12.4; 64 of 500, 8 of 128: 33 and 38; 16 of 2000: 29.8 and 27.6; 1000 of
   //   250, 8 of 64: 153 and 263), at head size 256 not (100 of 100, 2 x 8: 18.6 and 15.4);
   // - with more, where it need not cut runs, tables are short and a wave of blocks takes
-  //   them all (two requests of 32 tokens, 500 states, 8 x 4 of 128, 144 runs: 11.3 and 13.3;
-  //   16 of 200, 8 x 2 of 64, 384 runs: 8.5 and 9.7; 640 runs: 15.2 and 10.0);
+  //   them all, in runs of 8 rows, or of 16 below head size 256 (two requests of 32 tokens, 500
+  //   states, 8 x 4 of 128: 10.5 and 13.3; one of 16, 250 states, 4 x 8 of 256: 8.1 and
+  //   11.6; 16 of 16, 200 states, 8 x 2 of 64, 384 runs of 16: 8.5 and 9.7; of 32, 640 runs:
+  //   15.2 and 10.0);
   // - with few (page, 16 rows) units per SM at head size 256 (one request of 16 tokens, 800
   //   states, 4 x 8, 3.1 units: 16.1 and 18.2; of 3000, 11 units: 25.1 and 23.6);
   // - with few runs of more (one request of 4 tokens, 20,000 states, 4 x 8 of 256, 12 runs:
   //   38 and 50; of 8 tokens, 20 runs: 56 and 52; of 4, 60,000 states, 74 units: 78 and 73).
   const bool wide = s->head_dim == 256;
   const int64_t rows = (int64_t)n_q * s->group, items = (n_q / per_tile + n_req) * H;
-  const int64_t runs = (rows / kRowTile + n_req) * H, units = runs * s->max_pages;
+  auto runs = [&](int run_rows) { return (rows / run_rows + n_req) * H; };
+  const int64_t units = runs(kRowTile) * s->max_pages, wave = split_blocks(s->head_dim) * kTileBlocks;
   const bool whole = split_whole(true, n_req, n_req * H, s->max_pages);
   if (rows <= 8 * (int64_t)n_req || (!wide && rows <= 16 * (int64_t)n_req && (whole || items > 4 * kTileBlocks)) ||
-      (!wide && whole && s->max_pages <= kWholePages && runs <= (s->head_dim == 64 ? 3 : 2) * kTileBlocks) ||
+      (whole && s->max_pages <= kWholePages && runs(wide ? 8 : kRowTile) <= wave) ||
       (s->max_pages > kWholePages &&
-       ((wide && units <= 3 * kTileBlocks) || (runs <= 16 && units <= 50 * kTileBlocks))))
+       ((wide && units <= 3 * kTileBlocks) || (runs(kRowTile) <= 16 && units <= 50 * kTileBlocks))))
     return {0, 0, 1};
   // Two tiles share the keys and values and take about 1.5 times one tile's time, so one
   // is better where it needs at most 1.5 times the waves (four requests of 128 tokens,

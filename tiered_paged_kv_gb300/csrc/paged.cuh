@@ -76,10 +76,12 @@ struct PagedParams {
   int whole;     // a block per run (set at launch)
 };
 
+constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row tiles aims at
 constexpr int kPagedMaxBlocks = 512;  // blocks of a split launch; each owns two partial slots
 constexpr int kRowTile = 16;          // query rows of a split run, at most
 cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream);
 
+constexpr int split_blocks(int D) { return D == 256 ? 1 : D == 128 ? 2 : 3; }  // resident per SM
 constexpr int kScanned = 128;  // requests that one warp numbers: lane i has 4 i .. 4 i + 3
 // Short histories are not split: a block per run walks its pages in less time than the
 // numbering and the join take (one request of 4 pages, 8 x 8 heads of 128: 6.2 us whole, 9.1
@@ -93,7 +95,6 @@ inline bool split_whole(bool cross, int n_req, int64_t runs, int max_pages) {
   return max_pages <= (runs >= kBusyRuns ? kWholePagesBusy : kWholePages) && (!cross || n_req <= kScanned);
 }
 
-constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row tiles aims at
 constexpr int kTileRows = 128;    // query rows of a tile; a block takes `tiles` (1 or 2) of them
 cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
                                cudaStream_t stream);
