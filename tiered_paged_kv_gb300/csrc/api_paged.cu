@@ -106,7 +106,7 @@ void place_ws(PagedParams& p, int n_req, void* ws) {
   p.part_o = reinterpret_cast<float*>(w);
 }
 
-// How cross attention of n_q tokens is cut.  groups = 0: the split kernel's 16-row units.
+// How cross attention of n_q tokens is cut.  groups = 0: the split kernel's runs.
 // Otherwise row-tile items of one or two 128-row tiles: `groups` bounds them for one KV
 // head (whole ones, and one per request that is not), `splits` parts of the keys fill
 // the device where they are few.  The rules go by what the host knows (lengths are on

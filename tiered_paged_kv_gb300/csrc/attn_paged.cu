@@ -1,7 +1,7 @@
 // Attention of few query rows over paged keys and values whose lengths live on the
 // device: one new token per request, or a handful of query tokens per request.
 //
-// A run is 16 query rows of one (request, KV head): the G heads of a new token, or
+// A run is 8 or 16 query rows of one (request, KV head): the G heads of a new token, or
 // (token, head) pairs of cross attention.  Every run of a request reads the same pages
 // and costs that many units and kRunCost more (its queries and its join), so request b
 // costs (pages_b + kRunCost) * runs_b; the units are numbered request by request, run by
@@ -10,7 +10,8 @@
 // needs no host-side lengths.  A run inside one block's range is written out at once;
 // one that crosses ranges leaves a partial (running maximum, sum, unnormalised o) in
 // the block's two workspace slots -- slot 0: a run entered in the middle, slot 1: one
-// left before its end -- and the fold kernel joins the partials in block order.
+// left before its end -- and the fold kernel joins the partials in block order.  Where tables
+// are short (split_whole) a block takes one run whole, and there is no fold.
 //
 // Within a block a producer warp walks the range and feeds a ring of page stages by TMA
 // (64 tokens of keys and of values, 128-byte swizzle, a box per 16 tokens); four consumer
