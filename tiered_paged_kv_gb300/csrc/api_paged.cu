@@ -133,19 +133,14 @@ CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
   //   states, 8 x 4 of 128: 10.5 and 13.3; one of 16, 250 states, 4 x 8 of 256: 8.1 and
   //   11.6; 16 of 16, 200 states, 8 x 2 of 64, 384 runs of 16: 8.5 and 9.7; of 32, 640 runs:
   //   15.2 and 10.0);
-  // - with few (page, 16 rows) units per SM at head size 256 (one request of 16 tokens, 800
-  //   states, 4 x 8, 3.1 units: 16.1 and 18.2; of 3000, 11 units: 25.1 and 23.6);
-  // - with few runs of more (one request of 4 tokens, 20,000 states, 4 x 8 of 256, 12 runs:
-  //   38 and 50; of 8 tokens, 20 runs: 56 and 52; of 4, 60,000 states, 74 units: 78 and 73).
+  // - with few runs (split_few).
   const bool wide = s->head_dim == 256;
   const int64_t rows = (int64_t)n_q * s->group, items = (n_q / per_tile + n_req) * H;
   auto runs = [&](int run_rows) { return (rows / run_rows + n_req) * H; };
-  const int64_t units = runs(kRowTile) * s->max_pages, wave = split_blocks(s->head_dim) * kTileBlocks;
+  const int64_t wave = split_blocks(s->head_dim) * kTileBlocks;
   const bool whole = split_whole(true, n_req, n_req * H, s->max_pages);
   if (rows <= 8 * (int64_t)n_req || (!wide && rows <= 16 * (int64_t)n_req && (whole || items > 4 * kTileBlocks)) ||
-      (whole && s->max_pages <= kWholePages && runs(wide ? 8 : kRowTile) <= wave) ||
-      (s->max_pages > kWholePages &&
-       ((wide && units <= 3 * kTileBlocks) || (runs(kRowTile) <= 16 && units <= 50 * kTileBlocks))))
+      (whole && s->max_pages <= kWholePages && runs(wide ? 8 : kRowTile) <= wave) || split_few(runs(8), s->max_pages))
     return {0, 0, 1};
   // Two tiles share the keys and values and take about 1.5 times one tile's time, so one
   // is better where it needs at most 1.5 times the waves (four requests of 128 tokens,

@@ -820,12 +820,13 @@ static cudaError_t launch_dim(const PagedParams& p, int D, cudaStream_t stream) 
 
 cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream) {
   auto whole = [&] { return split_whole(p.q_off, p.n_req, p.q_off ? (int64_t)p.n_req * p.H : most_runs(p), p.max_pages); };
-  // Runs of 8 rows where requests have no more; also where all of them are resident at once
-  // and none is cut, each page's second reader then finding it in L2 (one request of 500
-  // tokens, 8 x 16 heads of 256: 10.4 us, 16.0 with runs of 16; nine: 11.0 and 16.3; where
-  // not all are resident, 18 of 300: 17.3 with runs of 8, 13.8 with 16).
+  // Runs of 8 rows where requests have no more; also where few of them are cut (read_twice),
+  // and where none is and all are resident at once, a page's second reader finding it in L2
+  // (one request of 500 tokens, 8 x 16 heads of 256: 10.4 us, 16.0 with runs of 16; nine: 11.0
+  // and 16.3; where not all are resident, 18 of 300: 17.3 with runs of 8, 13.8 with 16).
   p.run_rows = 8;
-  if ((int64_t)p.n_q * p.G > 8 * (int64_t)p.n_req && !(whole() && most_runs(p) <= split_blocks(D) * kTileBlocks))
+  if ((int64_t)p.n_q * p.G > 8 * (int64_t)p.n_req &&
+      !(whole() ? most_runs(p) <= split_blocks(D) * kTileBlocks : read_twice(most_runs(p), p.max_pages, D)))
     p.run_rows = kRowTile;
   p.whole = whole();
   return dtype == 0 ? launch_dim<Bf16>(p, D, stream) : launch_dim<F16>(p, D, stream);

@@ -94,6 +94,17 @@ constexpr int kWholePages = 8, kWholePagesBusy = 32, kBusyRuns = 128;
 inline bool split_whole(bool cross, int n_req, int64_t runs, int max_pages) {
   return max_pages <= (runs >= kBusyRuns ? kWholePagesBusy : kWholePages) && (!cross || n_req <= kScanned);
 }
+// Few runs of 8 rows, the split kernel's even where they are more than a request (one request of
+// 16 rows, 3000 states, 8 heads of 128: 11.7 us, 14.6 as row tiles; 4 heads of 256: 11.6 and
+// 18.2; of 64 rows, 36 runs: 17.6 and 20.2; of 128 rows, 8 heads of 128, 72 runs: 17.3 and 15.3;
+// of 64 rows, 20,000 states, 4 heads of 256, 74 (page, run) units per SM: 56 and 52).
+inline bool split_few(int64_t runs, int max_pages) { return runs <= 64 && runs * max_pages <= 50 * kTileBlocks; }
+// Runs of 8 rather than 16 rows read pages twice, with less work on each: for as long as
+// the pages stay in L2 (decode of 16 heads a group: 1000 tokens, 8 KV heads of 256, 10.8 us
+// against 14.3 in runs of 16; 5000: 16.7 and 18.2; 20,000, 160 MB: 48 and 43).
+inline bool read_twice(int64_t runs, int max_pages, int D) {
+  return split_few(runs, max_pages) && runs * max_pages / 2 * (kPageTokens * 4 * D) <= 100 << 20;
+}
 
 constexpr int kTileRows = 128;    // query rows of a tile; a block takes `tiles` (1 or 2) of them
 cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
