@@ -182,8 +182,10 @@ def test_runs_not_cut(n, most, q, pages, G, D):
         "bf16", seed=q, lead=2, tail=5, max_pages=pages)
 
 
-def test_sixteen_rows_of_many_requests():
-    run([(i * 7) % 33 for i in range(700)], [(i * 37) % 200 for i in range(700)], 1, 1, 64, "f16", seed=2)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,H,G,q,pages", [(700, 1, 1, 33, None), (60, 4, 4, 9, 8)])
+def test_sixteen_rows_of_many_requests(n, H, G, q, pages, D):
+    run([(i * 7) % q for i in range(n)], [(i * 37) % 200 for i in range(n)], H, G, D, "f16", seed=2, max_pages=pages)
 
 
 def test_rows_of_many_requests_see_ranges():

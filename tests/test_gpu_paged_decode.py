@@ -80,6 +80,23 @@ def test_lengths(lens, D):
     run(lens, 1, 4, D, "bf16", seed=len(lens))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,most,H,G,pages", [(60, 300, 4, 16, 5), (12, 1500, 4, 20, 40), (130, 200, 2, 12, 40), (7, 900, 3, 33, 40)])
+def test_many_rows(n, most, H, G, pages, D):
+    """More than eight heads a group, histories whole and cut, numbered by a warp, by the block."""
+    lens = [(i * 379 + i // 3) % (most + 1) for i in range(n)]
+    run(lens, H, G, D, "bf16", seed=G, max_pages=pages)
+
+
+@pytest.mark.parametrize("pages", [24, 40])
+def test_many_rows_windows_and_bad_pages(pages):
+    n = 24
+    lens = [(i * 379) % 1500 for i in range(n)]
+    begin = [max(0, x - 130 * (i % 5)) for i, x in enumerate(lens)]
+    lens[3], begin[3], begin[5] = 1000, 0, 0
+    run(lens, 4, 16, 128, "f16", begin=begin, o_f32=True, max_pages=pages, mute=[(3, 2), (3, 15), (5, 0)], status=(4, 1))
+
+
 @pytest.mark.parametrize("D", [64, 256])
 def test_windows(D):
     lens = [1, 64, 65, 200, 1000, 1000, 1000, 500, 0]
