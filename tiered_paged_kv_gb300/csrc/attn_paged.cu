@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 256 ? 1 : D == 64 ? 3 : kS
   SplitShared& S = *reinterpret_cast<SplitShared*>(stages + C::kStages * C::kStageBytes + C::kJoinBytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (smem_u32(stages) & 1023) {  // the swizzle counts on it
+    wait_before();
     if (tid == 0) atomicOr(p.status, kStatusTimeout);
     return;
   }
@@ -396,6 +397,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 256 ? 1 : D == 64 ? 3 : kS
     mbar_init(&S.empty[tid], kConsumers);
     fence_mbar_init();
   }
+  wait_before();
   Walk walk;
   if (p.whole) {
     // a block per run: nothing to join, and nothing to number if every request has as many
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 256 ? 1 : D == 64 ? 3 : kS
       return;
     }
   } else {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    start_next();
     int64_t lo, hi;
     if (p.n_req <= kScanned) {
       Numbers numbers;
@@ -680,7 +682,7 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
     numbers.load(p, request_units);
     total = numbers.total;
   } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_before();
     total = p.prefix[p.n_req];
   }
   const int64_t per = per_block(total, blocks);
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
   }
   // every block waits, whether it has a row or not: the launch must not end before the
   // one whose partials it joins
-  if (p.n_req <= kScanned) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.n_req <= kScanned) wait_before();
   if (!mine) return;
   // block i left the run before its end, the others entered it in the middle
   auto slot = [&](int k) { return (2 * (int64_t)(i + k) + (k == 0 ? 1 : 0)) * kRowTile + r; };
@@ -789,22 +791,11 @@ static cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
   });
   if (e != cudaSuccess) return e;
   const int blocks = p.whole ? (int)most_runs(p) : min(device_sms() * C::kBlocksPerSm, kPagedMaxBlocks);
-  split_kernel<T, D, kSmall><<<blocks, kPagedThreads, C::kSmem, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_early(split_kernel<T, D, kSmall>, blocks, kPagedThreads, C::kSmem, stream, p);
   if (e != cudaSuccess || p.whole || blocks == 1) return e;
   // the fold's blocks may start while the last ranges still run: they wait for them
   const int rows = p.q_off ? p.run_rows : min(p.G, p.run_rows);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((blocks - 1) * rows);
-  cfg.blockDim = dim3(64);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fold_paged_kernel<T, D>, p, blocks, rows);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_early(fold_paged_kernel<T, D>, (blocks - 1) * rows, 64, 0, stream, p, blocks, rows);
 }
 
 template <typename T, int D>

@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
   uint8_t* slots = qs + C::kTiles * C::kQBytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (smem_u32(raw) & 1023) {  // the swizzle counts on it
+    wait_before();
     if (tid == 0) atomicOr(p.status, kStatusTimeout);
     return;
   }
@@ -362,7 +363,8 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.kmap) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.vmap) : "memory");
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_before();
+  start_next();
   if (warp == C::kMma) tmem_alloc(&S.tmem);
   tc_fence_before();
   __syncthreads();
@@ -949,7 +951,7 @@ __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ 
   const int t = (want * C::kTiles + r / kTileRows) * per_tile + x;
   // every block waits, whether it has a row or not: the launch must not end before the
   // one whose parts it joins
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_before();
   if (b == p.n_req || x >= per_tile || t >= count) return;
   const int token = first + t, head = h * p.G + r % kTileRows - x * p.G;
   const int64_t group = w / C::kRows;  // (tile group, head)
@@ -988,21 +990,10 @@ static cudaError_t launch_t(const PagedParams& p, int groups, int splits, cudaSt
     return cudaFuncSetAttribute(tile_kernel<T, D, kT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  tile_kernel<T, D, kT><<<groups * p.H * splits, C::kThreads, C::kSmem, stream>>>(p, splits);
-  e = cudaGetLastError();
+  e = launch_early(tile_kernel<T, D, kT>, groups * p.H * splits, C::kThreads, C::kSmem, stream, p, splits);
   if (e != cudaSuccess || splits == 1) return e;
   // the fold's blocks may start while the last parts still run: they wait for them
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(groups * p.H * (C::kRows / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tile_fold_kernel<T, D, kT>, p, splits);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_early(tile_fold_kernel<T, D, kT>, groups * p.H * (C::kRows / 8), 256, 0, stream, p, splits);
 }
 
 template <int D, int kT>

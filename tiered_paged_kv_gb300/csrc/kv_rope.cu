@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         b[u] = *reinterpret_cast<const uint4*>(src + (t + u) * stride + cb);
       }
   };
+  wait_before();
   load(0);
 
   // ---- the tokens' angles and places
@@ -137,14 +138,9 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, int interleaved, cudaStr
   if (p.rot > 0) per = min(per, 2 * kRopePairs / p.rot);
   per = max(1, per);
   const int blocks = ((p.n_tokens - 1) / per + 1) * passes;
-  if (dtype == 0) {
-    if (interleaved) rope_kernel<Bf16, true><<<blocks, threads, 0, stream>>>(p, per, tasks, passes);
-    else rope_kernel<Bf16, false><<<blocks, threads, 0, stream>>>(p, per, tasks, passes);
-  } else {
-    if (interleaved) rope_kernel<F16, true><<<blocks, threads, 0, stream>>>(p, per, tasks, passes);
-    else rope_kernel<F16, false><<<blocks, threads, 0, stream>>>(p, per, tasks, passes);
-  }
-  return cudaGetLastError();
+  auto kernel = dtype == 0 ? (interleaved ? rope_kernel<Bf16, true> : rope_kernel<Bf16, false>)
+                           : (interleaved ? rope_kernel<F16, true> : rope_kernel<F16, false>);
+  return launch_early(kernel, blocks, threads, 0, stream, p, per, tasks, passes);
 }
 
 }  // namespace tpk

@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
   int32_t* taken = off + n + 1;  // [n] pages taken before it
   int32_t* gave = taken + n;     // [n] pages given back before it
   uint8_t* fine = reinterpret_cast<uint8_t*>(gave + n);  // [n] granted
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_before();
+  start_next();
 
   const int each = (n + kTabThreads - 1) / kTabThreads;
   const int b0 = min(tid * each, n), b1 = min(b0 + each, n);
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
 
 __global__ void __launch_bounds__(kFillThreads) maps_kernel(const TablesParams p) {
   extern __shared__ int32_t off[];  // [n + 1]
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_before();
   for (int b = threadIdx.x; b <= p.n_req; b += kFillThreads) off[b] = p.tok_off[b];
   __syncthreads();
   fill_maps(p, off, blockIdx.x * (kFillThreads * kFillTokens) + threadIdx.x, kFillThreads);
@@ -248,21 +249,11 @@ cudaError_t launch_tables(const TablesParams& p, cudaStream_t stream) {
       [&] { return cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most); });
   if (e != cudaSuccess) return e;
   const bool one = p.max_tokens <= kOneBlock;
-  tables_kernel<<<1, kTabThreads, (3 * p.n_req + 1) * sizeof(int32_t) + p.n_req, stream>>>(p, one);
-  e = cudaGetLastError();
+  e = launch_early(tables_kernel, 1, kTabThreads, (3 * p.n_req + 1) * sizeof(int32_t) + p.n_req, stream, p, (int)one);
   if (e != cudaSuccess || one) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.max_tokens + kFillThreads * kFillTokens - 1) / (kFillThreads * kFillTokens));
-  cfg.blockDim = dim3(kFillThreads);
-  cfg.dynamicSmemBytes = (p.n_req + 1) * sizeof(int32_t);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, maps_kernel, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const int per_block = kFillThreads * kFillTokens;
+  return launch_early(maps_kernel, (p.max_tokens + per_block - 1) / per_block, kFillThreads, (p.n_req + 1) * sizeof(int32_t),
+                      stream, p);
 }
 
 }  // namespace tpk
