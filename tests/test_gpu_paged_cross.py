@@ -239,3 +239,45 @@ def test_two_streams_and_capture(nq):
     a.o.fill_(float("nan"))
     g.replay()
     a.check("replayed with other lengths")
+
+
+@pytest.mark.parametrize("nq,lens,pages,G", [([1], [100], 5, 2), ([300], [900], None, 2), ([4, 3], [1000, 64], None, 20),
+                                             ([3, 2], [5000, 200], None, 4)],
+                         ids=lambda x: "-".join(map(str, x)) if isinstance(x, list) else str(x))
+def test_between_copies_forks_and_joins(nq, lens, pages, G):
+    """A call waits for whatever is before it in its stream, and what follows waits for it: copies
+    into its queries and over its results, calls of another stream, captured and not."""
+    a, b, c = (Cross(Pages(lens, 1, 128, "bf16", i, max_pages=pages), nq, G) for i in (1, 2, 3))
+    q, zero = c.dq.clone(), torch.zeros_like(c.dq)
+    s, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step(cur):
+        a.call(cur)
+        s2.wait_stream(cur)
+        b.call(s2)
+        a.call(cur)
+        cur.wait_stream(s2)
+        c.dq.copy_(q)
+        c.call(cur)
+        c.o.zero_()
+        c.o[:, c.pg.H * G * 128:] = float("nan")
+        c.call(cur)
+        c.dq.copy_(zero)
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(10):
+            step(s)
+    for x in (a, b, c):
+        x.check("eager")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step(torch.cuda.current_stream())
+    for x in (a, b, c):
+        x.o.fill_(float("nan"))
+        x.lse.fill_(float("nan"))
+    for _ in range(3):
+        g.replay()
+    for x in (a, b, c):
+        x.check("captured")
+    assert tpk.get_device_status(reset=True) == (0, 0)
