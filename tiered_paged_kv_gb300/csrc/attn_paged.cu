@@ -35,13 +35,14 @@ constexpr float kEmpty = -__builtin_huge_valf();
 constexpr int kConsumers = 4;
 constexpr int kPagedThreads = (kConsumers + 1) * 32;
 
-template <int D>
+template <int D, bool kMany>  // kMany: three blocks per SM at D = 128
 struct SplitCfg {
+  static_assert(!kMany || D == 128, "kMany");
   static constexpr int kPageBytes = kPageTokens * D * 2;   // keys or values of one page
   static constexpr int kStageBytes = 2 * kPageBytes;
   static constexpr int kBoxBytes = kBoxRows * D * 2;       // one warp's keys or values
-  static constexpr int kStages = D == 64 ? 4 : 3;
-  static constexpr int kBlocksPerSm = split_blocks(D);
+  static constexpr int kStages = D == 64 ? 4 : kMany ? 2 : 3;
+  static constexpr int kBlocksPerSm = kMany ? 3 : split_blocks(D);
   static constexpr int kJoin = D == 256 ? 256 : 64;  // channels joined at a time
   // floats a row, which spread the 8 rows (or the 4 lanes' row pairs) over the banks
   template <bool kSmall>
@@ -372,10 +373,10 @@ struct Rows {
 // The second bound asks for the registers of kBlocksPerSm blocks.  In the wide form at
 // D = 128 two fit without it (167 registers); with it the compiler spills (96 requests of
 // 1000 tokens, 16 rows: 73 us without, 80 with; asking for one block, which takes 214, 91).
-template <typename T, int D, bool kSmall>
-__global__ void __launch_bounds__(kPagedThreads, D == 256 ? 1 : D == 64 ? 3 : kSmall ? 2 : 0)
+template <typename T, int D, bool kSmall, bool kMany>
+__global__ void __launch_bounds__(kPagedThreads, D == 256 ? 1 : D == 64 || kMany ? 3 : kSmall ? 2 : 0)
     split_kernel(const __grid_constant__ PagedParams p) {
-  using C = SplitCfg<D>;
+  using C = SplitCfg<D, kMany>;
   extern __shared__ __align__(1024) uint8_t stages[];
   float* join = reinterpret_cast<float*>(stages + C::kStages * C::kStageBytes);
   static_assert(sizeof(SplitShared) <= C::kSharedBytes, "SplitShared");
@@ -782,16 +783,16 @@ static int64_t most_runs(const PagedParams& p) {
   return p.H * (p.q_off ? (int64_t)p.n_q * p.G / p.run_rows + p.n_req : p.n_req * each);
 }
 
-template <typename T, int D, bool kSmall>
+template <typename T, int D, bool kSmall, bool kMany>
 static cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
-  using C = SplitCfg<D>;
+  using C = SplitCfg<D, kMany>;
   static DeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(split_kernel<T, D, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return cudaFuncSetAttribute(split_kernel<T, D, kSmall, kMany>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
   const int blocks = p.whole ? (int)most_runs(p) : min(device_sms() * C::kBlocksPerSm, kPagedMaxBlocks);
-  e = launch_early(split_kernel<T, D, kSmall>, blocks, kPagedThreads, C::kSmem, stream, p);
+  e = launch_early(split_kernel<T, D, kSmall, kMany>, blocks, kPagedThreads, C::kSmem, stream, p);
   if (e != cudaSuccess || p.whole || blocks == 1) return e;
   // the fold's blocks may start while the last ranges still run: they wait for them
   const int rows = p.q_off ? p.run_rows : min(p.G, p.run_rows);
@@ -800,7 +801,16 @@ static cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
 
 template <typename T, int D>
 static cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
-  return p.run_rows == 8 ? launch_t<T, D, true>(p, stream) : launch_t<T, D, false>(p, stream);
+  if constexpr (D == 128) {
+    // A third block per SM, of two stages instead of three, for whole runs: 40 requests of 1500
+    // tokens, 8 heads, one wave instead of two, 51 -> 41 us; 400 of 250, 84 -> 75; not where its
+    // waves leave more of the device idle (64 of 1500, 512 runs: 62 and 74), nor where runs are
+    // cut (96 of 5000: 290 and 296).
+    auto waves = [&](int64_t blocks) { return (most_runs(p) + blocks * kTileBlocks - 1) / (blocks * kTileBlocks); };
+    if (p.run_rows == 8 && p.whole && waves(2) > 1 && 15 * waves(3) <= 11 * waves(2))
+      return launch_t<T, D, true, true>(p, stream);
+  }
+  return p.run_rows == 8 ? launch_t<T, D, true, false>(p, stream) : launch_t<T, D, false, false>(p, stream);
 }
 
 template <typename T>
