@@ -88,6 +88,15 @@ def test_many_rows(n, most, H, G, pages, D):
     run(lens, H, G, D, "bf16", seed=G, max_pages=pages)
 
 
+@pytest.mark.parametrize("n,D", [(110, 128), (130, 64), (130, 128), (110, 64)])
+def test_waves_of_whole_runs(n, D):
+    """One block per SM more or not; windows, bad pages, empty requests among them."""
+    lens = [(i * 137) % 700 for i in range(n)]
+    begin = [max(0, x - 200) if i % 3 == 0 else 0 for i, x in enumerate(lens)]
+    lens[7], begin[7] = 690, 0
+    run(lens, 4, 3, D, "f16", begin=begin, o_f32=True, mute=[(7, 1), (7, 10)], status=(4, 1), o_gap=8)
+
+
 @pytest.mark.parametrize("pages", [24, 40])
 def test_many_rows_windows_and_bad_pages(pages):
     n = 24

@@ -35,15 +35,15 @@ constexpr float kEmpty = -__builtin_huge_valf();
 constexpr int kConsumers = 4;
 constexpr int kPagedThreads = (kConsumers + 1) * 32;
 
-template <int D, bool kMany>  // kMany: three blocks per SM at D = 128
+template <int D, bool kMany>  // kMany: a block per SM more, of a stage less
 struct SplitCfg {
-  static_assert(!kMany || D == 128, "kMany");
+  static_assert(!kMany || D <= 128, "kMany");
   static constexpr int kPageBytes = kPageTokens * D * 2;   // keys or values of one page
   static constexpr int kStageBytes = 2 * kPageBytes;
   static constexpr int kBoxBytes = kBoxRows * D * 2;       // one warp's keys or values
-  static constexpr int kStages = D == 64 ? 4 : kMany ? 2 : 3;
-  static constexpr int kBlocksPerSm = kMany ? 3 : split_blocks(D);
-  static constexpr int kJoin = D == 256 ? 256 : 64;  // channels joined at a time
+  static constexpr int kStages = (D == 64 ? 4 : 3) - kMany;
+  static constexpr int kBlocksPerSm = split_blocks(D) + kMany;
+  static constexpr int kJoin = D == 256 ? 256 : D == 64 && kMany ? 32 : 64;  // channels joined at a time
   // floats a row, which spread the 8 rows (or the 4 lanes' row pairs) over the banks
   template <bool kSmall>
   static constexpr int kJoinStride = kJoin + (kSmall ? 4 : 8);
@@ -374,7 +374,7 @@ struct Rows {
 // D = 128 two fit without it (167 registers); with it the compiler spills (96 requests of
 // 1000 tokens, 16 rows: 73 us without, 80 with; asking for one block, which takes 214, 91).
 template <typename T, int D, bool kSmall, bool kMany>
-__global__ void __launch_bounds__(kPagedThreads, D == 256 ? 1 : D == 64 || kMany ? 3 : kSmall ? 2 : 0)
+__global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split_blocks(D) + kMany)
     split_kernel(const __grid_constant__ PagedParams p) {
   using C = SplitCfg<D, kMany>;
   extern __shared__ __align__(1024) uint8_t stages[];
@@ -801,13 +801,14 @@ static cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
 
 template <typename T, int D>
 static cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
-  if constexpr (D == 128) {
-    // A third block per SM, of two stages instead of three, for whole runs: 40 requests of 1500
-    // tokens, 8 heads, one wave instead of two, 51 -> 41 us; 400 of 250, 84 -> 75; not where its
-    // waves leave more of the device idle (64 of 1500, 512 runs: 62 and 74), nor where runs are
-    // cut (96 of 5000: 290 and 296).
+  if constexpr (D <= 128) {
+    // A block per SM more, of a stage less, for whole runs: 40 requests of 1500 tokens, 8 heads of
+    // 128, one wave instead of two, 51 -> 41 us; 64 of 1500, heads of 64, 44 -> 34; 400 of 250, 128,
+    // 84 -> 75; not where its waves leave more of the device idle (64 of 1500, 128: 62 and 74),
+    // nor where runs are cut (96 of 5000, 128: 290 and 296).
+    constexpr int kFew = split_blocks(D);
     auto waves = [&](int64_t blocks) { return (most_runs(p) + blocks * kTileBlocks - 1) / (blocks * kTileBlocks); };
-    if (p.run_rows == 8 && p.whole && waves(2) > 1 && 15 * waves(3) <= 11 * waves(2))
+    if (p.run_rows == 8 && p.whole && waves(kFew) > 1 && 10 * (kFew + 1) * waves(kFew + 1) <= 11 * kFew * waves(kFew))
       return launch_t<T, D, true, true>(p, stream);
   }
   return p.run_rows == 8 ? launch_t<T, D, true, false>(p, stream) : launch_t<T, D, false, false>(p, stream);
