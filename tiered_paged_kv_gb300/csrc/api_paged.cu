@@ -91,16 +91,16 @@ tpk_status make_maps(PagedParams& p, const tpk_paged_shape* s, const void* k_poo
   return st == TPK_OK ? make_map(&p.vmap, s->dtype, rank, v_pool, dims, strides, box) : st;
 }
 
-// Workspace of a split launch: the numbering table, then the partials.
-size_t split_ws_bytes(const tpk_paged_shape* s, int n_req) {
+// Workspace of a split launch: the records of the runs to join, then the partials.
+size_t split_ws_bytes(const tpk_paged_shape* s) {
   const size_t slots = 2 * (size_t)kPagedMaxBlocks * kRowTile;
-  return align256((size_t)(n_req + 1) * 8) + align256(2 * slots * 4) + slots * s->head_dim * 4;
+  return align256(kPagedMaxBlocks * sizeof(RunCut)) + align256(2 * slots * 4) + slots * s->head_dim * 4;
 }
 
-void place_ws(PagedParams& p, int n_req, void* ws) {
+void place_ws(PagedParams& p, void* ws) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  p.prefix = reinterpret_cast<int64_t*>(w);
-  w += align256((size_t)(n_req + 1) * 8);
+  p.cuts = reinterpret_cast<RunCut*>(w);
+  w += align256(kPagedMaxBlocks * sizeof(RunCut));
   p.part_ml = reinterpret_cast<float*>(w);
   w += align256(4 * (size_t)kPagedMaxBlocks * kRowTile * 4);
   p.part_o = reinterpret_cast<float*>(w);
@@ -159,7 +159,7 @@ CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
 
 size_t cross_ws_bytes(const tpk_paged_shape* s, int n_req, int n_q) {
   const CrossPlan c = cross_plan(s, n_req, n_q);
-  if (c.groups == 0) return split_ws_bytes(s, n_req);
+  if (c.groups == 0) return split_ws_bytes(s);
   if (c.splits == 1) return 256;
   const size_t rows = (size_t)c.rows(s);
   return align256(rows * 8) + rows * s->head_dim * 4;
@@ -313,7 +313,7 @@ tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const 
 }
 
 size_t tpk_decode_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req) {
-  return sized(shape, n_req) ? split_ws_bytes(shape, n_req) : 0;
+  return sized(shape, n_req) ? split_ws_bytes(shape) : 0;
 }
 
 tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const void* q, int64_t q_stride,
@@ -328,7 +328,7 @@ tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const 
                        tpk_decode_paged_workspace_bytes(shape, n_req));
   if (st == TPK_OK) st = make_maps(p, shape, k_pool, v_pool, true);
   if (st != TPK_OK) return st;
-  place_ws(p, n_req, ws);
+  place_ws(p, ws);
   p.begin = tok_begin;
   p.o_f32 = o_f32;
   p.n_q = n_req;
@@ -362,7 +362,7 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
   if (st != TPK_OK) return st;
   cudaError_t e;
   if (plan.groups == 0) {
-    place_ws(p, n_req, ws);
+    place_ws(p, ws);
     e = launch_paged_split(p, shape->head_dim, shape->dtype, reinterpret_cast<cudaStream_t>(stream));
   } else {
     const int64_t rows = plan.rows(shape);

@@ -384,11 +384,14 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (smem_u32(stages) & 1023) {  // the swizzle counts on it
     wait_before();
-    if (tid == 0) atomicOr(p.status, kStatusTimeout);
+    if (tid == 0) {
+      atomicOr(p.status, kStatusTimeout);
+      if (!p.whole) p.cuts[blockIdx.x].parts = 0;
+    }
     return;
   }
 
-  // ---- the numbering: this block's range, and (block 0) the table for the fold
+  // ---- the numbering: this block's range
   if (tid == kConsumers * 32) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.kmap) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.vmap) : "memory");
@@ -400,6 +403,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
   }
   wait_before();
   Walk walk;
+  int64_t per = 0;  // numbers of a range
   if (p.whole) {
     // a block per run: nothing to join, and nothing to number if every request has as many
     int64_t run;
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
     if (p.n_req <= kScanned) {
       Numbers numbers;
       numbers.load(p, request_units);
-      const int64_t per = per_block(numbers.total, gridDim.x);
+      per = per_block(numbers.total, gridDim.x);
       lo = min(per * blockIdx.x, numbers.total);
       hi = min(lo + per, numbers.total);
       if (lo < hi) numbers.find(lo, walk.b, walk.base);
@@ -462,28 +466,27 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
         if (w < warp) before += S.scan[w];
         total += S.scan[w];
       }
-      const int64_t per = per_block(total, gridDim.x);
+      per = per_block(total, gridDim.x);
       lo = min(per * blockIdx.x, total);
       hi = min(lo + per, total);
-      if ((lo < hi && lo >= before && lo < before + mine) || blockIdx.x == 0) {
+      if (lo < hi && lo >= before && lo < before + mine) {
         int64_t at = before;
         for (int b = b0; b < b1; ++b) {
           const int64_t work = request_units(p, b);
-          if (lo < hi && lo >= at && lo < at + work) {
+          if (lo >= at && lo < at + work) {
             S.first = b;
             S.base = at;
           }
-          if (blockIdx.x == 0) p.prefix[b] = at;
           at += work;
         }
       }
-      if (blockIdx.x == 0 && tid == 0) p.prefix[p.n_req] = total;
       __syncthreads();
       walk.b = S.first;
       walk.base = S.base;
     }
     walk.at = lo;
     walk.end = hi;
+    if (tid == 0) p.cuts[blockIdx.x].parts = 0;  // until this block leaves a run before its end
 
   // ---- requests that attend nothing
   for (int b = blockIdx.x; b < p.n_req; b += gridDim.x) {
@@ -626,6 +629,9 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
       int token, head;
       const bool write = run_row(p, first, count, h, tile, r, token, head) && !dead;
       const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+      // the join's record: this block has the run's first page and not its last
+      if (tid == 0 && pass == 0 && !whole && s.page == 0)
+        p.cuts[blockIdx.x] = {first, count, h, tile, (int)((s.pages - s.count - 1) / per) + 2};
       if (write && tid % kPer == 0) {
         if (whole) {
           p.lse[(int64_t)token * HQ + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
@@ -664,64 +670,30 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
   }
 }
 
-// Joins the partials of the runs that cross block ranges: block (i, r) takes row r of
-// the run that holds the first number of range i + 1, if the run's first page is in range
-// i.  The
+// Joins the partials of the runs that cross block ranges: block (i, r) takes row r of the
+// run that range i begins and leaves, if there is one (its record).  It reads nothing before
+// its wait: only there are the writes of the launches before it sure to be seen.  The
 // partials' maxima are read at once, one a thread; then every thread sums its four
 // channels over the partials in block order, eight loads in flight.
-constexpr int kFoldParts = 64;  // weights held at a time
+constexpr int kFoldParts = 64;  // weights held at a time, one a thread
 template <typename T, int D>
 __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ PagedParams p, int blocks, int rows) {
   __shared__ float weight[kFoldParts];
   __shared__ float red[2];
   const int i = blockIdx.x / rows, r = blockIdx.x % rows, tid = threadIdx.x;
-  // ---- which run: from the lengths where they are few, before the partials are there
-  int64_t total, base = 0;
-  int b = 0;
-  Numbers numbers;
-  if (p.n_req <= kScanned) {
-    numbers.load(p, request_units);
-    total = numbers.total;
-  } else {
-    wait_before();
-    total = p.prefix[p.n_req];
-  }
-  const int64_t per = per_block(total, blocks);
-  const int64_t cut = per * (i + 1);
-  bool mine = cut < total;
-  int n = 0, token = 0, head = 0;
-  if (mine) {
-    if (p.n_req <= kScanned) {
-      numbers.find(cut, b, base);
-    } else {
-      int lo = 0, hi = p.n_req - 1;
-      while (lo < hi) {  // the request that holds number `cut`
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.prefix[mid] <= cut) lo = mid; else hi = mid - 1;
-      }
-      b = lo;
-      base = p.prefix[b];
-    }
-    int lo, hi, first, count;
-    const int units = request_pages(p, b, lo, hi) + kRunCost;
-    const int run = (int)((cut - base) / units);
-    const int64_t end = base + (int64_t)(run + 1) * units, start = end - units + kRunCost;  // its pages
-    mine = start < cut && start >= per * i;  // crossed here, and not joined at an earlier cut
-    request_rows(p, b, first, count);
-    const int tiles = request_runs(p, b) / p.H;
-    const int h = run / tiles;
-    mine = mine && run_row(p, first, count, h, run - h * tiles, r, token, head);
-    n = (int)((end - 1) / per) - i + 1;  // blocks i .. i + n - 1 hold a piece
-  }
-  // every block waits, whether it has a row or not: the launch must not end before the
-  // one whose partials it joins
-  if (p.n_req <= kScanned) wait_before();
-  if (!mine) return;
   // block i left the run before its end, the others entered it in the middle
   auto slot = [&](int k) { return (2 * (int64_t)(i + k) + (k == 0 ? 1 : 0)) * kRowTile + r; };
   const float* part_l = p.part_ml + 2 * (int64_t)blocks * kRowTile;
-  float M = kEmpty;
-  for (int k = tid; k < n; k += 64) M = fmaxf(M, p.part_ml[slot(k)]);
+  wait_before();
+  // the first partials' statistics, on their way together with the record
+  const bool may = i + tid < blocks;
+  const float m0 = may ? p.part_ml[slot(tid)] : kEmpty, l0 = may ? part_l[slot(tid)] : 0.f;
+  const RunCut cut = p.cuts[i];
+  const int n = cut.parts;  // blocks i .. i + n - 1 hold a piece
+  int token, head;
+  if (n == 0 || !run_row(p, cut.first, cut.count, cut.h, cut.tile, r, token, head)) return;
+  float M = tid < n ? m0 : kEmpty;
+  for (int k = tid + 64; k < n; k += 64) M = fmaxf(M, p.part_ml[slot(k)]);
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   if ((tid & 31) == 0) red[tid >> 5] = M;
@@ -737,8 +709,8 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
   for (int k0 = 0; k0 < n; k0 += kFoldParts) {
     const int cnt = min(kFoldParts, n - k0);
     __syncthreads();
-    if (tid < cnt) weight[tid] = exp2f(p.part_ml[slot(k0 + tid)] - ref);
-    float mine = tid < cnt ? weight[tid] * part_l[slot(k0 + tid)] : 0.f;
+    if (tid < cnt) weight[tid] = exp2f((k0 == 0 ? m0 : p.part_ml[slot(k0 + tid)]) - ref);
+    float mine = tid < cnt ? weight[tid] * (k0 == 0 ? l0 : part_l[slot(k0 + tid)]) : 0.f;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
     __syncthreads();

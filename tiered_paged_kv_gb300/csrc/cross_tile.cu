@@ -932,7 +932,9 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
   }
 }
 
-// Joins the parts of a split launch, one warp per row of a tile group.
+// Joins the parts of a split launch, one warp per row of a tile group, kJoined parts' values in
+// flight.
+constexpr int kJoined = 4;
 template <typename T, int D, int kT>
 __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ PagedParams p, int splits) {
   using C = TileCfg<D, kT>;
@@ -940,37 +942,69 @@ __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ 
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int r = (int)(w % C::kRows);
   const int h = (int)(w / C::kRows % p.H);
-  int want = (int)(w / C::kRows / p.H), b = 0, first = 0, count = 0;
-  for (; b < p.n_req; ++b) {
-    request_rows(p, b, first, count);
-    const int n = (count + C::kTiles * per_tile - 1) / (C::kTiles * per_tile);
-    if (want < n) break;
-    want -= n;
+  int want = (int)(w / C::kRows / p.H), first = 0, count = 0;
+  const int64_t group = w / C::kRows;  // (tile group, head)
+  auto at = [&](int k) { return (group * splits + k) * C::kRows + r; };
+  wait_before();  // nothing is read before it
+  // a part's (maximum, sum) a lane, and the first parts' values, on their way while the row's
+  // request is looked up
+  float2 ml = make_float2(kNone, 0.f), v[kJoined][D / 64];
+  if (lane < splits) ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at(lane));
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int j = 0; j < kJoined; ++j)
+      if (k0 + j < splits)
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e)
+          v[j][e] = *reinterpret_cast<const float2*>(p.part_o + at(k0 + j) * D + e * 64 + 2 * lane);
+  };
+  load(0);
+  // ---- the row's request: 32 at a time, their tile groups added up
+  bool found = false;
+  for (int b0 = 0; b0 < p.n_req && !found; b0 += 32) {
+    int a = 0, c = 0;
+    if (b0 + lane < p.n_req) request_rows(p, b0 + lane, a, c);
+    const int groups = (c + C::kTiles * per_tile - 1) / (C::kTiles * per_tile);
+    int inc = groups;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += up;
+    }
+    const uint32_t here = __ballot_sync(0xffffffffu, want < inc);
+    found = here != 0;
+    const int src = found ? __ffs(here) - 1 : 31;
+    first = __shfl_sync(0xffffffffu, a, src);
+    count = __shfl_sync(0xffffffffu, c, src);
+    want -= __shfl_sync(0xffffffffu, found ? inc - groups : inc, src);
   }
   const int x = r % kTileRows / p.G;
   const int t = (want * C::kTiles + r / kTileRows) * per_tile + x;
-  // every block waits, whether it has a row or not: the launch must not end before the
-  // one whose parts it joins
-  wait_before();
-  if (b == p.n_req || x >= per_tile || t >= count) return;
+  if (!found || x >= per_tile || t >= count) return;
   const int token = first + t, head = h * p.G + r % kTileRows - x * p.G;
-  const int64_t group = w / C::kRows;  // (tile group, head)
-  auto at = [&](int k) { return (group * splits + k) * C::kRows + r; };
-  float M = kNone;
-  for (int k = 0; k < splits; ++k) M = fmaxf(M, p.part_ml[2 * at(k)]);
+  float M = ml.x;
+  for (int k = lane + 32; k < splits; k += 32) M = fmaxf(M, p.part_ml[2 * at(k)]);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   float L = 0.f, o[D / 32];
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-  for (int k = 0; k < splits; ++k) {
-    const float m = p.part_ml[2 * at(k)];
-    if (m == kNone) continue;
-    const float f = exp2f(m - M);
-    L += f * p.part_ml[2 * at(k) + 1];
+  for (int k0 = 0; k0 < splits; k0 += kJoined) {
+    if (k0 > 0) load(k0);
+    if (k0 > 0 && (k0 & 31) == 0 && k0 + lane < splits)
+      ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at(k0 + lane));
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) {
-      const float2 v = *reinterpret_cast<const float2*>(p.part_o + at(k) * D + e * 64 + 2 * lane);
-      o[2 * e] += f * v.x;
-      o[2 * e + 1] += f * v.y;
+    for (int j = 0; j < kJoined; ++j) {
+      if (k0 + j >= splits) break;
+      const float m = __shfl_sync(0xffffffffu, ml.x, (k0 + j) & 31), l = __shfl_sync(0xffffffffu, ml.y, (k0 + j) & 31);
+      if (m == kNone) continue;
+      const float f = exp2f(m - M);
+      L += f * l;
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        o[2 * e] += f * v[j][e].x;
+        o[2 * e + 1] += f * v[j][e].y;
+      }
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;

@@ -50,6 +50,12 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, int interleaved, cudaStr
 
 // --------------------------------------------------------------- attention
 constexpr int kBoxRows = 16;  // rows of a page in one copy of the split kernel: one warp's
+// A run that crosses ranges of a split launch, as its first block records it for the join.
+struct __align__(16) RunCut {
+  int first, count;  // the request's query rows
+  int h, tile;       // the run's KV head, and its number within the request's rows
+  int parts;         // blocks that hold a piece of it; 0: no such run
+};
 struct PagedParams {
   // pools with the 128-byte swizzle.  Row tiles: [slot * H * 64][D], boxes of 64 rows x 64
   // channels; split kernel: [D / 64][slot * H * 64][64], boxes of all channels of kBoxRows rows
@@ -64,7 +70,7 @@ struct PagedParams {
   const int32_t* begin;  // decode: first token attended, or null
   const int32_t* q_off;  // cross: where each request's query rows begin; null: decode
   const int32_t* range;  // cross: [n_q][2] or null
-  int64_t* prefix;       // workspace: pages of work before each request
+  RunCut* cuts;          // workspace: of each block
   float* part_ml;        // workspace: [slot][16] running maximum, then [slot][16] sum
   float* part_o;         // workspace: [slot][16][D], not normalised
   int* status;
@@ -177,8 +183,8 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
 // wait here for its results before they read or write anything.  Every block waits, whether it
 // has work or not: a launch must not end before the one it waits for.
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the next launch start; after wait_before, so that what it reads before its own wait was
-// written two launches back.
+// Lets the next launch start.  It may read what this one reads or writes only after its own wait:
+// this launch's wait shows the results before it to this launch alone.
 __device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void named_barrier(int id, int threads) {
