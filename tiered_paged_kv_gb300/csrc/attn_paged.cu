@@ -620,12 +620,13 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
 #pragma unroll
     for (int pass = 0; pass < (kSmall ? 1 : 2); ++pass) {
       const int row = tid / kPer, r = row + 8 * pass;
+      // A maximum skips NaN, a sum does not: a row whose scores are NaN has no maximum, yet a sum
+      // that is not 0, which tells it from a row that sees nothing.
       float M = kEmpty, L = 0.f;
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, S.m[w][r]);
 #pragma unroll
-      for (int w = 0; w < kConsumers; ++w)
-        if (S.m[w][r] != kEmpty) L += exp2f(S.m[w][r] - M) * S.l[w][r];
+      for (int w = 0; w < kConsumers; ++w) L += exp2f(S.m[w][r] - (M == kEmpty ? 0.f : M)) * S.l[w][r];
       int token, head;
       const bool write = run_row(p, first, count, h, tile, r, token, head) && !dead;
       const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
