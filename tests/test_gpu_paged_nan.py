@@ -53,8 +53,17 @@ def test_decode(lens, H, G, pages, D):
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("nq,lens,H,G", [([3, 2], [100, 300], 1, 4), ([4, 3], [5000, 64], 1, 2),  # split kernel
-                                         ([200, 150], [300, 70], 64, 1)],                    # row tiles
+                                         ([200, 150], [300, 70], 64, 1),                     # row tiles
+                                         ([300, 20], [2000, 700], 1, 2), ([40, 130], [900, 3000], 1, 3)],  # keys split
                          ids=lambda x: "-".join(map(str, x)) if isinstance(x, list) else str(x))
 def test_cross(nq, lens, H, G, D):
     c = Cross(Pages(lens, H, D, "f16", 4), nq, G)
     poison(c, range(0, c.T, 3), [0, H * G - 1], c.T)
+
+
+def test_cross_ranges_with_split_keys():
+    """A row that sees nothing beside a NaN row: one is empty, the other is not."""
+    r = [(0, 0) if i % 4 == 1 else (i * 3, i * 3 + 500) for i in range(300)]
+    c = Cross(Pages([2000], 1, 128, "bf16", 5), [300], 2, ranges=r)
+    poison(c, range(0, 300, 4), [1], 300)
+    assert (c.lse[1::4] == float("-inf")).all() and (c.o[1::4] == 0).all()

@@ -877,7 +877,8 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       }
       const int64_t at = (int64_t)it.id * C::kRows + hrow;  // this part's row in the workspace
       const float inv = splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      const bool write = live && ok && !(splits > 1 && m == kNone);  // the fold does not read an empty part
+      // the fold does not use an empty part (by its sum: one of NaN scores has no maximum either)
+      const bool write = live && ok && !(splits > 1 && l == 0.f);
       if (live && ok && half == 0) {
         if (splits > 1) {
           p.part_ml[2 * at] = m;
@@ -997,8 +998,8 @@ __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ 
     for (int j = 0; j < kJoined; ++j) {
       if (k0 + j >= splits) break;
       const float m = __shfl_sync(0xffffffffu, ml.x, (k0 + j) & 31), l = __shfl_sync(0xffffffffu, ml.y, (k0 + j) & 31);
-      if (m == kNone) continue;
-      const float f = exp2f(m - M);
+      if (l == 0.f) continue;
+      const float f = exp2f(m - M);  // NaN where no part has a maximum: what sums there are are NaN
       L += f * l;
 #pragma unroll
       for (int e = 0; e < D / 64; ++e) {
