@@ -15,8 +15,13 @@ __global__ void __launch_bounds__(kHeadDim) merge_kernel(int n_parts, int rows, 
   const float ninf = -__builtin_huge_valf();
   float la = lse_acc[row];
   float M = la;
-  for (int i = 0; i < n_parts; ++i) M = fmaxf(M, lse_parts[(int64_t)i * rows + row]);
-  if (M == ninf) return;  // everything empty: the accumulator (0, -inf) stays as it is
+  bool empty = la == ninf;  // by every part: a maximum skips NaN
+  for (int i = 0; i < n_parts; ++i) {
+    const float li = lse_parts[(int64_t)i * rows + row];
+    M = fmaxf(M, li);
+    empty = empty && li == ninf;
+  }
+  if (empty) return;  // the accumulator (0, -inf) stays as it is
   float L = (la == ninf) ? 0.f : expf(la - M);
   for (int i = 0; i < n_parts; ++i) {
     float li = lse_parts[(int64_t)i * rows + row];
