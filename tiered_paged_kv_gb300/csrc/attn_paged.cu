@@ -19,9 +19,9 @@
 // ends.  Boxes outside the request's span are neither copied nor computed: 96 windows of
 // 1000 tokens, 8 x 5 heads of 128, 66.9 -> 64.4 us.
 // Both products run on mma.sync m16n8k16 with float32 accumulators (struct Rows).  The
-// weights enter PV as two 16-bit planes (the rounded weight and what the rounding left,
-// about 16 bits in bfloat16), so they add no error of their own next to the rounding of the
-// output.  A tensor tile of 128 rows would hold 8 or 16 useful ones; the few rows make the
+// weights enter PV as two 16-bit planes (the rounded weight and what the rounding left:
+// about 16 bits in bfloat16; 22 in float16, and at its lower end 2^-40 of the largest weight),
+// so they add no error of their own next to the rounding of the output.  A tensor tile of 128 rows would hold 8 or 16 useful ones; the few rows make the
 // kernel bound by HBM (4 H D bytes per attended token against 4 H G D operations).
 //
 // Measured: 16 requests of 32,000 tokens at head sizes 64, 128, 256: 6.8, 6.9, 6.9 TB/s; one
@@ -313,6 +313,7 @@ struct Rows {
       l[e] += sum;
     }
     // ---- o += weights * values, in two planes: the rounded weights, and what that left
+    constexpr float kScale = 1 << T::kWeightBits;  // put takes it out again
     uint32_t hi[4], lw[4];
 #pragma unroll
     for (int i = 0; i < (kSmall ? 2 : 4); ++i) {
@@ -324,6 +325,8 @@ struct Rows {
         a = x[i & 1][i & 2];
         b = x[i & 1][(i & 2) + 1];
       }
+      a *= kScale;
+      b *= kScale;
       hi[i] = T::pack(a, b);
       const float2 back = T::unpack(hi[i]);
       lw[i] = T::pack(a - back.x, b - back.y);
@@ -351,7 +354,7 @@ struct Rows {
     }
   }
 
-  // Puts kJoin channels from c0 on, scaled, into `to` (8 rows of `stride` floats): the run's
+  // Puts kJoin channels from c0 on, times f, into `to` (8 rows of `stride` floats): the run's
   // rows 8 pass .. 8 pass + 7.
   template <int kJoin>
   __device__ __forceinline__ void put(float* to, int stride, int c0, int pass, const float (&f)[2]) const {
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
       float top = kEmpty;
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, S.m[w][rows.row(e)]);
-      f[e] = rows.m[e] == kEmpty ? 0.f : exp2f(rows.m[e] - top);
+      f[e] = (rows.m[e] == kEmpty ? 0.f : exp2f(rows.m[e] - top)) * (1.f / (1 << T::kWeightBits));
     }
     constexpr int kPer = kConsumers * 4, kStride = C::template kJoinStride<kSmall>;
 #pragma unroll

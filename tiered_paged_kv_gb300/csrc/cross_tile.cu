@@ -21,9 +21,10 @@
 // in order, so QK(i + 2) may overwrite the buffer that PV(i) reads its weights from.
 // PV(i) starts on half of each row's weights while the other half is being formed.
 //
-// The reference maximum of a row moves only when the running maximum has grown by more
-// than 2^8 (weights then stay below 256, exact in range for both types), so the pass that
-// rescales O in TMEM is rare.  Weights are rounded once to the input type -- as the
+// The reference of a row's weights moves only when its maximum has grown by more than 2^8
+// (2^4 in float16), so the pass that rescales O in TMEM is rare.  In float16 it stands 2^11
+// below the maximum it was taken from: weights stay below 2^15, and those far below the
+// maximum are held to 2^-36 of it (struct F16).  Weights are rounded once to the input type -- as the
 // tensor core needs them beside V -- while their sum is kept unrounded in float32: the
 // rounding of a weight is of the size of the output's own.
 //
@@ -40,7 +41,11 @@
 namespace tpk {
 
 constexpr float kNone = -__builtin_huge_valf();
-constexpr float kSlack = 8.f;  // log2 of the largest weight
+// log2 of a row's largest weight over its reference, and of how much more it may become
+template <typename T>
+constexpr int kLift = T::kWeightBits > 0 ? T::kWeightBits - 4 : 0;
+template <typename T>
+constexpr int kSlack = T::kWeightBits > 0 ? 4 : 8;
 constexpr int kKeys = 128;     // tokens of a key tile
 constexpr uint32_t kTmemCols = 512;
 
@@ -817,11 +822,11 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         ok = ok && !__any_sync(0xffffffffu, other != other);
         if (!ok) break;
         const float mt = fmaxf(mine, other) * qscale;
-        const bool grow = mt > m + kSlack || (m == kNone && mt > kNone);
+        const bool grow = mt - m > kLift<T> + kSlack<T>;  // not where both are -inf
         if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? ex2(m - mt) : 1.f;
+          const float to = mt - kLift<T>, f = grow ? ex2(m - to) : 1.f;
           l *= f;
-          if (grow) m = mt;
+          if (grow) m = to;
           if (n > 0) {
             // the product before these weights has ended: with two tiles it came before
             // the scores just read

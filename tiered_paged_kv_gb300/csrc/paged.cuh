@@ -117,7 +117,11 @@ cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int tiles
                                cudaStream_t stream);
 
 // ------------------------------------------------------------------- types
+// kWeightBits: weights, at most 1, enter the product with the values times 2^kWeightBits.  float16
+// steps by 2^-24 at its lower end, and many weights below that may count together: scaled by 2^15
+// they fill its range (largest value 65,504).  bfloat16 has float32's range and needs no scale.
 struct Bf16 {
+  static constexpr int kWeightBits = 0;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
@@ -131,6 +135,7 @@ struct Bf16 {
   }
 };
 struct F16 {
+  static constexpr int kWeightBits = 15;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
