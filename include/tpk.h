@@ -557,7 +557,10 @@ tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const 
  *   n_tokens   dev int32 [n_req] (clamped as above); kv_range: dev int32 [n_q][2] or NULL
  *   o          dev [n_q] rows of o_stride elements, of shape->dtype; lse: dev float32
  *              [n_q][H*G]
- * States within n_tokens[b] must be finite; pool rows past it may hold anything.
+ * States within n_tokens[b] must be finite; pool rows past it may hold anything.  Scores
+ * (sm_scale times a query times a state) past 2^22 in size in float16, 2^28 in bfloat16, whose
+ * differences float32 no longer holds, may turn their row's o and lse into NaN; they never leave
+ * a row finite and wrong.
  * ws: dev workspace of tpk_cross_paged_workspace_bytes(shape, n_req, n_q) bytes (no
  * initialisation); calls sharing one must not overlap on the GPU.  n_req in [1, 4096];
  * n_q >= 0 (0 is a no-op).  Strides, errors and capture as for tpk_decode_attn_paged.

@@ -46,6 +46,15 @@ template <typename T>
 constexpr int kLift = T::kWeightBits > 0 ? T::kWeightBits - 4 : 0;
 template <typename T>
 constexpr int kSlack = T::kWeightBits > 0 ? 4 : 8;
+// References from here on are refused: the maximum is rounded when it is scaled, the scores are not
+// (a fused step forms scaled score - reference), so a weight may be 2^(half a float32 step) over the
+// largest meant.  At 2^23 that is 2^0.5 and float16 still holds it, at 2^29 2^32 (bfloat16); further
+// out weights pass the type's range or all vanish.  Such a row becomes NaN, o and lse.  (Scaling and
+// rounding the scores first where references are large cost the prompts 2-3 % wherever it was put.)
+template <typename T>
+__device__ __forceinline__ bool far_off(float m) {
+  return fabsf(m) >= (T::kWeightBits > 0 ? 0x1p23f : 0x1p29f) && m != kNone;
+}
 constexpr int kKeys = 128;     // tokens of a key tile
 constexpr uint32_t kTmemCols = 512;
 
@@ -824,7 +833,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         const float mt = fmaxf(mine, other) * qscale;
         const bool grow = mt - m > kLift<T> + kSlack<T>;  // not where both are -inf
         if (__any_sync(0xffffffffu, grow)) {
-          const float to = mt - kLift<T>, f = grow ? ex2(m - to) : 1.f;
+          const float to = mt - kLift<T>, f = !grow ? 1.f : far_off<T>(m) ? __int_as_float(0x7fffffff) : ex2(m - to);
           l *= f;
           if (grow) m = to;
           if (n > 0) {
@@ -877,6 +886,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         told(0, half) = l;
         named_barrier(1 + pair, 64);
         l += told(0, half ^ 1);
+        if (far_off<T>(m)) l = __int_as_float(0x7fffffff);
         ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[tile], items++ & 1, p.status, p.wait_ns)) != 0;
         tc_fence_after();
       }
