@@ -33,6 +33,7 @@ int* device_status_word();
 int device_sms();
 void* tensor_map_encoder();
 uint64_t wait_limit_ns();
+int stall_unit();
 }  // namespace tpk
 
 namespace {
@@ -261,7 +262,7 @@ tpk_status launch_decode(const tpk_shape* s, const DecodeParams& p, const ReqPla
 void tpk::set_error(const char* msg) { g_err = msg; }
 
 // For the other translation units: the status word and SM count of the current
-// device, the tensor-map encoder and the limit of the bounded waits.
+// device, the tensor-map encoder, the limit of the bounded waits and the stalled block.
 int* tpk::device_status_word() { return status_ptr(); }
 int tpk::device_sms() { return num_sms(); }
 void* tpk::tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
@@ -269,6 +270,7 @@ uint64_t tpk::wait_limit_ns() {
   const uint64_t w = g_test_wait_ns.load(std::memory_order_relaxed);
   return w > 0 ? w : kWaitLimitNs;
 }
+int tpk::stall_unit() { return g_test_stall_unit.load(std::memory_order_relaxed); }
 
 extern "C" {
 

@@ -16,6 +16,7 @@ void set_error(const char* msg);
 int* device_status_word();
 void* tensor_map_encoder();
 uint64_t wait_limit_ns();
+int stall_unit();
 }  // namespace tpk
 
 using namespace tpk;
@@ -197,6 +198,7 @@ tpk_status begin_attention(PagedParams& p, const tpk_paged_shape* s, int n_req, 
   p.o_stride = o_stride;
   p.kv_slots = s->kv_slots;
   p.wait_ns = wait_limit_ns();
+  p.stall_unit = stall_unit();
   const float scale = s->sm_scale == 0.f ? 1.f / std::sqrt((float)s->head_dim) : s->sm_scale;
   p.qscale = scale * kLog2e;
   p.n_req = n_req;

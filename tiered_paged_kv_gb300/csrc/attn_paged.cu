@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
   Segment s;
   if (warp == kConsumers) {
     // ------------------------------------------------------------- producer
+    const bool stalled = (int)blockIdx.x == p.stall_unit;
     int item = 0;
     bool dead = false;
     while (!dead && walk.next(p, s)) {
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
               break;
             }
           }
-          if (elect_one()) {
+          if (elect_one() && !(item == 0 && stalled)) {
             const bool ok = slot >= 0 && slot < p.kv_slots;
             S.valid[st] = ok;
             if (ok) {
@@ -552,9 +553,10 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
         }
       }
     }
-    if (dead)  // let the copies in flight land before the block ends
-      for (int i = max(0, item - C::kStages); i < item; ++i)
-        mbar_wait(&S.full[i % C::kStages], (i / C::kStages) & 1, p.status, p.wait_ns);
+    // No copy is in flight when the block ends, whoever gave up: the latest item of each stage has
+    // landed (those before it had, or its stage would not have been free).
+    for (int i = max(stalled ? 1 : 0, item - C::kStages); i < item; ++i)
+      mbar_wait(&S.full[i % C::kStages], (i / C::kStages) & 1, p.status, p.wait_ns);
     return;
   }
 
@@ -595,7 +597,8 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
         rows.tokens(p, smem_u32(ks), smem_u32(vs), tok0);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.empty[st]);
+      // a stage that was not seen full is not free: the producer then stops too
+      if (lane == 0 && !dead) mbar_arrive(&S.empty[st]);
     }
 
     // ---- join the warps' states, 8 rows at a time by kPer threads each

@@ -80,6 +80,7 @@ struct PagedParams {
   int n_req, n_q, max_pages, H, G, o_f32;
   int run_rows;  // query rows of a run, 8 or 16 (set at launch)
   int whole;     // a block per run (set at launch)
+  int stall_unit;  // test hook: this block's first page, or key tile, is neither copied nor signalled (-1: none)
 };
 
 constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row tiles aims at
