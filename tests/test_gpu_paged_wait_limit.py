@@ -1,5 +1,5 @@
 """Bounded device waits of the paged attention kernels.  With a short limit and one block
-whose first page is neither copied nor signalled, every role of the block gives
+whose first page (or key tile) is neither copied nor signalled, every role of the block gives
 up, what it did copy lands, the call returns and the status word says so; the next call is
 right."""
 import time
@@ -9,6 +9,7 @@ import torch
 
 import tiered_paged_kv_gb300 as tpk
 from paged_util import Pages
+from test_gpu_paged_cross import Cross
 from test_gpu_paged_decode import Decode
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +48,12 @@ def stalled(c, unit=0):
                          ids=lambda x: f"{len(x)}x{max(x)}" if isinstance(x, list) else str(x))
 def test_decode(lens, H, G, pages, unit, D):
     stalled(Decode(Pages(lens, H, D, "bf16", 3, max_pages=pages), G), unit)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq,lens,H,G,mute", [([4, 3], [5000, 64], 1, 2, []), ([200, 150], [1300, 70], 64, 1, []),
+                                              ([300, 20], [2000, 700], 1, 2, [(0, 3)]), ([100], [30], 4, 1, []),
+                                              ([513, 700], [400, 1000], 16, 4, [(1, 0), (1, 15)])],
+                         ids=lambda x: "-".join(map(str, x)) if isinstance(x, list) and x and isinstance(x[0], int) else None)
+def test_cross(nq, lens, H, G, mute, D):
+    stalled(Cross(Pages(lens, H, D, "bf16", 4), nq, G, mute=mute))

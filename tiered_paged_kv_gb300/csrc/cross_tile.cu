@@ -98,6 +98,9 @@ struct TileShared {
   uint64_t item_full[2], item_empty[2];
   Item item[2];
   uint32_t tmem;
+  // what the block must see land before it ends: by slot, the copies that complete its `full`; those
+  // that complete `tail` and `q_full`
+  int laps[8], tails, loads;
   int fine[2][8][2];               // [item parity][pair of warps][half]: waits met so far
   float half[4 * kTileRows];       // what the two threads of a row tell each other
 };
@@ -350,8 +353,10 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
     return;
   }
   if (tid == 0) {
+    S.tails = S.loads = 0;
 #pragma unroll
     for (int i = 0; i < C::kSlots; ++i) {
+      S.laps[i] = 0;
       mbar_init(&S.full[i], 1);
       mbar_init(&S.empty[i], 1);
     }
@@ -428,7 +433,8 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       if (!ok) return;
       uint8_t* dst = slots + st * C::kSlotBytes;
       uint64_t* bar = clear ? &S.tail : &S.full[st];
-      if (elect_one()) {
+      if (elect_one() && !(!values && pos == 0 && (int)blockIdx.x == p.stall_unit)) {
+        if (clear) S.tails = tails + 1; else S.laps[st] = lap + 1;
         if (n > 0) mbar_arrive_expect_tx(bar, n * (C::kSlotBytes / 2));
         else mbar_arrive(bar);
 #pragma unroll
@@ -451,7 +457,10 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
                 make_uint4(0, 0, 0, 0);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.full[st]);
+        if (lane == 0 && ok) {
+          S.laps[st] = lap + 1;
+          mbar_arrive(&S.full[st]);
+        }
       }
     }
   };
@@ -462,12 +471,6 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
   };
   auto v_pos = [&](const Item& it, int base, int j) {
     return base + C::kParts * (C::kTiles == 2 || j + 1 == it.nk ? 2 * j + 1 : 2 * j + 2);
-  };
-  // a loader that gave up lets its latest copies land before the block ends
-  auto land = [&](int pos) {
-    if (pos < 0) return;
-    for (int c = 0; c < C::kParts; ++c)
-      mbar_wait(&S.full[(pos + c) % C::kSlots], (pos + c) / C::kSlots & 1, p.status, p.wait_ns);
   };
 
   if (warp == C::kMma) {
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
     const bool sorted = splits == 1 && p.n_req <= 64;
     Requests requests;
     requests.per_group = C::kTiles * per_tile;
-    int base = 0, pos = -1, tails = 0;  // ring positions before this item; the latest one filled
+    int base = 0, tails = 0;  // ring positions before this item
     bool ok = true;
     auto wait = [&](uint64_t* bar, int parity) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, p.status, p.wait_ns)) != 0;
@@ -668,14 +671,12 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         for (int j = 0; j < it.nk && ok; ++j) {
           if (j + 4 == it.nk) ask();
           if (C::kTwoLoaders) {
-            pos = k_pos(it, base, j);
-            load_tile(Keys{}, it, w, j, pos, tails, ok);
+            load_tile(Keys{}, it, w, j, k_pos(it, base, j), tails, ok);
             continue;
           }
           if (C::kTiles == 2 || j == 0) load_tile(Keys{}, it, w, j, k_pos(it, base, j), tails, ok);
-          if (C::kTiles == 1 && j + 1 < it.nk) load_tile(Keys{}, it, w2, j + 1, k_pos(it, base, j + 1), tails, ok);
-          pos = v_pos(it, base, j);
-          load_tile(Values{}, it, w, j, pos, tails, ok);
+          if (C::kTiles == 1 && j + 1 < it.nk && ok) load_tile(Keys{}, it, w2, j + 1, k_pos(it, base, j + 1), tails, ok);
+          if (ok) load_tile(Values{}, it, w, j, v_pos(it, base, j), tails, ok);
         }
         base += 2 * C::kParts * it.nk;
       }
@@ -694,25 +695,18 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         break;
       }
     }
-    if (!ok) {
-      mbar_wait(&S.taken, asked & 1, p.status, p.wait_ns);
-      land(pos);
-    }
+    if (!ok) mbar_wait(&S.taken, asked & 1, p.status, p.wait_ns);
     __syncwarp();
   } else if (C::kTwoLoaders && warp == C::kValues) {
     // ------------------------------------------------------------------ values
-    int base = 0, pos = -1, tails = 0;
+    int base = 0, tails = 0;
     bool ok = true;
     Item it;
     for (int k = 0; ok && next_item(k, it) && it.id >= 0; ++k) {
       TableWindow w;
-      for (int j = 0; j < it.nk && ok; ++j) {
-        pos = v_pos(it, base, j);
-        load_tile(Values{}, it, w, j, pos, tails, ok);
-      }
+      for (int j = 0; j < it.nk && ok; ++j) load_tile(Values{}, it, w, j, v_pos(it, base, j), tails, ok);
       base += 2 * C::kParts * it.nk;
     }
-    if (!ok) land(pos);
     __syncwarp();
   } else if (warp == C::kQuery) {
     // ----------------------------------------------------------------- queries
@@ -728,6 +722,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       // past the last, zero: no row of theirs is written
       const int tiles = it.tokens > per_tile ? 2 : 1;
       if (elect_one()) {
+        S.loads = items;
         mbar_arrive_expect_tx(&S.q_full, tiles * per_tile * G * D * 2);
         for (int x = 0; x < tiles; ++x)
 #pragma unroll
@@ -737,7 +732,6 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       }
       __syncwarp();
     }
-    if (items > 0) mbar_wait(&S.q_full, (items - 1) & 1, p.status, p.wait_ns);  // none in flight at the end
   } else {
     // ----------------------------------------------------------------- softmax
     // Warp w has rows 32 (w mod 4) .. of tile w / 8 (a warp reaches the TMEM rows of its
@@ -945,6 +939,13 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
   if (warp == C::kMma) {
     tc_fence_after();
     tmem_dealloc(tmem);
+  }
+  // No copy is in flight when the block ends, whichever role gave up.  (A copy into a slot means
+  // that the one before it there has landed.)
+  if (tid < C::kSlots + 2) {
+    uint64_t* const bar = tid < C::kSlots ? &S.full[tid] : tid == C::kSlots ? &S.tail : &S.q_full;
+    const int n = tid < C::kSlots ? S.laps[tid] : tid == C::kSlots ? S.tails : S.loads;
+    if (n > 0) mbar_wait(bar, (n - 1) & 1, p.status, p.wait_ns);
   }
 }
 
