@@ -534,7 +534,7 @@ tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const 
  * range may hold anything, NaN and infinities too.  A page-table entry outside the pool
  * is skipped and sets bit 0 of the device status.
  * ws: dev workspace of tpk_decode_paged_workspace_bytes(shape, n_req) bytes (no
- * initialisation); calls sharing one must not overlap on the GPU.  n_req in [1, 4096].
+ * initialisation; enough for fewer requests too); calls sharing one must not overlap on the GPU.  n_req in [1, 4096].
  * Strides are multiples of 8 elements, at least H*G*D.  Capturable once the device has
  * seen one uncaptured call of the same head_dim and dtype.
  */
@@ -562,7 +562,8 @@ tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const 
  * differences float32 no longer holds, may turn their row's o and lse into NaN; they never leave
  * a row finite and wrong.
  * ws: dev workspace of tpk_cross_paged_workspace_bytes(shape, n_req, n_q) bytes (no
- * initialisation); calls sharing one must not overlap on the GPU.  n_req in [1, 4096];
+ * initialisation), which is enough for every call of the same shape with no more requests
+ * and no more query tokens; calls sharing one must not overlap on the GPU.  n_req in [1, 4096];
  * n_q >= 0 (0 is a no-op).  Strides, errors and capture as for tpk_decode_attn_paged.
  */
 size_t tpk_cross_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_q);

@@ -158,12 +158,25 @@ CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
   return {tiles, groups, std::max<int64_t>(splits, 1)};
 }
 
+// Workspace of split row tiles: each row's maximum and sum, then its output.
+size_t tile_ws_bytes(const tpk_paged_shape* s, size_t rows) { return align256(rows * 8) + rows * s->head_dim * 4; }
+
 size_t cross_ws_bytes(const tpk_paged_shape* s, int n_req, int n_q) {
   const CrossPlan c = cross_plan(s, n_req, n_q);
   if (c.groups == 0) return split_ws_bytes(s);
   if (c.splits == 1) return 256;
-  const size_t rows = (size_t)c.rows(s);
-  return align256(rows * 8) + rows * s->head_dim * 4;
+  return tile_ws_bytes(s, (size_t)c.rows(s));
+}
+
+// An upper bound of that for all calls of the same shape with at most n_req requests and n_q
+// tokens: which kernel takes a call does not go by size alone.  Row tiles are cut to at most
+// kTileBlocks items, and one request with more than eight rows may take them.
+size_t cross_ws_bound(const tpk_paged_shape* s, int n_req, int n_q) {
+  if ((int64_t)n_q * s->group <= 8) return split_ws_bytes(s);
+  const int64_t items = ((int64_t)n_q / (kTileRows / s->group) + n_req) * s->kv_heads;
+  const int64_t splits = s->max_pages > 0 ? (s->max_pages + 3) / 4 : 1;
+  const int64_t most = items < kTileBlocks && splits < kTileBlocks ? std::min<int64_t>(items * splits, kTileBlocks) : kTileBlocks;
+  return std::max(split_ws_bytes(s), tile_ws_bytes(s, most * (s->head_dim == 256 ? 1 : 2) * kTileRows));
 }
 
 bool sized(const tpk_paged_shape* s, int n_req) {
@@ -339,7 +352,7 @@ tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const 
 }
 
 size_t tpk_cross_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_q) {
-  return sized(shape, n_req) && n_q >= 0 && shape->kv_heads > 0 && shape->group > 0 && shape->group <= kMaxGroup ? cross_ws_bytes(shape, n_req, n_q) : 0;
+  return sized(shape, n_req) && n_q >= 0 && shape->kv_heads > 0 && shape->group > 0 && shape->group <= kMaxGroup ? cross_ws_bound(shape, n_req, n_q) : 0;
 }
 
 tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q, const void* q, int64_t q_stride,
@@ -353,7 +366,7 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
   if (!q_off) return fail(TPK_ERR_INVALID, "null pointer argument");
   PagedParams p;
   st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
-                       tpk_cross_paged_workspace_bytes(shape, n_req, n_q));
+                       sized(shape, n_req) ? cross_ws_bytes(shape, n_req, n_q) : 0);
   if (st != TPK_OK) return st;
   if (n_q == 0) return TPK_OK;
   p.q_off = q_off;
