@@ -480,7 +480,8 @@ typedef struct {
  *   positions         dev int32 [max_tokens]: its position (0 past the last)
  *   token_req         dev int32 [max_tokens]: its request (-1 past the last)
  * n_free_out may be n_free_in, len_out may be len_old or len_new: updated in place.
- * Other outputs overlap nothing.  n_req in [1, 4096], n_req * max_pages < 2^31;
+ * Other outputs overlap nothing.  Capturable once the device has seen one uncaptured
+ * call.  n_req in [1, 4096], n_req * max_pages < 2^31;
  * max_tokens >= 0 (its three maps may be null if 0).
  */
 tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old, const int32_t* len_new,
@@ -510,7 +511,8 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
  * q and q_out may both be NULL (store only); k, v and both pools may all be NULL
  * (rotate q only).  rot_dim is a multiple of 16, at most head_dim; 0 stores k as it is
  * (positions and inv_freq are then not read).  Strides are multiples of 8 elements, at
- * least heads * head_dim; shape->max_pages and sm_scale are not used.
+ * least heads * head_dim; shape->max_pages and sm_scale are not used.  Capturable once
+ * the device has seen one uncaptured call.
  */
 tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const void* q, int64_t q_stride,
                               const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -534,9 +536,10 @@ tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const 
  * range may hold anything, NaN and infinities too.  A page-table entry outside the pool
  * is skipped and sets bit 0 of the device status.
  * ws: dev workspace of tpk_decode_paged_workspace_bytes(shape, n_req) bytes (no
- * initialisation; enough for fewer requests too); calls sharing one must not overlap on the GPU.  n_req in [1, 4096].
- * Strides are multiples of 8 elements, at least H*G*D.  Capturable once the device has
- * seen one uncaptured call of the same head_dim and dtype.
+ * initialisation; enough for fewer requests too); calls sharing one must not overlap on
+ * the GPU.  n_req in [1, 4096].  Strides are multiples of 8 elements, at least H*G*D.
+ * Capturable once the device has seen one uncaptured attention call of the same head_dim
+ * and dtype, whatever its other arguments.
  */
 size_t tpk_decode_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req);
 tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const void* q, int64_t q_stride,
