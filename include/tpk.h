@@ -509,7 +509,8 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
  *   inv_freq   dev float32 [rot_dim / 2], finite
  *   slot_map   dev int64 [n_tokens]; NULL only without keys (every row is then live)
  * q and q_out may both be NULL (store only); k, v and both pools may all be NULL
- * (rotate q only).  rot_dim is a multiple of 16, at most head_dim; 0 stores k as it is
+ * (rotate q only).  n_tokens = 0 is a no-op; what has a row per token may then be null.
+ * rot_dim is a multiple of 16, at most head_dim; 0 stores k as it is
  * (positions and inv_freq are then not read).  Strides are multiples of 8 elements, at
  * least heads * head_dim; shape->max_pages and sm_scale are not used.  Capturable once
  * the device has seen one uncaptured call.
@@ -567,7 +568,8 @@ tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const 
  * ws: dev workspace of tpk_cross_paged_workspace_bytes(shape, n_req, n_q) bytes (no
  * initialisation), which is enough for every call of the same shape with no more requests
  * and no more query tokens; calls sharing one must not overlap on the GPU.  n_req in [1, 4096];
- * n_q >= 0 (0 is a no-op).  Strides, errors and capture as for tpk_decode_attn_paged.
+ * n_q >= 0 (0 is a no-op; q, kv_range, o, lse and ws may then be null).  Strides, errors
+ * and capture as for tpk_decode_attn_paged.
  */
 size_t tpk_cross_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_q);
 tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q, const void* q, int64_t q_stride,

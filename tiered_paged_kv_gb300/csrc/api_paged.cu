@@ -183,19 +183,25 @@ bool sized(const tpk_paged_shape* s, int n_req) {
   return s && n_req >= 1 && n_req <= kMaxPagedReq && (s->head_dim == 64 || s->head_dim == 128 || s->head_dim == 256);
 }
 
+tpk_status check_counts(const tpk_paged_shape* s, int n_req) {
+  if (s->max_pages < 1 || s->max_pages > kMaxTableRow)
+    return fail(TPK_ERR_INVALID, "max_pages %d out of [1, %d]", s->max_pages, kMaxTableRow);
+  if (n_req < 1 || n_req > kMaxPagedReq) return fail(TPK_ERR_INVALID, "n_req %d out of [1, %d]", n_req, kMaxPagedReq);
+  return TPK_OK;
+}
+
 // What both attention calls check and fill in.
 tpk_status begin_attention(PagedParams& p, const tpk_paged_shape* s, int n_req, const void* q, int64_t q_stride,
                            const void* k_pool, const void* v_pool, const int32_t* page_table, const int32_t* n_tokens,
                            void* o, int64_t o_stride, float* lse, void* ws, size_t ws_bytes, size_t need) {
-  if (s->max_pages < 1 || s->max_pages > kMaxTableRow)
-    return fail(TPK_ERR_INVALID, "max_pages %d out of [1, %d]", s->max_pages, kMaxTableRow);
-  if (n_req < 1 || n_req > kMaxPagedReq) return fail(TPK_ERR_INVALID, "n_req %d out of [1, %d]", n_req, kMaxPagedReq);
+  tpk_status st = check_counts(s, n_req);
+  if (st != TPK_OK) return st;
   if (!q || !k_pool || !v_pool || !page_table || !n_tokens || !o || !lse || !ws)
     return fail(TPK_ERR_INVALID, "null pointer argument");
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(o) || !aligned16(ws))
     return fail(TPK_ERR_INVALID, "q, pools, o and ws must be 16-byte aligned");
   const int64_t row = (int64_t)s->kv_heads * s->group * s->head_dim;
-  tpk_status st = check_stride("q_stride", q_stride, row);
+  st = check_stride("q_stride", q_stride, row);
   if (st == TPK_OK) st = check_stride("o_stride", o_stride, row);
   if (st != TPK_OK) return st;
   if (ws_bytes < need) return fail(TPK_ERR_NOMEM, "workspace %zu bytes < %zu required", ws_bytes, need);
@@ -273,13 +279,14 @@ tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const 
   if (n_tokens < 0) return fail(TPK_ERR_INVALID, "n_tokens %d < 0", n_tokens);
   if (rot_dim < 0 || rot_dim > D || rot_dim % 16) return fail(TPK_ERR_INVALID, "rot_dim %d (a multiple of 16 up to %d)", rot_dim, D);
   if (interleaved != 0 && interleaved != 1) return fail(TPK_ERR_INVALID, "interleaved %d (0 or 1)", interleaved);
-  const bool queries = q || q_out, keys = k || v || k_pool || v_pool;
+  const bool none = n_tokens == 0;  // empty rows have no address
+  const bool queries = q || q_out, keys = (k || v || k_pool || v_pool) && !(none && !k && !v && k_pool && v_pool);
   if (queries && !(q && q_out)) return fail(TPK_ERR_INVALID, "q and q_out go together");
   if (keys && !(k && v && k_pool && v_pool)) return fail(TPK_ERR_INVALID, "k, v and both pools go together");
-  if (!queries && !keys) return fail(TPK_ERR_INVALID, "nothing to rotate or store");
-  if (keys && !slot_map) return fail(TPK_ERR_INVALID, "null slot_map");
+  if (!queries && !keys && !none) return fail(TPK_ERR_INVALID, "nothing to rotate or store");
+  if (keys && !slot_map && !none) return fail(TPK_ERR_INVALID, "null slot_map");
   if (rot_dim > 0) {
-    if (!positions || !inv_freq) return fail(TPK_ERR_INVALID, "null positions or inv_freq");
+    if ((!positions && !none) || !inv_freq) return fail(TPK_ERR_INVALID, "null positions or inv_freq");
     if (n_axes < 1 || n_axes > 4) return fail(TPK_ERR_INVALID, "n_axes %d out of [1, 4]", n_axes);
   }
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool))
@@ -301,7 +308,7 @@ tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const 
     p.axis_of[j] = axis_of ? axis_of[j] : 0;
     if (p.axis_of[j] >= n_axes) return fail(TPK_ERR_INVALID, "axis_of[%d] = %d of %d axes", j, p.axis_of[j], n_axes);
   }
-  if (n_tokens == 0) return TPK_OK;
+  if (none) return TPK_OK;
   p.q = static_cast<const uint16_t*>(q);
   p.k = static_cast<const uint16_t*>(k);
   p.v = static_cast<const uint16_t*>(v);
@@ -364,11 +371,11 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
   if (n_q < 0 || (int64_t)n_q * shape->kv_heads * shape->group > 0x7fffffffLL)
     return fail(TPK_ERR_INVALID, "n_q %d (at most 2^31 query rows)", n_q);
   if (!q_off) return fail(TPK_ERR_INVALID, "null pointer argument");
+  if (n_q == 0) return check_counts(shape, n_req);  // empty rows have no address
   PagedParams p;
   st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
                        sized(shape, n_req) ? cross_ws_bytes(shape, n_req, n_q) : 0);
   if (st != TPK_OK) return st;
-  if (n_q == 0) return TPK_OK;
   p.q_off = q_off;
   p.range = kv_range;
   p.n_q = n_q;
