@@ -300,6 +300,7 @@ def _calls():
         spec = importlib.util.spec_from_file_location("_tpk_call", path, loader=loader)
         module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
+        module.set_shape_type(PagedShape)
         _call = module
     return _call
 

@@ -3,7 +3,8 @@
  * few microseconds of GPU work, and converting their twenty arguments through ctypes takes
  * as long as the work; here it takes about one microsecond.  A pointer argument is None, an
  * int or an object with data_ptr(); a stream None, an int or an object with cuda_stream; a
- * host array or a shape anything with a buffer.  The functions return the call's status.
+ * host array anything with a buffer; a shape None or a PagedShape, whose type is handed over
+ * by set_shape_type.  The functions return the call's status.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -11,6 +12,7 @@
 #include "tpk.h"
 
 static PyObject *s_data_ptr, *s_cuda_stream;
+static PyTypeObject* shape_type;
 
 /* The argument list of one call, read in order; `bad` once one did not convert. */
 typedef struct {
@@ -96,6 +98,16 @@ static const void* buffer(reader* r, Py_buffer* b, Py_ssize_t bytes) {
   return b->buf;
 }
 
+static const tpk_paged_shape* shape_of(reader* r, Py_buffer* b) {
+  PyObject* o = r->at < r->n ? r->args[r->at] : NULL;
+  const tpk_paged_shape* s = buffer(r, b, sizeof(tpk_paged_shape));
+  if (s && !r->bad && !(shape_type && PyObject_TypeCheck(o, shape_type))) {
+    PyErr_Format(PyExc_TypeError, "a PagedShape, not %R", (PyObject*)Py_TYPE(o));
+    r->bad = 1;
+  }
+  return s;
+}
+
 static PyObject* done(reader* r, tpk_status st) {
   if (r->bad || r->at != r->n) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
@@ -134,7 +146,7 @@ static PyObject* kv_rope_append(PyObject* self, PyObject* const* args, Py_ssize_
   (void)self;
   reader r = {args, n, 0, 0};
   Py_buffer sb, ab;
-  const tpk_paged_shape* shape = buffer(&r, &sb, sizeof(tpk_paged_shape));
+  const tpk_paged_shape* shape = shape_of(&r, &sb);
   const int n_tokens = narrow(&r);
   const void* q = pointer(&r);
   const int64_t q_stride = wide(&r);
@@ -167,7 +179,7 @@ static PyObject* decode_attn_paged(PyObject* self, PyObject* const* args, Py_ssi
   (void)self;
   reader r = {args, n, 0, 0};
   Py_buffer sb;
-  const tpk_paged_shape* shape = buffer(&r, &sb, sizeof(tpk_paged_shape));
+  const tpk_paged_shape* shape = shape_of(&r, &sb);
   const int n_req = narrow(&r);
   const void* q = pointer(&r);
   const int64_t q_stride = wide(&r);
@@ -190,7 +202,7 @@ static PyObject* cross_attn_paged(PyObject* self, PyObject* const* args, Py_ssiz
   (void)self;
   reader r = {args, n, 0, 0};
   Py_buffer sb;
-  const tpk_paged_shape* shape = buffer(&r, &sb, sizeof(tpk_paged_shape));
+  const tpk_paged_shape* shape = shape_of(&r, &sb);
   const int n_req = narrow(&r), n_q = narrow(&r);
   const void* q = pointer(&r);
   const int64_t q_stride = wide(&r);
@@ -209,9 +221,18 @@ static PyObject* cross_attn_paged(PyObject* self, PyObject* const* args, Py_ssiz
   return done(&r, st);
 }
 
+static PyObject* set_shape_type(PyObject* self, PyObject* type) {
+  (void)self;
+  if (!PyType_Check(type)) return PyErr_Format(PyExc_TypeError, "a type, not %R", type);
+  Py_INCREF(type);
+  Py_XSETREF(shape_type, (PyTypeObject*)type);
+  Py_RETURN_NONE;
+}
+
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(kv_tables_update), METHOD(kv_rope_append), METHOD(decode_attn_paged),
-                                METHOD(cross_attn_paged), {NULL, NULL, 0, NULL}};
+                                METHOD(cross_attn_paged), {"set_shape_type", set_shape_type, METH_O, NULL},
+                                {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tpk_call", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__tpk_call(void) {
