@@ -44,3 +44,21 @@ def test_anything_else_is_refused(other):
     for f in refused(other):
         with pytest.raises((TypeError, ValueError)):
             f()
+
+
+def test_a_module_per_python_version():
+    import importlib.machinery
+    assert build.CALL.endswith(importlib.machinery.EXTENSION_SUFFIXES[0]) and "cpython-3" in build.CALL
+
+
+def test_without_the_headers_the_other_calls_are_built(tmp_path, monkeypatch):
+    """No Python.h: the library is built all the same, and the calls that need the module say so."""
+    monkeypatch.setattr(build.sysconfig, "get_path", lambda *a, **k: str(tmp_path))
+    monkeypatch.setattr(build, "CALL", str(tmp_path / "_tpk_call.so"))
+    monkeypatch.setattr(tpk, "_call", None)
+    with pytest.warns(UserWarning, match="Python.h"):
+        assert build.build() == build.LIB
+    assert tpk.lib().tpk_version()
+    assert tpk.decode_paged_workspace_bytes(tpk.PagedShape(**GOOD), 1) > 0
+    with pytest.raises(RuntimeError, match="Python.h"):
+        tpk.decode_attn_paged(tpk.PagedShape(**GOOD), 0, 16, 64, 16, 16, 16, 16, None, 16, 64, False, 16, 16, 0)

@@ -295,7 +295,8 @@ def _calls():
         lib()
         path = _build_mod.CALL
         if not os.path.exists(path):
-            raise RuntimeError(f"_tpk_call.so not built ({path}); run tiered_paged_kv_gb300.build.build()")
+            raise RuntimeError(f"the module of the serving step's calls is not built ({path}): run "
+                               "tiered_paged_kv_gb300.build.build(), which needs Python.h")
         loader = importlib.machinery.ExtensionFileLoader("_tpk_call", path)
         spec = importlib.util.spec_from_file_location("_tpk_call", path, loader=loader)
         module = importlib.util.module_from_spec(spec)

@@ -11,6 +11,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libtpk.so")
-CALL = os.path.join(OUT_DIR, "_tpk_call.so")
+CALL = os.path.join(OUT_DIR, "_tpk_call" + sysconfig.get_config_var("EXT_SUFFIX"))  # one per Python version
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -85,11 +86,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
 
 def _build_call(force: bool) -> None:
+    include = sysconfig.get_path("include")
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        warnings.warn(f"no Python.h in {include}: the serving step's calls are not built, the others are")
+        return
     src = os.path.join(CSRC, "binding.c")
     if not force and not _stale(CALL, [src, LIB] + headers()):
         return
     tmp = CALL + f".tmp{os.getpid()}"
-    cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_path("include"), "-I", INCLUDE,
+    cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", include, "-I", INCLUDE,
            src, "-o", tmp, "-L", OUT_DIR, "-ltpk", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
