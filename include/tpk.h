@@ -497,8 +497,9 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
  * angle positions[axis_of[j]][t] * inv_freq[j]:
  *   (a, b) -> (a cos - b sin, b cos + a sin),
  * where pair j is channels (j, j + rot_dim / 2), or (2 j, 2 j + 1) if interleaved; the
- * other channels are copied.  The angle is reduced in fixed point, exact to 2^-32
- * turns at any 32-bit position; the products run in float32 and are rounded once.
+ * other channels are copied.  The angle is reduced in fixed point and rounded to float32
+ * then, off by at most 2^-26 + 2^-31 turns at any 32-bit position; the products run in
+ * float32 and are rounded once.
  * Rotated queries go to q_out (rows of q_out_stride elements; may be q itself with the
  * same stride), rotated keys and the values to row slot_map[t] of the pools.
  * A token with a negative slot is padding: its rows of q_out and of the pools are left
@@ -506,7 +507,8 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
  * the device status.  Tokens of one call must have distinct slots.
  *   positions  dev int32 [n_axes][n_tokens]
  *   axis_of    host uint8 [rot_dim / 2], each < n_axes; NULL: axis 0 everywhere
- *   inv_freq   dev float32 [rot_dim / 2], finite
+ *   inv_freq   dev float32 [rot_dim / 2], below 2^32 in size (others, infinities and NaN
+ *              turn their pairs into NaN)
  *   slot_map   dev int64 [n_tokens]; NULL only without keys (every row is then live)
  * q and q_out may both be NULL (store only); k, v and both pools may all be NULL
  * (rotate q only).  n_tokens = 0 is a no-op; what has a row per token may then be null.

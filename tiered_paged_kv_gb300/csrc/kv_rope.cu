@@ -3,10 +3,12 @@
 //
 // The angle of pair j at position x is x * inv_freq[j].  Only its fraction of a turn
 // matters, so the frequency is held as F = frac(inv_freq / 2 pi) * 2^64, formed from
-// the float's 24-bit significand and 96 bits of 1 / (2 pi) in integers (within one
-// unit), and x * F mod 2^64 is the angle in units of 2^-64 turns whatever x: at a
-// 32-bit position it is off by at most 2^-33 turns, where a float32 product is off by
-// 10^-2 radians at 128K.  Its upper 32 bits, signed, go through sincospif.
+// the float's 24-bit significand and 96 bits of 1 / (2 pi) in integers (within two units
+// below 2^32: one for the digits left out, one for the bits shifted out), and x * F mod
+// 2^64 is the angle in units of 2^-64 turns whatever x: at a 32-bit position it is off by
+// at most 2^-32 turns, where a float32 product is off by 10^-2 radians at 128K.  Its upper
+// 32 bits, rounded (2^-33) and signed, go through sincospif as a float32 (up to 2^-26 turns
+// next to a half): 2^-26 + 2^-31 turns in all.
 //
 // A thread keeps one piece of every token's row -- 16 channels of one head: 8 pairs, or
 // 16 channels copied; two 16-byte loads and stores -- so all index arithmetic is done
@@ -23,7 +25,7 @@ constexpr int kRopePairs = 1024;   // angles a block holds: tokens * rot / 2
 constexpr int kRopeTokens = 8;     // tokens of a block, at most (4: 39.1 us, 8: 36.5, 16: 40.9 at 8200 tokens)
 constexpr int kRopeUnroll = 4;
 
-// frac(f / (2 pi)) in units of 2^-64 turns.
+// frac(f / (2 pi)) in units of 2^-64 turns, |f| < 2^32.
 __device__ __forceinline__ uint64_t turns64(float f) {
   const uint32_t w = __float_as_uint(f);
   const int e = (w >> 23) & 0xff;
@@ -32,10 +34,7 @@ __device__ __forceinline__ uint64_t turns64(float f) {
   const unsigned __int128 c = ((unsigned __int128)0x28be60dbu << 64) | 0x9391054a7f09d5f4ull;
   const int shift = 182 - (e ? e : 1);  // f = m 2^(e - 150), so F = m c 2^(e - 150) 2^(64 - 96)
   const unsigned __int128 x = m * c;
-  uint64_t t;
-  if (shift >= 128) t = 0;
-  else if (shift >= 0) t = (uint64_t)(x >> shift);
-  else t = shift > -64 ? (uint64_t)(x << -shift) : 0;
+  const uint64_t t = shift < 128 ? (uint64_t)(x >> shift) : 0;  // at least 24
   return (w >> 31) ? 0 - t : t;
 }
 
@@ -78,9 +77,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   for (int i = tid; i < nt * half; i += blockDim.x) {
     const int t = i / half, x = i - t * half;
     const int64_t pos = p.positions[(int64_t)p.axis_of[x] * p.n_tokens + t0 + t];
-    const uint64_t angle = turns64(p.inv_freq[x]) * (uint64_t)pos;
+    const float f = p.inv_freq[x];
+    const uint64_t angle = turns64(f) * (uint64_t)pos;
     float s, c;
     sincospif((float)(int32_t)((angle + 0x80000000u) >> 32) * 0x1p-31f, &s, &c);  // of pi * (2 * turns)
+    if (!(fabsf(f) < 0x1p32f)) s = c = __int_as_float(0x7fffffff);
     reinterpret_cast<float2*>(turn + t * (half >> 1) + (x >> 1 & 3) * (half >> 3) + (x >> 3))[x & 1] = make_float2(c, s);
   }
   if (tid < nt) {
