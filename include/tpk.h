@@ -535,8 +535,10 @@ tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const 
  *   o          dev [n_req] rows of o_stride elements, [H*G][D]: of shape->dtype, or
  *              float32 if o_f32 (what tpk_merge_lse folds with other tiers' partials)
  *   lse        dev float32 [n_req][H*G]
- * A request that sees nothing gets o = 0, lse = -inf.  Pool rows outside the attended
- * range may hold anything, NaN and infinities too.  A page-table entry outside the pool
+ * A request that sees nothing gets o = 0, lse = -inf; a query row with a NaN gets NaN in
+ * both.  Keys and values that are attended must be finite (an infinite value makes its
+ * channel infinite or NaN).  Pool rows outside the attended range may hold anything, NaN
+ * and infinities too.  A page-table entry outside the pool
  * is skipped and sets bit 0 of the device status.
  * ws: dev workspace of tpk_decode_paged_workspace_bytes(shape, n_req) bytes (no
  * initialisation; enough for fewer requests too); calls sharing one must not overlap on

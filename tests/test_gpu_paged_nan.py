@@ -67,3 +67,20 @@ def test_cross_ranges_with_split_keys():
     c = Cross(Pages([2000], 1, 128, "bf16", 5), [300], 2, ranges=r)
     poison(c, range(0, 300, 4), [1], 300)
     assert (c.lse[1::4] == float("-inf")).all() and (c.o[1::4] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [200, 5000])
+def test_an_infinite_value_stays_in_its_channel(n, D):
+    pg = Pages([n], 1, D, "bf16", 6)
+    d = Decode(pg, 4)
+    d.call()
+    d.check()
+    o, lse = d.o.clone(), d.lse.clone()
+    d.v[pg.table[0, 1].item(), 0, 5, 7] = float("inf")
+    d.call()
+    torch.cuda.synchronize()
+    got = d.o.view(4, D)
+    assert not torch.isfinite(got[:, 7]).any() and torch.equal(d.lse, lse)
+    keep = torch.arange(D) != 7
+    assert torch.equal(got[:, keep], o.view(4, D)[:, keep])
