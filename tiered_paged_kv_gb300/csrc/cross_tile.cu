@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
     if (bad && lane == 0) atomicOr(p.status, kStatusBadSlot);
     // values whose weight is 0 must not be NaN: rows past the last token in its 16-token
     // group (later groups are not multiplied), and pages not there
-    const bool clear = values && (bad || (tok0 + kKeys > it.len && (it.len & 15)));
+    const bool clear = values && (bad || (it.len - tok0 < kKeys && (it.len & 15)));
     const int y0 = (slot0 * p.H + it.h) * kPageTokens, y1 = (slot1 * p.H + it.h) * kPageTokens;
     const CUtensorMap* map = values ? &p.vmap : &p.kmap;
 #pragma unroll
