@@ -158,9 +158,11 @@ tpk_status make_pool_maps(DecodeParams& p, const tpk_shape* s, const void* k_poo
   const void* pools[2] = {k_pool, v_pool};
   CUtensorMap* maps[2] = {&p.kmap, &p.vmap};
   for (int i = 0; i < 2; ++i) {
-    CUresult r = fn(maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pools[i]), dims, strides, box,
-                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = with_context([&] {
+      return fn(maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pools[i]), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
     if (r != CUDA_SUCCESS) return fail(TPK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   }
   return TPK_OK;

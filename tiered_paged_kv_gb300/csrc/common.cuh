@@ -233,6 +233,16 @@ int per_device_int(std::atomic<int> (&cache)[kMaxDevices], F&& compute) {
   return v;
 }
 
+// A driver call of the encoder's kind wants a current context, which a host thread that has made no
+// runtime call yet does not have: the device's own is made current then, and the call repeated.
+template <class F>
+CUresult with_context(F&& call) {
+  const CUresult r = call();
+  int dev = 0;
+  if (r != CUDA_ERROR_INVALID_CONTEXT || cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return r;
+  return call();
+}
+
 // ------------------------------------------------------------- PTX wrappers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
