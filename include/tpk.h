@@ -437,8 +437,11 @@ tpk_status tpk_tiers_destroy(tpk_tiers* tiers);
  * to paged states of another length (an encoder's, or a prompt's own).  They follow
  * the conventions above (ownership, pointers, streams, errors); their pools are
  * [slot][kv_heads][64][head_dim] of bfloat16 or float16, their page table is int32
- * [n_req][max_pages] (row b: the slots of request b's pages in order).  There is no
- * counterpart in the pages this library follows.
+ * [n_req][max_pages] (row b: the slots of request b's pages in order).  Queries, keys,
+ * values, outputs, pools and workspaces are 16-byte aligned; lengths, tables, maps,
+ * ranges, frequencies and lse need only be aligned to their elements, so a part of one
+ * may be passed.  Others are refused.  There is no counterpart in the pages this library
+ * follows.
  */
 enum { TPK_BF16 = 0, TPK_F16 = 1 };
 typedef struct {

@@ -39,6 +39,12 @@ tpk_status cuda_fail(cudaError_t e, const char* what) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Arrays of 4-byte (and one of 8-byte) elements, read as such; null passes.
+template <typename... P>
+bool aligned_to(size_t bytes, P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & (bytes - 1)) == 0;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int kMaxHeads = 1024, kMaxGroup = 128, kMaxTableRow = (1 << 25) - 1;
@@ -201,6 +207,7 @@ tpk_status begin_attention(PagedParams& p, const tpk_paged_shape* s, int n_req, 
     return fail(TPK_ERR_INVALID, "null pointer argument");
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(o) || !aligned16(ws))
     return fail(TPK_ERR_INVALID, "q, pools, o and ws must be 16-byte aligned");
+  if (!aligned_to(4, page_table, n_tokens, lse)) return fail(TPK_ERR_INVALID, "page_table, n_tokens and lse must be 4-byte aligned");
   const int64_t row = (int64_t)s->kv_heads * s->group * s->head_dim;
   st = check_stride("q_stride", q_stride, row);
   if (st == TPK_OK) st = check_stride("o_stride", o_stride, row);
@@ -246,6 +253,9 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
   if (!len_old || !len_new || !page_table || !n_free_in || !n_free_out || !len_out || !granted || !tok_off ||
       (free_cap > 0 && !free_slots) || (max_tokens > 0 && (!slot_map || !positions || !token_req)))
     return fail(TPK_ERR_INVALID, "null pointer argument");
+  if (!aligned_to(4, len_old, len_new, page_table, free_slots, n_free_in, n_free_out, len_out, granted, tok_off, positions, token_req) ||
+      !aligned_to(8, slot_map))
+    return fail(TPK_ERR_INVALID, "an array is not aligned to its elements");
   TablesParams p;
   p.len_old = len_old;
   p.len_new = len_new;
@@ -292,6 +302,8 @@ tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const 
   }
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool))
     return fail(TPK_ERR_INVALID, "q, k, v, q_out and pools must be 16-byte aligned");
+  if (!aligned_to(4, positions, inv_freq) || !aligned_to(8, slot_map))
+    return fail(TPK_ERR_INVALID, "positions, inv_freq or slot_map is not aligned to its elements");
   if (queries) {
     st = check_stride("q_stride", q_stride, (int64_t)HQ * D);
     if (st == TPK_OK) st = check_stride("q_out_stride", q_out_stride, (int64_t)HQ * D);
@@ -346,6 +358,7 @@ tpk_status tpk_decode_attn_paged(const tpk_paged_shape* shape, int n_req, const 
   tpk_status st = check_paged(shape);
   if (st != TPK_OK) return st;
   if (o_f32 != 0 && o_f32 != 1) return fail(TPK_ERR_INVALID, "o_f32 %d (0 or 1)", o_f32);
+  if (!aligned_to(4, tok_begin)) return fail(TPK_ERR_INVALID, "tok_begin must be 4-byte aligned");
   PagedParams p;
   st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
                        tpk_decode_paged_workspace_bytes(shape, n_req));
@@ -372,6 +385,7 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
   if (n_q < 0 || (int64_t)n_q * shape->kv_heads * shape->group > 0x7fffffffLL)
     return fail(TPK_ERR_INVALID, "n_q %d (at most 2^31 query rows)", n_q);
   if (!q_off) return fail(TPK_ERR_INVALID, "null pointer argument");
+  if (!aligned_to(4, q_off, kv_range)) return fail(TPK_ERR_INVALID, "q_off and kv_range must be 4-byte aligned");
   if (n_q == 0) return check_counts(shape, n_req);  // empty rows have no address
   PagedParams p;
   st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
