@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
 // its wait: only there are the writes of the launches before it sure to be seen.  The
 // partials' maxima are read at once, one a thread; then every thread sums its four
 // channels over the partials in block order, eight loads in flight.
-constexpr int kFoldParts = 64;  // weights held at a time, one a thread
+constexpr int kFoldParts = 64;  // weights held at a time
 template <typename T, int D>
 __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ PagedParams p, int blocks, int rows) {
   __shared__ float weight[kFoldParts];
@@ -692,15 +692,12 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
   auto slot = [&](int k) { return (2 * (int64_t)(i + k) + (k == 0 ? 1 : 0)) * kRowTile + r; };
   const float* part_l = p.part_ml + 2 * (int64_t)blocks * kRowTile;
   wait_before();
-  // the first partials' statistics, on their way together with the record
-  const bool may = i + tid < blocks;
-  const float m0 = may ? p.part_ml[slot(tid)] : kEmpty, l0 = may ? part_l[slot(tid)] : 0.f;
   const RunCut cut = p.cuts[i];
   const int n = cut.parts;  // blocks i .. i + n - 1 hold a piece
   int token, head;
   if (n == 0 || !run_row(p, cut.first, cut.count, cut.h, cut.tile, r, token, head)) return;
-  float M = tid < n ? m0 : kEmpty;
-  for (int k = tid + 64; k < n; k += 64) M = fmaxf(M, p.part_ml[slot(k)]);
+  float M = kEmpty;
+  for (int k = tid; k < n; k += 64) M = fmaxf(M, p.part_ml[slot(k)]);
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   if ((tid & 31) == 0) red[tid >> 5] = M;
@@ -716,8 +713,8 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
   for (int k0 = 0; k0 < n; k0 += kFoldParts) {
     const int cnt = min(kFoldParts, n - k0);
     __syncthreads();
-    if (tid < cnt) weight[tid] = exp2f((k0 == 0 ? m0 : p.part_ml[slot(k0 + tid)]) - ref);
-    float mine = tid < cnt ? weight[tid] * (k0 == 0 ? l0 : part_l[slot(k0 + tid)]) : 0.f;
+    if (tid < cnt) weight[tid] = exp2f(p.part_ml[slot(k0 + tid)] - ref);
+    float mine = tid < cnt ? weight[tid] * part_l[slot(k0 + tid)] : 0.f;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
     __syncthreads();
