@@ -165,8 +165,12 @@ CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
   return {tiles, groups, std::max<int64_t>(splits, 1)};
 }
 
-// Workspace of split row tiles: each row's maximum and sum, then its output.
-size_t tile_ws_bytes(const tpk_paged_shape* s, size_t rows) { return align256(rows * 8) + rows * s->head_dim * 4; }
+// Workspace of split row tiles: the groups' records (at most kTileBlocks), each row's maximum and
+// sum, then its output.
+constexpr size_t kGroupBytes = (kTileBlocks * sizeof(RunCut) + 255) / 256 * 256;
+size_t tile_ws_bytes(const tpk_paged_shape* s, size_t rows) {
+  return kGroupBytes + align256(rows * 8) + rows * s->head_dim * 4;
+}
 
 size_t cross_ws_bytes(const tpk_paged_shape* s, int n_req, int n_q) {
   const CrossPlan c = cross_plan(s, n_req, n_q);
@@ -409,8 +413,9 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
     const cuuint32_t box[3] = {64, (cuuint32_t)shape->group, (cuuint32_t)(kTileRows / shape->group)};
     st = make_map(&p.qmap, shape->dtype, 3, q, dims, strides, box);
     if (st != TPK_OK) return st;
-    p.part_ml = static_cast<float*>(ws);
-    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256((size_t)rows * 8));
+    p.cuts = static_cast<RunCut*>(ws);
+    p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kGroupBytes);
+    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kGroupBytes + align256((size_t)rows * 8));
     e = launch_cross_tiles(p, shape->head_dim, shape->dtype, plan.tiles, (int)plan.groups, (int)plan.splits,
                            reinterpret_cast<cudaStream_t>(stream));
   }

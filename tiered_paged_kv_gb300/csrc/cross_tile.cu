@@ -632,8 +632,12 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       Item it;
       const int part = id % splits;
       it.id = id;
+      it.first = 0;
       it.h = id / splits % p.H;
-      if (requests.find(p, lane, sorted, id / splits / p.H, it)) {
+      const bool found = requests.find(p, lane, sorted, id / splits / p.H, it);
+      // the join's record, by the block of the group's first part
+      if (splits > 1 && part == 0 && lane == 0) p.cuts[id / splits] = {it.first, found ? it.tokens : 0, it.h, 0, splits};
+      if (found) {
         int clo = 0, chi = it.len;
         if (p.range) {  // what any of its rows sees
           clo = 0x7fffffff;
@@ -945,22 +949,21 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
   }
 }
 
-// Joins the parts of a split launch, one warp per row of a tile group, kJoined parts' values in
-// flight.
+// Joins the parts of a split launch, one warp per row of a tile group, which the group's record
+// gives its query token; kJoined parts' values in flight.
 constexpr int kJoined = 4;
 template <typename T, int D, int kT>
 __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ PagedParams p, int splits) {
   using C = TileCfg<D, kT>;
   const int lane = threadIdx.x & 31, per_tile = kTileRows / p.G;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int r = (int)(w % C::kRows);
-  const int h = (int)(w / C::kRows % p.H);
-  int want = (int)(w / C::kRows / p.H), first = 0, count = 0;
-  const int64_t group = w / C::kRows;  // (tile group, head)
+  // 32 bits do: keys are split only where all items together are at most kTileBlocks
+  const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int r = w % C::kRows, group = w / C::kRows, h = group % p.H;  // group: of tiles, and a head
+  const int x = r % kTileRows / p.G, t = r / kTileRows * per_tile + x;
   auto at = [&](int k) { return (group * splits + k) * C::kRows + r; };
   wait_before();  // nothing is read before it
-  // a part's (maximum, sum) a lane, and the first parts' values, on their way while the row's
-  // request is looked up
+  // the group's query tokens; a part's (maximum, sum) a lane; the first parts' values
+  const RunCut cut = p.cuts[group];
   float2 ml = make_float2(kNone, 0.f), v[kJoined][D / 64];
   if (lane < splits) ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at(lane));
   auto load = [&](int k0) {
@@ -969,32 +972,12 @@ __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ 
       if (k0 + j < splits)
 #pragma unroll
         for (int e = 0; e < D / 64; ++e)
-          v[j][e] = *reinterpret_cast<const float2*>(p.part_o + at(k0 + j) * D + e * 64 + 2 * lane);
+          v[j][e] = *reinterpret_cast<const float2*>(p.part_o + (int64_t)at(k0 + j) * D + e * 64 + 2 * lane);
   };
+  // (a record that a block which gave up did not write may hold anything)
+  const int token = cut.first + t, head = h * p.G + r % kTileRows - x * p.G;
+  if (x >= per_tile || t >= cut.count || (unsigned)cut.first >= (unsigned)p.n_q || token >= p.n_q) return;
   load(0);
-  // ---- the row's request: 32 at a time, their tile groups added up
-  bool found = false;
-  for (int b0 = 0; b0 < p.n_req && !found; b0 += 32) {
-    int a = 0, c = 0;
-    if (b0 + lane < p.n_req) request_rows(p, b0 + lane, a, c);
-    const int groups = (c + C::kTiles * per_tile - 1) / (C::kTiles * per_tile);
-    int inc = groups;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += up;
-    }
-    const uint32_t here = __ballot_sync(0xffffffffu, want < inc);
-    found = here != 0;
-    const int src = found ? __ffs(here) - 1 : 31;
-    first = __shfl_sync(0xffffffffu, a, src);
-    count = __shfl_sync(0xffffffffu, c, src);
-    want -= __shfl_sync(0xffffffffu, found ? inc - groups : inc, src);
-  }
-  const int x = r % kTileRows / p.G;
-  const int t = (want * C::kTiles + r / kTileRows) * per_tile + x;
-  if (!found || x >= per_tile || t >= count) return;
-  const int token = first + t, head = h * p.G + r % kTileRows - x * p.G;
   float M = ml.x;
   for (int k = lane + 32; k < splits; k += 32) M = fmaxf(M, p.part_ml[2 * at(k)]);
 #pragma unroll

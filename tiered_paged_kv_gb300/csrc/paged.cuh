@@ -50,9 +50,10 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, int interleaved, cudaStr
 
 // --------------------------------------------------------------- attention
 constexpr int kBoxRows = 16;  // rows of a page in one copy of the split kernel: one warp's
-// A run that crosses ranges of a split launch, as its first block records it for the join.
+// What a block records for the join of a run that crosses its range, or of a group of row tiles
+// whose keys are split.
 struct __align__(16) RunCut {
-  int first, count;  // the request's query rows
+  int first, count;  // the request's query rows; the group's
   int h, tile;       // the run's KV head, and its number within the request's rows
   int parts;         // blocks that hold a piece of it; 0: no such run
 };
@@ -70,7 +71,7 @@ struct PagedParams {
   const int32_t* begin;  // decode: first token attended, or null
   const int32_t* q_off;  // cross: where each request's query rows begin; null: decode
   const int32_t* range;  // cross: [n_q][2] or null
-  RunCut* cuts;          // workspace: of each block
+  RunCut* cuts;          // workspace: of each block, or group of row tiles
   float* part_ml;        // workspace: [slot][16] running maximum, then [slot][16] sum
   float* part_o;         // workspace: [slot][16][D], not normalised
   int* status;
