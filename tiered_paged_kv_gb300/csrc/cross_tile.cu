@@ -33,9 +33,9 @@
 // order.  Bound: the tensor cores (4 D operations per score); for D = 64 the exponentials, for
 // D = 256 the arrival of keys and values (128 rows use 128 KB in 2,048 matrix cycles).
 //
-// Measured: two requests of 4,096 tokens, 8,192 states, 4 heads per KV head: 915, 1,576 and
-// 1,175 TFLOP/s at D = 64, 128, 256; eight requests of 300 to 1,500 tokens, 1,601 to 6,404
-// states at D = 128 305 us, 1,370 TFLOP/s.
+// Measured: two requests of 4,096 tokens, 8,192 states, 8 x 4 heads: 922, 1,546 and 1,332
+// TFLOP/s at D = 64, 128, 256; eight requests of 300 to 1,500 tokens, 1,601 to 6,404
+// states at D = 128 311 us, 1,340 TFLOP/s.
 #include "paged.cuh"
 
 namespace tpk {
