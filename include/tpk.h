@@ -527,6 +527,25 @@ tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const 
                               int64_t q_out_stride, void* k_pool, void* v_pool, tpk_stream_t stream);
 
 /*
+ * The same with a norm of each head first: query and key heads x become
+ *   y_c = x_c * w_c / sqrt(sum_c x_c^2 / D + eps),  c over the head's D channels,
+ * w being q_weight or k_weight, and are then rotated (or, with rot_dim 0, only stored).
+ * Values are stored as they are.  Sums and products run in float32 and are rounded once;
+ * values of any size are taken (the squares are scaled where float32 would not hold
+ * them).  A head of zeros stays zero if eps > 0; a head with an infinity or a NaN
+ * becomes what the formula gives (NaN where it is infinite over infinite).
+ *   q_weight, k_weight  dev [D] of shape->dtype, 16-byte aligned; NULL: ones
+ *   eps                 finite, not negative
+ * The other arguments, and what is refused, as for tpk_kv_rope_append.
+ */
+tpk_status tpk_kv_norm_rope_append(const tpk_paged_shape* shape, int n_tokens, const void* q, int64_t q_stride,
+                                   const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                   const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+                                   int n_axes, const uint8_t* axis_of, const float* inv_freq, int rot_dim,
+                                   int interleaved, const int64_t* slot_map, void* q_out, int64_t q_out_stride,
+                                   void* k_pool, void* v_pool, tpk_stream_t stream);
+
+/*
  * Attention of one new token per request over its pages.  Request b's query heads
  * attend tokens [tok_begin[b], n_tokens[b]) (tok_begin NULL: from 0; a sliding window
  * otherwise); token t lives in row t % 64 of slot page_table[b][t / 64].  The work is

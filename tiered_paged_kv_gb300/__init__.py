@@ -28,7 +28,7 @@ __all__ = [
     "get_device_status",
     "static_scratch_bytes", "decode_hybrid_batched_static", "Stager", "Tiers", "TiersPlan",
     "PACK13_RECORD_BYTES", "PACK13_PLANE_ENC", "PACK13_PLANE_RAW", "kv_pack13_pages", "kv_unpack13_pages",
-    "PagedShape", "BF16", "F16", "kv_tables_update", "kv_rope_append", "decode_paged_workspace_bytes",
+    "PagedShape", "BF16", "F16", "kv_tables_update", "kv_rope_append", "kv_norm_rope_append", "decode_paged_workspace_bytes",
     "decode_attn_paged", "cross_paged_workspace_bytes", "cross_attn_paged",
 ]
 
@@ -141,13 +141,16 @@ def lib():
         L.tpk_kv_tables_update.argtypes = [i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp]
         L.tpk_kv_rope_append.argtypes = [gp, i32, vp, i64, vp, i64, vp, i64, vp, i32, vp, vp, i32, i32, vp, vp, i64,
                                          vp, vp, vp]
+        L.tpk_kv_norm_rope_append.argtypes = [gp, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, vp, i32, vp, vp,
+                                              i32, i32, vp, vp, i64, vp, vp, vp]
         L.tpk_decode_paged_workspace_bytes.argtypes = [gp, i32]
         L.tpk_decode_paged_workspace_bytes.restype = sz
         L.tpk_decode_attn_paged.argtypes = [gp, i32, vp, i64, vp, vp, vp, vp, vp, vp, i64, i32, vp, vp, sz, vp]
         L.tpk_cross_paged_workspace_bytes.argtypes = [gp, i32, i32]
         L.tpk_cross_paged_workspace_bytes.restype = sz
         L.tpk_cross_attn_paged.argtypes = [gp, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, sz, vp]
-        for name in ("tpk_kv_tables_update", "tpk_kv_rope_append", "tpk_decode_attn_paged", "tpk_cross_attn_paged"):
+        for name in ("tpk_kv_tables_update", "tpk_kv_rope_append", "tpk_kv_norm_rope_append", "tpk_decode_attn_paged",
+                     "tpk_cross_attn_paged"):
             getattr(L, name).restype = i32
         for name in ("tpk_kv_quantize_pages", "tpk_kv_quantize_pages_given_scales", "tpk_kv_pack13_pages",
                      "tpk_kv_unpack13_pages", "tpk_decode_attn_exact",
@@ -326,6 +329,19 @@ def kv_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, posit
     st = (_call or _calls()).kv_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, positions, n_axes,
                                             axis_of, inv_freq, rot_dim, interleaved, slot_map, q_out, q_out_stride,
                                             k_pool, v_pool, stream)
+    if st:
+        _check(st)
+
+
+def kv_norm_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, positions, n_axes,
+                        axis_of, inv_freq, rot_dim, interleaved, slot_map, q_out, q_out_stride, k_pool, v_pool,
+                        stream=None):
+    """As kv_rope_append, each query and key head first divided by its root mean square
+    and multiplied by its channels' factors (see tpk_kv_norm_rope_append); a weight may
+    be None."""
+    st = (_call or _calls()).kv_norm_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight,
+                                                 eps, positions, n_axes, axis_of, inv_freq, rot_dim, interleaved,
+                                                 slot_map, q_out, q_out_stride, k_pool, v_pool, stream)
     if st:
         _check(st)
 

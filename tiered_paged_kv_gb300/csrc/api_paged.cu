@@ -239,6 +239,91 @@ tpk_status begin_attention(PagedParams& p, const tpk_paged_shape* s, int n_req, 
   return TPK_OK;
 }
 
+// The norms of a rotary store: each head's root mean square, then a factor for each channel.
+struct Norms {
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+};
+
+tpk_status rope_append(const tpk_paged_shape* shape, int n_tokens, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, const Norms* norms, const int32_t* positions,
+                       int n_axes, const uint8_t* axis_of, const float* inv_freq, int rot_dim, int interleaved,
+                       const int64_t* slot_map, void* q_out, int64_t q_out_stride, void* k_pool, void* v_pool,
+                       tpk_stream_t stream) {
+  tpk_status st = check_paged(shape);
+  if (st != TPK_OK) return st;
+  const int H = shape->kv_heads, HQ = H * shape->group, D = shape->head_dim;
+  if (n_tokens < 0) return fail(TPK_ERR_INVALID, "n_tokens %d < 0", n_tokens);
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 16) return fail(TPK_ERR_INVALID, "rot_dim %d (a multiple of 16 up to %d)", rot_dim, D);
+  if (interleaved != 0 && interleaved != 1) return fail(TPK_ERR_INVALID, "interleaved %d (0 or 1)", interleaved);
+  const bool none = n_tokens == 0;  // empty rows have no address
+  const bool queries = q || q_out, keys = (k || v || k_pool || v_pool) && !(none && !k && !v && k_pool && v_pool);
+  if (queries && !(q && q_out)) return fail(TPK_ERR_INVALID, "q and q_out go together");
+  if (keys && !(k && v && k_pool && v_pool)) return fail(TPK_ERR_INVALID, "k, v and both pools go together");
+  if (!queries && !keys && !none) return fail(TPK_ERR_INVALID, "nothing to rotate or store");
+  if (keys && !slot_map && !none) return fail(TPK_ERR_INVALID, "null slot_map");
+  if (rot_dim > 0) {
+    if ((!positions && !none) || !inv_freq) return fail(TPK_ERR_INVALID, "null positions or inv_freq");
+    if (n_axes < 1 || n_axes > 4) return fail(TPK_ERR_INVALID, "n_axes %d out of [1, 4]", n_axes);
+  }
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool))
+    return fail(TPK_ERR_INVALID, "q, k, v, q_out and pools must be 16-byte aligned");
+  if (!aligned_to(4, positions, inv_freq) || !aligned_to(8, slot_map))
+    return fail(TPK_ERR_INVALID, "positions, inv_freq or slot_map is not aligned to its elements");
+  if (norms) {
+    if (!std::isfinite(norms->eps) || norms->eps < 0.f) return fail(TPK_ERR_INVALID, "eps %g (finite, not negative)", norms->eps);
+    if (!aligned16(norms->q_weight) || !aligned16(norms->k_weight))
+      return fail(TPK_ERR_INVALID, "q_weight and k_weight must be 16-byte aligned");
+  }
+  if (queries) {
+    st = check_stride("q_stride", q_stride, (int64_t)HQ * D);
+    if (st == TPK_OK) st = check_stride("q_out_stride", q_out_stride, (int64_t)HQ * D);
+    if (st != TPK_OK) return st;
+    if (q == q_out && q_stride != q_out_stride) return fail(TPK_ERR_INVALID, "q_out is q with another stride");
+  }
+  if (keys) {
+    st = check_stride("k_stride", k_stride, (int64_t)H * D);
+    if (st == TPK_OK) st = check_stride("v_stride", v_stride, (int64_t)H * D);
+    if (st != TPK_OK) return st;
+  }
+  RopeParams p;
+  std::memset(&p, 0, sizeof p);
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    p.axis_of[j] = axis_of ? axis_of[j] : 0;
+    if (p.axis_of[j] >= n_axes) return fail(TPK_ERR_INVALID, "axis_of[%d] = %d of %d axes", j, p.axis_of[j], n_axes);
+  }
+  if (none) return TPK_OK;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_pool = static_cast<uint16_t*>(k_pool);
+  p.v_pool = static_cast<uint16_t*>(v_pool);
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.slot_map = slot_map;
+  if (norms) {
+    p.q_weight = static_cast<const uint16_t*>(norms->q_weight);
+    p.k_weight = static_cast<const uint16_t*>(norms->k_weight);
+    p.eps = norms->eps;
+  }
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.slot_limit = shape->kv_slots * kPageTokens;
+  p.status = device_status_word();
+  if (!p.status) return fail(TPK_ERR_CUDA, "cannot resolve the device status word");
+  p.n_tokens = n_tokens;
+  p.H = H;
+  p.HQ = queries ? HQ : 0;
+  p.D = D;
+  p.rot = rot_dim;
+  const cudaError_t e = (norms ? launch_norm_rope : launch_rope)(p, shape->dtype, interleaved, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TPK_OK : cuda_fail(e, "rotary store launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -288,67 +373,19 @@ tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const 
                               const int32_t* positions, int n_axes, const uint8_t* axis_of, const float* inv_freq,
                               int rot_dim, int interleaved, const int64_t* slot_map, void* q_out,
                               int64_t q_out_stride, void* k_pool, void* v_pool, tpk_stream_t stream) {
-  tpk_status st = check_paged(shape);
-  if (st != TPK_OK) return st;
-  const int H = shape->kv_heads, HQ = H * shape->group, D = shape->head_dim;
-  if (n_tokens < 0) return fail(TPK_ERR_INVALID, "n_tokens %d < 0", n_tokens);
-  if (rot_dim < 0 || rot_dim > D || rot_dim % 16) return fail(TPK_ERR_INVALID, "rot_dim %d (a multiple of 16 up to %d)", rot_dim, D);
-  if (interleaved != 0 && interleaved != 1) return fail(TPK_ERR_INVALID, "interleaved %d (0 or 1)", interleaved);
-  const bool none = n_tokens == 0;  // empty rows have no address
-  const bool queries = q || q_out, keys = (k || v || k_pool || v_pool) && !(none && !k && !v && k_pool && v_pool);
-  if (queries && !(q && q_out)) return fail(TPK_ERR_INVALID, "q and q_out go together");
-  if (keys && !(k && v && k_pool && v_pool)) return fail(TPK_ERR_INVALID, "k, v and both pools go together");
-  if (!queries && !keys && !none) return fail(TPK_ERR_INVALID, "nothing to rotate or store");
-  if (keys && !slot_map && !none) return fail(TPK_ERR_INVALID, "null slot_map");
-  if (rot_dim > 0) {
-    if ((!positions && !none) || !inv_freq) return fail(TPK_ERR_INVALID, "null positions or inv_freq");
-    if (n_axes < 1 || n_axes > 4) return fail(TPK_ERR_INVALID, "n_axes %d out of [1, 4]", n_axes);
-  }
-  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool))
-    return fail(TPK_ERR_INVALID, "q, k, v, q_out and pools must be 16-byte aligned");
-  if (!aligned_to(4, positions, inv_freq) || !aligned_to(8, slot_map))
-    return fail(TPK_ERR_INVALID, "positions, inv_freq or slot_map is not aligned to its elements");
-  if (queries) {
-    st = check_stride("q_stride", q_stride, (int64_t)HQ * D);
-    if (st == TPK_OK) st = check_stride("q_out_stride", q_out_stride, (int64_t)HQ * D);
-    if (st != TPK_OK) return st;
-    if (q == q_out && q_stride != q_out_stride) return fail(TPK_ERR_INVALID, "q_out is q with another stride");
-  }
-  if (keys) {
-    st = check_stride("k_stride", k_stride, (int64_t)H * D);
-    if (st == TPK_OK) st = check_stride("v_stride", v_stride, (int64_t)H * D);
-    if (st != TPK_OK) return st;
-  }
-  RopeParams p;
-  std::memset(&p, 0, sizeof p);
-  for (int j = 0; j < rot_dim / 2; ++j) {
-    p.axis_of[j] = axis_of ? axis_of[j] : 0;
-    if (p.axis_of[j] >= n_axes) return fail(TPK_ERR_INVALID, "axis_of[%d] = %d of %d axes", j, p.axis_of[j], n_axes);
-  }
-  if (none) return TPK_OK;
-  p.q = static_cast<const uint16_t*>(q);
-  p.k = static_cast<const uint16_t*>(k);
-  p.v = static_cast<const uint16_t*>(v);
-  p.q_out = static_cast<uint16_t*>(q_out);
-  p.k_pool = static_cast<uint16_t*>(k_pool);
-  p.v_pool = static_cast<uint16_t*>(v_pool);
-  p.positions = positions;
-  p.inv_freq = inv_freq;
-  p.slot_map = slot_map;
-  p.q_stride = q_stride;
-  p.k_stride = k_stride;
-  p.v_stride = v_stride;
-  p.q_out_stride = q_out_stride;
-  p.slot_limit = shape->kv_slots * kPageTokens;
-  p.status = device_status_word();
-  if (!p.status) return fail(TPK_ERR_CUDA, "cannot resolve the device status word");
-  p.n_tokens = n_tokens;
-  p.H = H;
-  p.HQ = queries ? HQ : 0;
-  p.D = D;
-  p.rot = rot_dim;
-  const cudaError_t e = launch_rope(p, shape->dtype, interleaved, reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? TPK_OK : cuda_fail(e, "rotary store launch");
+  return rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, nullptr, positions, n_axes, axis_of, inv_freq,
+                     rot_dim, interleaved, slot_map, q_out, q_out_stride, k_pool, v_pool, stream);
+}
+
+tpk_status tpk_kv_norm_rope_append(const tpk_paged_shape* shape, int n_tokens, const void* q, int64_t q_stride,
+                                   const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                   const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+                                   int n_axes, const uint8_t* axis_of, const float* inv_freq, int rot_dim,
+                                   int interleaved, const int64_t* slot_map, void* q_out, int64_t q_out_stride,
+                                   void* k_pool, void* v_pool, tpk_stream_t stream) {
+  const Norms norms = {q_weight, k_weight, eps};
+  return rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, &norms, positions, n_axes, axis_of, inv_freq,
+                     rot_dim, interleaved, slot_map, q_out, q_out_stride, k_pool, v_pool, stream);
 }
 
 size_t tpk_decode_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req) {

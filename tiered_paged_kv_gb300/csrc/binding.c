@@ -82,6 +82,13 @@ static int narrow(reader* r) {
   return (int)v;
 }
 
+static float real(reader* r) {
+  PyObject* o = take(r);
+  const double v = o ? PyFloat_AsDouble(o) : 0.0;
+  if (v == -1.0 && PyErr_Occurred()) r->bad = 1;
+  return (float)v;
+}
+
 /* A buffer of at least `bytes` bytes, or NULL for None; released by the caller. */
 static const void* buffer(reader* r, Py_buffer* b, Py_ssize_t bytes) {
   PyObject* o = take(r);
@@ -142,8 +149,8 @@ static PyObject* kv_tables_update(PyObject* self, PyObject* const* args, Py_ssiz
   return done(&r, st);
 }
 
-static PyObject* kv_rope_append(PyObject* self, PyObject* const* args, Py_ssize_t n) {
-  (void)self;
+/* Both rotary stores: `norm` has the heads' factors after v_stride. */
+static PyObject* rope_append(PyObject* const* args, Py_ssize_t n, int norm) {
   reader r = {args, n, 0, 0};
   Py_buffer sb, ab;
   const tpk_paged_shape* shape = shape_of(&r, &sb);
@@ -154,6 +161,8 @@ static PyObject* kv_rope_append(PyObject* self, PyObject* const* args, Py_ssize_
   const int64_t k_stride = wide(&r);
   const void* v = pointer(&r);
   const int64_t v_stride = wide(&r);
+  const void *q_weight = norm ? pointer(&r) : NULL, *k_weight = norm ? pointer(&r) : NULL;
+  const float eps = norm ? real(&r) : 0.f;
   const int32_t* positions = pointer(&r);
   const int n_axes = narrow(&r);
   const uint8_t* axis_of = buffer(&r, &ab, 0);
@@ -168,11 +177,24 @@ static PyObject* kv_rope_append(PyObject* self, PyObject* const* args, Py_ssize_
     PyErr_Format(PyExc_ValueError, "axis_of has %zd bytes, not %d", ab.len, rot_dim / 2);
     r.bad = 1;
   }
-  RUN(r, tpk_kv_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, positions, n_axes, axis_of,
-                            inv_freq, rot_dim, interleaved, slot_map, q_out, q_out_stride, k_pool, v_pool, s));
+  RUN(r, norm ? tpk_kv_norm_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps,
+                                        positions, n_axes, axis_of, inv_freq, rot_dim, interleaved, slot_map, q_out,
+                                        q_out_stride, k_pool, v_pool, s)
+              : tpk_kv_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, positions, n_axes, axis_of,
+                                   inv_freq, rot_dim, interleaved, slot_map, q_out, q_out_stride, k_pool, v_pool, s));
   if (sb.obj) PyBuffer_Release(&sb);
   if (ab.obj) PyBuffer_Release(&ab);
   return done(&r, st);
+}
+
+static PyObject* kv_rope_append(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  (void)self;
+  return rope_append(args, n, 0);
+}
+
+static PyObject* kv_norm_rope_append(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  (void)self;
+  return rope_append(args, n, 1);
 }
 
 static PyObject* decode_attn_paged(PyObject* self, PyObject* const* args, Py_ssize_t n) {
@@ -230,7 +252,7 @@ static PyObject* set_shape_type(PyObject* self, PyObject* type) {
 }
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
-static PyMethodDef methods[] = {METHOD(kv_tables_update), METHOD(kv_rope_append), METHOD(decode_attn_paged),
+static PyMethodDef methods[] = {METHOD(kv_tables_update), METHOD(kv_rope_append), METHOD(kv_norm_rope_append), METHOD(decode_attn_paged),
                                 METHOD(cross_attn_paged), {"set_shape_type", set_shape_type, METH_O, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tpk_call", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -16,7 +16,7 @@
 // shared memory once per block and serve every head.  Bound: HBM, (2 HQ + 4 H) D * 2
 // bytes per token.  Measured: 8,200 tokens of 32 + 8 heads of 128 (202 MB) 33.6 us, 6.0
 // TB/s; 16 tokens of 32 + 4 heads of 256 2.3 us.
-#include "paged.cuh"
+#include "rope.cuh"
 
 namespace tpk {
 
@@ -24,19 +24,6 @@ constexpr int kRopeThreads = 256;  // at most
 constexpr int kRopePairs = 1024;   // angles a block holds: tokens * rot / 2
 constexpr int kRopeTokens = 8;     // tokens of a block, at most (4: 39.1 us, 8: 36.5, 16: 40.9 at 8200 tokens)
 constexpr int kRopeUnroll = 4;
-
-// frac(f / (2 pi)) in units of 2^-64 turns, |f| < 2^32.
-__device__ __forceinline__ uint64_t turns64(float f) {
-  const uint32_t w = __float_as_uint(f);
-  const int e = (w >> 23) & 0xff;
-  const uint32_t m = (w & 0x7fffff) | (e ? 0x800000u : 0);
-  // 1 / (2 pi) * 2^96
-  const unsigned __int128 c = ((unsigned __int128)0x28be60dbu << 64) | 0x9391054a7f09d5f4ull;
-  const int shift = 182 - (e ? e : 1);  // f = m 2^(e - 150), so F = m c 2^(e - 150) 2^(64 - 96)
-  const unsigned __int128 x = m * c;
-  const uint64_t t = shift < 128 ? (uint64_t)(x >> shift) : 0;  // at least 24
-  return (w >> 31) ? 0 - t : t;
-}
 
 template <typename T, bool kPairs>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p, int per, int tasks,
@@ -77,12 +64,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   for (int i = tid; i < nt * half; i += blockDim.x) {
     const int t = i / half, x = i - t * half;
     const int64_t pos = p.positions[(int64_t)p.axis_of[x] * p.n_tokens + t0 + t];
-    const float f = p.inv_freq[x];
-    const uint64_t angle = turns64(f) * (uint64_t)pos;
-    float s, c;
-    sincospif((float)(int32_t)((angle + 0x80000000u) >> 32) * 0x1p-31f, &s, &c);  // of pi * (2 * turns)
-    if (!(fabsf(f) < 0x1p32f)) s = c = __int_as_float(0x7fffffff);
-    reinterpret_cast<float2*>(turn + t * (half >> 1) + (x >> 1 & 3) * (half >> 3) + (x >> 3))[x & 1] = make_float2(c, s);
+    const float2 cs = turned_by(p.inv_freq[x], pos);
+    reinterpret_cast<float2*>(turn + t * (half >> 1) + (x >> 1 & 3) * (half >> 3) + (x >> 3))[x & 1] = cs;
   }
   if (tid < nt) {
     const int64_t slot = p.slot_map ? p.slot_map[t0 + tid] : 0;

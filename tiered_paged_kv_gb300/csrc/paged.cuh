@@ -40,13 +40,17 @@ struct RopeParams {
   const int32_t* positions;
   const float* inv_freq;
   const int64_t* slot_map;  // null: every row is live
+  const uint16_t* q_weight;  // norms: a factor for each channel, or null (ones)
+  const uint16_t* k_weight;
   int64_t q_stride, k_stride, v_stride, q_out_stride;
   int64_t slot_limit;  // kv_slots * 64
   int* status;
   int n_tokens, H, HQ, D, rot;
+  float eps;  // norms: added to the mean square
   uint8_t axis_of[128];
 };
 cudaError_t launch_rope(const RopeParams& p, int dtype, int interleaved, cudaStream_t stream);
+cudaError_t launch_norm_rope(const RopeParams& p, int dtype, int interleaved, cudaStream_t stream);
 
 // --------------------------------------------------------------- attention
 constexpr int kBoxRows = 16;  // rows of a page in one copy of the split kernel: one warp's
@@ -196,6 +200,33 @@ __device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.laun
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Request b's attended tokens [lo, hi), cut into what its table row can hold.
