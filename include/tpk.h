@@ -494,6 +494,97 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
                                 tpk_stream_t stream);
 
 /*
+ * Pages that several requests share.  A request's row of the page table may name pages
+ * that other rows name too: answers sampled from one prompt, the beams of a search, a
+ * prompt kept for later.  shares[x] counts the holders of slot x beyond the first (0 for
+ * a slot with one holder, and for a free one), so that a batch without shared pages has
+ * zeros, as tpk_kv_tables_update leaves them; pages held outside the batch are counted
+ * in by the caller.  A request that holds shared pages is ended or cut by the call below:
+ * tpk_kv_tables_update pushes the pages it gives back whoever else holds them (it may
+ * grow such a request).
+ *
+ * Fork, end and cut, for all requests at once.  Request b becomes the first len_keep[b]
+ * tokens (len_keep NULL: all) of what request source[b] was before the call: another
+ * request's history, or its own (cut where len_keep[b] is less than its length, as it was
+ * otherwise); with source[b] = -1 it ends.  Whole pages are shared.  A history that ends
+ * inside a page will be written on there, so that page becomes the request's alone:
+ *   - a request that stays as it was keeps its pages;
+ *   - if nobody else holds the page after the call, the first request in order that asks
+ *     for it keeps it;
+ *   - every other one gets a new slot, copy_dst[b], for the rows of slot copy_src[b], which
+ *     tpk_kv_pages_copy then moves.
+ * First the slots that nobody holds any more are pushed on the stack of free slots, the
+ * highest first; then the new slots are taken from its top, in request order.  A request
+ * for whose copy no slot is left keeps its whole pages only; one whose source, length or
+ * len_keep is out of range (or more than its source has) stays as it was: both have
+ * granted[b] = 0.
+ *   source, len_in, len_keep  dev int32 [n_req]; len_in: the lengths before the call
+ *   table_in, table_out  dev int32 [n_req][max_pages], not the same; entries of table_out
+ *                        past a request's pages are left as they were
+ *   shares_in, shares_out     dev int32 [kv_slots] (may be the same)
+ *   free_slots           dev int32 [free_cap], updated in place (what is not on the stack
+ *                        afterwards is left as it was); n_free_in, n_free_out: dev
+ *                        int32 [1] (may be the same; a count out of [0, free_cap] is
+ *                        clamped; slots pushed past free_cap are dropped)
+ *   len_out              dev int32 [n_req] (may be len_in); granted: dev int32 [n_req]
+ *   copy_src, copy_dst   dev int32 [n_req]: -1 where nothing is copied
+ * Lengths out of [0, 64 * max_pages], table entries outside the pool, more releases of a
+ * slot than it has holders, and dropped slots set bit 0 of the device status; such entries
+ * are left out.  Outputs overlap nothing else.
+ * ws: dev workspace of tpk_kv_pages_workspace_bytes(kv_slots, n_req) bytes, 16-byte aligned
+ * (no initialisation); calls sharing one must not overlap on the GPU.  n_req in [1, 4096],
+ * n_req * max_pages < 2^31, kv_slots + free_cap < 2^31.  Capturable once the device has
+ * seen one uncaptured call.
+ */
+size_t tpk_kv_pages_workspace_bytes(int64_t kv_slots, int n_req);
+tpk_status tpk_kv_pages_fork(int n_req, int max_pages, int64_t kv_slots, const int32_t* source, const int32_t* len_in,
+                             const int32_t* len_keep, const int32_t* table_in, int32_t* table_out,
+                             const int32_t* shares_in, int32_t* shares_out, int32_t* free_slots, int free_cap,
+                             const int32_t* n_free_in, int32_t* n_free_out, int32_t* len_out, int32_t* granted,
+                             int32_t* copy_src, int32_t* copy_dst, void* ws, size_t ws_bytes, tpk_stream_t stream);
+
+/*
+ * Compaction: pages move from the top of the pool into free slots at its bottom, so that
+ * the pool's end can be given back.  The slots not on the stack are in use.  The r-th
+ * lowest free slot takes the page of the r-th highest slot in use, for as long as that is
+ * higher and r < max_copies (few at a time, over several calls, or all at once).
+ *   n_tokens             dev int32 [n_req]: tokens of each table row
+ *   table_in, table_out  dev int32 [n_req][max_pages] (may be the same): the rows' pages
+ *                        get their new slots, other entries of table_out are left alone
+ *   shares_in, shares_out     dev int32 [kv_slots] (may be the same): holders go along
+ *   free_in, free_out    dev int32 [free_cap] (may be the same): free_out is the stack
+ *                        afterwards, the lowest slot on top; n_free_in, n_free_out: dev
+ *                        int32 [1] (may be the same)
+ *   new_slot             dev int32 [kv_slots]: where the page of each slot in use is now
+ *                        (for holders outside the batch); -1 for the free ones
+ *   copy_src, copy_dst   dev int32 [max_copies], -1 past the last; n_copies: dev int32 [1].
+ *                        tpk_kv_pages_copy moves the pages: no slot is in both lists.
+ * Free entries outside the pool, table entries that are on the stack or outside the pool
+ * (left as they are), lengths out of range and a full stack set bit 0 of the device status.
+ * Workspace, limits and capture as for tpk_kv_pages_fork; max_copies in [0, kv_slots].
+ */
+tpk_status tpk_kv_pages_compact(int n_req, int max_pages, int64_t kv_slots, const int32_t* n_tokens,
+                                const int32_t* table_in, int32_t* table_out, const int32_t* shares_in,
+                                int32_t* shares_out, const int32_t* free_in, int32_t* free_out, int free_cap,
+                                const int32_t* n_free_in, int32_t* n_free_out, int32_t* new_slot, int max_copies,
+                                int32_t* copy_src, int32_t* copy_dst, int32_t* n_copies, void* ws, size_t ws_bytes,
+                                tpk_stream_t stream);
+
+/*
+ * Copies pages within the pools of n_layers layers: slot src[i] to slot dst[i], of every
+ * pool.  Pairs with a negative slot are skipped (the lists of the two calls above as they
+ * are), pairs outside the pool too, setting bit 0 of the device status.  No slot may be the
+ * destination of two pairs, nor a source and a destination (a pair of equal slots is
+ * skipped).
+ *   k_pools, v_pools     host arrays of n_layers device pools [kv_slots][kv_heads][64][head_dim]
+ *   src, dst             dev int32 [n_pages]
+ * Of the shape kv_heads, head_dim, dtype and kv_slots count.  n_layers in [1, 4096]; n_pages
+ * >= 0 (0 is a no-op).
+ */
+tpk_status tpk_kv_pages_copy(const tpk_paged_shape* shape, int n_layers, void* const* k_pools, void* const* v_pools,
+                             int n_pages, const int32_t* src, const int32_t* dst, tpk_stream_t stream);
+
+/*
  * Rotary positions with up to four axes, and the store of new keys and values into
  * their pages.  Token t's row of q (or k) is [heads][D] at q + t * q_stride elements.
  * The first rot_dim channels of each head are rotated, pair j of rot_dim / 2 by the

@@ -28,7 +28,8 @@ __all__ = [
     "get_device_status",
     "static_scratch_bytes", "decode_hybrid_batched_static", "Stager", "Tiers", "TiersPlan",
     "PACK13_RECORD_BYTES", "PACK13_PLANE_ENC", "PACK13_PLANE_RAW", "kv_pack13_pages", "kv_unpack13_pages",
-    "PagedShape", "BF16", "F16", "kv_tables_update", "kv_rope_append", "kv_norm_rope_append", "decode_paged_workspace_bytes",
+    "PagedShape", "BF16", "F16", "kv_tables_update", "kv_rope_append", "kv_norm_rope_append", "kv_pages_workspace_bytes",
+    "kv_pages_fork", "kv_pages_compact", "kv_pages_copy", "decode_paged_workspace_bytes",
     "decode_attn_paged", "cross_paged_workspace_bytes", "cross_attn_paged",
 ]
 
@@ -143,6 +144,12 @@ def lib():
                                          vp, vp, vp]
         L.tpk_kv_norm_rope_append.argtypes = [gp, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, vp, i32, vp, vp,
                                               i32, i32, vp, vp, i64, vp, vp, vp]
+        L.tpk_kv_pages_workspace_bytes.argtypes = [i64, i32]
+        L.tpk_kv_pages_workspace_bytes.restype = sz
+        L.tpk_kv_pages_fork.argtypes = [i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.tpk_kv_pages_compact.argtypes = [i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, sz,
+                                           vp]
+        L.tpk_kv_pages_copy.argtypes = [gp, i32, pp, pp, i32, vp, vp, vp]
         L.tpk_decode_paged_workspace_bytes.argtypes = [gp, i32]
         L.tpk_decode_paged_workspace_bytes.restype = sz
         L.tpk_decode_attn_paged.argtypes = [gp, i32, vp, i64, vp, vp, vp, vp, vp, vp, i64, i32, vp, vp, sz, vp]
@@ -150,7 +157,7 @@ def lib():
         L.tpk_cross_paged_workspace_bytes.restype = sz
         L.tpk_cross_attn_paged.argtypes = [gp, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, sz, vp]
         for name in ("tpk_kv_tables_update", "tpk_kv_rope_append", "tpk_kv_norm_rope_append", "tpk_decode_attn_paged",
-                     "tpk_cross_attn_paged"):
+                     "tpk_cross_attn_paged", "tpk_kv_pages_fork", "tpk_kv_pages_compact", "tpk_kv_pages_copy"):
             getattr(L, name).restype = i32
         for name in ("tpk_kv_quantize_pages", "tpk_kv_quantize_pages_given_scales", "tpk_kv_pack13_pages",
                      "tpk_kv_unpack13_pages", "tpk_decode_attn_exact",
@@ -342,6 +349,40 @@ def kv_norm_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, 
     st = (_call or _calls()).kv_norm_rope_append(shape, n_tokens, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight,
                                                  eps, positions, n_axes, axis_of, inv_freq, rot_dim, interleaved,
                                                  slot_map, q_out, q_out_stride, k_pool, v_pool, stream)
+    if st:
+        _check(st)
+
+
+def kv_pages_workspace_bytes(kv_slots, n_req):
+    return int(lib().tpk_kv_pages_workspace_bytes(kv_slots, n_req))
+
+
+def kv_pages_fork(n_req, max_pages, kv_slots, source, len_in, len_keep, table_in, table_out, shares_in, shares_out, free_slots,
+                  free_cap, n_free_in, n_free_out, len_out, granted, copy_src, copy_dst, ws, ws_bytes, stream=None):
+    """Requests become (parts of) others, end or are cut, sharing whole pages (see
+    tpk_kv_pages_fork); every array is a device buffer."""
+    st = (_call or _calls()).kv_pages_fork(n_req, max_pages, kv_slots, source, len_in, len_keep, table_in, table_out, shares_in,
+                                           shares_out, free_slots, free_cap, n_free_in, n_free_out, len_out, granted,
+                                           copy_src, copy_dst, ws, ws_bytes, stream)
+    if st:
+        _check(st)
+
+
+def kv_pages_compact(n_req, max_pages, kv_slots, n_tokens, table_in, table_out, shares_in, shares_out, free_in, free_out, free_cap,
+                     n_free_in, n_free_out, new_slot, max_copies, copy_src, copy_dst, n_copies, ws, ws_bytes, stream=None):
+    """Pages from the top of the pool into free slots at its bottom (see
+    tpk_kv_pages_compact); every array is a device buffer."""
+    st = (_call or _calls()).kv_pages_compact(n_req, max_pages, kv_slots, n_tokens, table_in, table_out, shares_in, shares_out,
+                                              free_in, free_out, free_cap, n_free_in, n_free_out, new_slot, max_copies,
+                                              copy_src, copy_dst, n_copies, ws, ws_bytes, stream)
+    if st:
+        _check(st)
+
+
+def kv_pages_copy(shape, k_pools, v_pools, n_pages, src, dst, stream=None):
+    """Slot src[i] to slot dst[i] in every pool (see tpk_kv_pages_copy); k_pools and v_pools
+    are lists of one pool per layer."""
+    st = (_call or _calls()).kv_pages_copy(shape, k_pools, v_pools, n_pages, src, dst, stream)
     if st:
         _check(st)
 

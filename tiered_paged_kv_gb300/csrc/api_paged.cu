@@ -201,6 +201,24 @@ tpk_status check_counts(const tpk_paged_shape* s, int n_req) {
   return TPK_OK;
 }
 
+// Workspace of the calls on shared pages: counts, then three words for each slot.
+constexpr int kMaxLayers = 4096, kPagesCounts = 64;
+size_t pages_ws_bytes(int64_t kv_slots) { return align256((kPagesCounts + 3 * (size_t)kv_slots) * sizeof(int32_t)); }
+
+tpk_status check_pages(int n_req, int max_pages, int64_t kv_slots, int free_cap, const void* ws, size_t ws_bytes) {
+  if (n_req < 1 || n_req > kMaxPagedReq) return fail(TPK_ERR_INVALID, "n_req %d out of [1, %d]", n_req, kMaxPagedReq);
+  if (max_pages < 1 || max_pages > kMaxTableRow || (int64_t)n_req * max_pages > 0x7fffffffLL)
+    return fail(TPK_ERR_INVALID, "page table of %d x %d entries", n_req, max_pages);
+  if (free_cap < 0) return fail(TPK_ERR_INVALID, "free_cap %d < 0", free_cap);
+  if (kv_slots < 1 || kv_slots > 0x7fffffffLL - free_cap - 8192)
+    return fail(TPK_ERR_INVALID, "kv_slots %lld", (long long)kv_slots);
+  if (!ws) return fail(TPK_ERR_INVALID, "null pointer argument");
+  if (!aligned16(ws)) return fail(TPK_ERR_INVALID, "ws must be 16-byte aligned");
+  const size_t need = pages_ws_bytes(kv_slots);
+  if (ws_bytes < need) return fail(TPK_ERR_NOMEM, "workspace %zu bytes < %zu required", ws_bytes, need);
+  return TPK_OK;
+}
+
 // What both attention calls check and fill in.
 tpk_status begin_attention(PagedParams& p, const tpk_paged_shape* s, int n_req, const void* q, int64_t q_stride,
                            const void* k_pool, const void* v_pool, const int32_t* page_table, const int32_t* n_tokens,
@@ -366,6 +384,131 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
   p.max_tokens = max_tokens;
   const cudaError_t e = launch_tables(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? TPK_OK : cuda_fail(e, "tables launch");
+}
+
+size_t tpk_kv_pages_workspace_bytes(int64_t kv_slots, int n_req) {
+  return kv_slots >= 1 && kv_slots <= 0x7fffffff && n_req >= 1 && n_req <= kMaxPagedReq ? pages_ws_bytes(kv_slots) : 0;
+}
+
+tpk_status tpk_kv_pages_fork(int n_req, int max_pages, int64_t kv_slots, const int32_t* source, const int32_t* len_in,
+                             const int32_t* len_keep, const int32_t* table_in, int32_t* table_out,
+                             const int32_t* shares_in, int32_t* shares_out, int32_t* free_slots, int free_cap,
+                             const int32_t* n_free_in, int32_t* n_free_out, int32_t* len_out, int32_t* granted,
+                             int32_t* copy_src, int32_t* copy_dst, void* ws, size_t ws_bytes, tpk_stream_t stream) {
+  const tpk_status st = check_pages(n_req, max_pages, kv_slots, free_cap, ws, ws_bytes);
+  if (st != TPK_OK) return st;
+  if (!source || !len_in || !table_in || !table_out || !shares_in || !shares_out || (free_cap > 0 && !free_slots) ||
+      !n_free_in || !n_free_out || !len_out || !granted || !copy_src || !copy_dst)
+    return fail(TPK_ERR_INVALID, "null pointer argument");
+  if (!aligned_to(4, source, len_in, len_keep, table_in, table_out, shares_in, shares_out, free_slots, n_free_in, n_free_out,
+                  len_out, granted, copy_src, copy_dst))
+    return fail(TPK_ERR_INVALID, "an array is not aligned to its elements");
+  if (table_in == table_out) return fail(TPK_ERR_INVALID, "table_out is table_in");
+  ForkParams p;
+  p.source = source;
+  p.len_in = len_in;
+  p.len_keep = len_keep;
+  p.table_in = table_in;
+  p.table_out = table_out;
+  p.shares_in = shares_in;
+  p.shares_out = shares_out;
+  p.free_slots = free_slots;
+  p.n_free_in = n_free_in;
+  p.n_free_out = n_free_out;
+  p.len_out = len_out;
+  p.granted = granted;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.counts = static_cast<int32_t*>(ws);
+  p.open = p.counts + kPagesCounts;
+  p.first = p.open + kv_slots;
+  p.pushed = p.first + kv_slots;
+  p.status = device_status_word();
+  if (!p.status) return fail(TPK_ERR_CUDA, "cannot resolve the device status word");
+  p.n_req = n_req;
+  p.max_pages = max_pages;
+  p.kv_slots = (int)kv_slots;
+  p.free_cap = free_cap;
+  const cudaError_t e = launch_fork(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TPK_OK : cuda_fail(e, "fork launch");
+}
+
+tpk_status tpk_kv_pages_compact(int n_req, int max_pages, int64_t kv_slots, const int32_t* n_tokens,
+                                const int32_t* table_in, int32_t* table_out, const int32_t* shares_in,
+                                int32_t* shares_out, const int32_t* free_in, int32_t* free_out, int free_cap,
+                                const int32_t* n_free_in, int32_t* n_free_out, int32_t* new_slot, int max_copies,
+                                int32_t* copy_src, int32_t* copy_dst, int32_t* n_copies, void* ws, size_t ws_bytes,
+                                tpk_stream_t stream) {
+  const tpk_status st = check_pages(n_req, max_pages, kv_slots, free_cap, ws, ws_bytes);
+  if (st != TPK_OK) return st;
+  if (max_copies < 0 || max_copies > kv_slots) return fail(TPK_ERR_INVALID, "max_copies %d out of [0, kv_slots]", max_copies);
+  if (!n_tokens || !table_in || !table_out || !shares_in || !shares_out || (free_cap > 0 && (!free_in || !free_out)) ||
+      !n_free_in || !n_free_out || !new_slot || !n_copies || (max_copies > 0 && (!copy_src || !copy_dst)))
+    return fail(TPK_ERR_INVALID, "null pointer argument");
+  if (!aligned_to(4, n_tokens, table_in, table_out, shares_in, shares_out, free_in, free_out, n_free_in, n_free_out, new_slot,
+                  copy_src, copy_dst, n_copies))
+    return fail(TPK_ERR_INVALID, "an array is not aligned to its elements");
+  CompactParams p;
+  p.n_tokens = n_tokens;
+  p.table_in = table_in;
+  p.table_out = table_out;
+  p.shares_in = shares_in;
+  p.shares_out = shares_out;
+  p.free_in = free_in;
+  p.free_out = free_out;
+  p.n_free_in = n_free_in;
+  p.n_free_out = n_free_out;
+  p.new_slot = new_slot;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.n_copies = n_copies;
+  p.counts = static_cast<int32_t*>(ws);
+  p.mark = p.counts + kPagesCounts;
+  p.status = device_status_word();
+  if (!p.status) return fail(TPK_ERR_CUDA, "cannot resolve the device status word");
+  p.n_req = n_req;
+  p.max_pages = max_pages;
+  p.kv_slots = (int)kv_slots;
+  p.free_cap = free_cap;
+  p.max_copies = max_copies;
+  const cudaError_t e = launch_compact(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TPK_OK : cuda_fail(e, "compaction launch");
+}
+
+tpk_status tpk_kv_pages_copy(const tpk_paged_shape* shape, int n_layers, void* const* k_pools, void* const* v_pools,
+                             int n_pages, const int32_t* src, const int32_t* dst, tpk_stream_t stream) {
+  const tpk_status st = check_paged(shape);
+  if (st != TPK_OK) return st;
+  if (n_layers < 1 || n_layers > kMaxLayers) return fail(TPK_ERR_INVALID, "n_layers %d out of [1, %d]", n_layers, kMaxLayers);
+  if (n_pages < 0) return fail(TPK_ERR_INVALID, "n_pages %d < 0", n_pages);
+  if (!k_pools || !v_pools) return fail(TPK_ERR_INVALID, "null pointer argument");
+  for (int i = 0; i < n_layers; ++i) {
+    if (!k_pools[i] || !v_pools[i]) return fail(TPK_ERR_INVALID, "null pool of layer %d", i);
+    if (!aligned16(k_pools[i]) || !aligned16(v_pools[i])) return fail(TPK_ERR_INVALID, "pools must be 16-byte aligned");
+  }
+  if (n_pages == 0) return TPK_OK;
+  if (!src || !dst) return fail(TPK_ERR_INVALID, "null pointer argument");
+  if (!aligned_to(4, src, dst)) return fail(TPK_ERR_INVALID, "src and dst must be 4-byte aligned");
+  PagesCopyParams p;
+  p.src = src;
+  p.dst = dst;
+  p.page_bytes = (int64_t)shape->kv_heads * kPageTokens * shape->head_dim * 2;
+  p.kv_slots = shape->kv_slots;
+  p.n_pages = n_pages;
+  p.status = device_status_word();
+  if (!p.status) return fail(TPK_ERR_CUDA, "cannot resolve the device status word");
+  for (int i = 0; i < n_layers; i += kCopyPools / 2) {
+    const int n = std::min(kCopyPools / 2, n_layers - i);
+    std::memset(p.pools, 0, sizeof p.pools);
+    for (int j = 0; j < n; ++j) {
+      p.pools[2 * j] = static_cast<uint8_t*>(k_pools[i + j]);
+      p.pools[2 * j + 1] = static_cast<uint8_t*>(v_pools[i + j]);
+    }
+    p.n_pools = 2 * n;
+    const cudaError_t e = launch_pages_copy(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "page copy launch");
+  }
+  return TPK_OK;
 }
 
 tpk_status tpk_kv_rope_append(const tpk_paged_shape* shape, int n_tokens, const void* q, int64_t q_stride,

@@ -243,6 +243,98 @@ static PyObject* cross_attn_paged(PyObject* self, PyObject* const* args, Py_ssiz
   return done(&r, st);
 }
 
+static PyObject* kv_pages_fork(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  (void)self;
+  reader r = {args, n, 0, 0};
+  const int n_req = narrow(&r), max_pages = narrow(&r);
+  const int64_t kv_slots = wide(&r);
+  const int32_t *source = pointer(&r), *len_in = pointer(&r), *len_keep = pointer(&r), *table_in = pointer(&r);
+  int32_t* table_out = pointer(&r);
+  const int32_t* shares_in = pointer(&r);
+  int32_t *shares_out = pointer(&r), *free_slots = pointer(&r);
+  const int free_cap = narrow(&r);
+  const int32_t* n_free_in = pointer(&r);
+  int32_t *n_free_out = pointer(&r), *len_out = pointer(&r), *granted = pointer(&r);
+  int32_t *copy_src = pointer(&r), *copy_dst = pointer(&r);
+  void* ws = pointer(&r);
+  const int64_t ws_bytes = wide(&r);
+  const tpk_stream_t s = stream(&r);
+  RUN(r, tpk_kv_pages_fork(n_req, max_pages, kv_slots, source, len_in, len_keep, table_in, table_out, shares_in, shares_out,
+                           free_slots, free_cap, n_free_in, n_free_out, len_out, granted, copy_src, copy_dst, ws,
+                           ws_bytes < 0 ? 0 : (size_t)ws_bytes, s));
+  return done(&r, st);
+}
+
+static PyObject* kv_pages_compact(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  (void)self;
+  reader r = {args, n, 0, 0};
+  const int n_req = narrow(&r), max_pages = narrow(&r);
+  const int64_t kv_slots = wide(&r);
+  const int32_t *n_tokens = pointer(&r), *table_in = pointer(&r);
+  int32_t* table_out = pointer(&r);
+  const int32_t* shares_in = pointer(&r);
+  int32_t* shares_out = pointer(&r);
+  const int32_t* free_in = pointer(&r);
+  int32_t* free_out = pointer(&r);
+  const int free_cap = narrow(&r);
+  const int32_t* n_free_in = pointer(&r);
+  int32_t *n_free_out = pointer(&r), *new_slot = pointer(&r);
+  const int max_copies = narrow(&r);
+  int32_t *copy_src = pointer(&r), *copy_dst = pointer(&r), *n_copies = pointer(&r);
+  void* ws = pointer(&r);
+  const int64_t ws_bytes = wide(&r);
+  const tpk_stream_t s = stream(&r);
+  RUN(r, tpk_kv_pages_compact(n_req, max_pages, kv_slots, n_tokens, table_in, table_out, shares_in, shares_out, free_in,
+                              free_out, free_cap, n_free_in, n_free_out, new_slot, max_copies, copy_src, copy_dst,
+                              n_copies, ws, ws_bytes < 0 ? 0 : (size_t)ws_bytes, s));
+  return done(&r, st);
+}
+
+/* The pointers of a list or tuple (freed by the caller), and how many. */
+static void** pointers(reader* r, Py_ssize_t* count) {
+  PyObject* o = take(r);
+  *count = 0;
+  if (!o) return NULL;
+  PyObject* list = PySequence_Fast(o, "a list of pools");
+  void** p = list ? PyMem_Malloc((PySequence_Fast_GET_SIZE(list) + 1) * sizeof(void*)) : NULL;
+  if (!p) {
+    if (list) PyErr_NoMemory();
+    Py_XDECREF(list);
+    r->bad = 1;
+    return NULL;
+  }
+  reader items = {PySequence_Fast_ITEMS(list), PySequence_Fast_GET_SIZE(list), 0, 0};
+  while (items.at < items.n && !items.bad) {
+    p[*count] = pointer(&items);
+    ++*count;
+  }
+  Py_DECREF(list);
+  if (items.bad) r->bad = 1;
+  return p;
+}
+
+static PyObject* kv_pages_copy(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  (void)self;
+  reader r = {args, n, 0, 0};
+  Py_buffer sb;
+  Py_ssize_t layers, others;
+  const tpk_paged_shape* shape = shape_of(&r, &sb);
+  void** k_pools = pointers(&r, &layers);
+  void** v_pools = pointers(&r, &others);
+  const int n_pages = narrow(&r);
+  const int32_t *src = pointer(&r), *dst = pointer(&r);
+  const tpk_stream_t s = stream(&r);
+  if (!r.bad && layers != others) {
+    PyErr_Format(PyExc_ValueError, "%zd pools of keys and %zd of values", layers, others);
+    r.bad = 1;
+  }
+  RUN(r, tpk_kv_pages_copy(shape, layers > INT32_MAX ? -1 : (int)layers, k_pools, v_pools, n_pages, src, dst, s));
+  if (sb.obj) PyBuffer_Release(&sb);
+  PyMem_Free(k_pools);
+  PyMem_Free(v_pools);
+  return done(&r, st);
+}
+
 static PyObject* set_shape_type(PyObject* self, PyObject* type) {
   (void)self;
   if (!PyType_Check(type)) return PyErr_Format(PyExc_TypeError, "a type, not %R", type);
@@ -253,7 +345,8 @@ static PyObject* set_shape_type(PyObject* self, PyObject* type) {
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(kv_tables_update), METHOD(kv_rope_append), METHOD(kv_norm_rope_append), METHOD(decode_attn_paged),
-                                METHOD(cross_attn_paged), {"set_shape_type", set_shape_type, METH_O, NULL},
+                                METHOD(cross_attn_paged), METHOD(kv_pages_fork), METHOD(kv_pages_compact),
+                                METHOD(kv_pages_copy), {"set_shape_type", set_shape_type, METH_O, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tpk_call", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -1,0 +1,468 @@
+// Upkeep of pages that several requests share: forks (with ends and cuts), compaction, and the
+// copies that these ask for.
+//
+// Forks and compaction are bookkeeping on whole numbers: a few bytes for each page-table entry
+// and each slot, in phases that each need all of the phase before.  Each call is one launch of one
+// cluster of kParts blocks, whose barrier separates the phases: a batch of 64 beams or a pool of
+// ten thousand slots is bound by the latency of its phases, not by what eight SMs can read, and a
+// barrier of a cluster costs less than a launch.  Sums and counts go by integer atomics, which
+// give the same in any order; ranks go by scans, so that the result is the one that the
+// definition's order gives.
+//
+// Bound: latency for those two, HBM for the copies (two bytes moved for each byte of a page).
+#include <climits>
+
+#include "paged.cuh"
+
+namespace tpk {
+
+constexpr int kParts = 8;  // blocks of the cluster (as many as every device takes)
+constexpr int kPartThreads = 1024;
+constexpr int kPartWarps = kPartThreads / 32;
+
+// All blocks of the cluster have come here, and see what the others wrote before.
+__device__ __forceinline__ void parts_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int my_part() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ int pages_of(int tokens) { return (tokens >> 6) + ((tokens & 63) != 0); }
+
+// How many of the block's threads below this one have the flag, and how many in all.
+__device__ __forceinline__ int rank_in_block(bool flag, int* warp_counts, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned votes = __ballot_sync(0xffffffffu, flag);
+  __syncthreads();  // the last call's counts have been read
+  if (lane == 0) warp_counts[warp] = __popc(votes);
+  __syncthreads();
+  const int mine = warp_counts[lane];
+  int inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += up;
+  }
+  total = __shfl_sync(0xffffffffu, inc, 31);
+  return __shfl_sync(0xffffffffu, inc - mine, warp) + __popc(votes & ((1u << lane) - 1));
+}
+
+// The slots, cut into equal stretches for the parts; within a stretch tiles of a block's width.
+struct Stretch {
+  int begin, end;
+  __device__ __forceinline__ Stretch(int n, int part) {
+    const int per = (int)(((int64_t)n + kParts - 1) / kParts);
+    begin = (int)min((int64_t)per * part, (int64_t)n);
+    end = min(begin + per, n);
+  }
+};
+
+// Counts of all parts, in global memory: what each part adds up before a barrier.
+__device__ __forceinline__ int before_part(const int* counts, int part) {
+  int sum = 0;
+  for (int i = 0; i < part; ++i) sum += __ldcg(counts + i);
+  return sum;
+}
+
+// ------------------------------------------------------------------- fork
+// Holders: shares_in[x] + 1 hold slot x.  A request that changes (another source, or cut) lets its
+// old pages go and takes up the whole pages that it keeps; base = holders after that.  A kept
+// history that ends inside page x makes x the request's open page: it will be written on.
+//   base = 0: the first of the requests with open page x keeps it, the others copy it;
+//   base > 0: all of them copy it.
+// A slot that is copied from is held by somebody, so that it is not handed out in the same call.
+constexpr int kMostReq = kMaxPagedReq;
+struct ForkShared {
+  int counts[kPartWarps];
+  int source[kMostReq];  // whose table row the request's pages come from
+  int keep[kMostReq];    // tokens it keeps
+  int fresh[kMostReq];   // the slot of its copied page; -1: none; -2: nothing to do, -3: refused
+};
+constexpr int kNone = -1, kSame = -2, kRefused = -3;
+
+__global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams p) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  ForkShared& S = *reinterpret_cast<ForkShared*>(raw);
+  const int tid = threadIdx.x, part = my_part(), n = p.n_req;
+  const int lane = tid & 31, warp = part * kPartWarps + (tid >> 5);
+  wait_before();
+  const int cap = (int)min((int64_t)p.max_pages * kPageTokens, (int64_t)INT_MAX);
+  bool bad = false;
+  auto length = [&](int b) {
+    const int v = p.len_in[b], c = min(max(v, 0), cap);
+    bad |= v != c;
+    return c;
+  };
+  const int n_free = min(max(*p.n_free_in, 0), p.free_cap);
+  // ---- what each request asks for (every part for itself)
+  for (int b = tid; b < n; b += kPartThreads) {
+    const int own = length(b);
+    int s = p.source[b], keep = 0, state = kNone;
+    if (s == -1) {
+      s = b;  // ends
+    } else if (s < 0 || s >= n) {
+      state = kRefused;
+    } else {
+      const int len = length(s);
+      keep = p.len_keep ? p.len_keep[b] : len;
+      if (keep < 0 || keep > len) state = kRefused;
+    }
+    if (state == kRefused) {
+      s = b;
+      keep = own;
+    } else if (s == b && keep == own) {
+      state = kSame;
+    }
+    S.source[b] = s;
+    S.keep[b] = keep;
+    S.fresh[b] = state;
+  }
+  const Stretch mine(p.kv_slots, part);
+  for (int i = mine.begin + tid; i < mine.end; i += kPartThreads) {
+    if (p.shares_in != p.shares_out) p.shares_out[i] = p.shares_in[i];
+    p.open[i] = 0;
+    p.first[i] = INT_MAX;
+  }
+  __syncthreads();
+  parts_meet();
+
+  // ---- holders: some warps to a request, or some requests to a warp
+  const int warps = kParts * kPartWarps, team = max(1, warps / n);
+  auto valid = [&](int x) {
+    const bool ok = x >= 0 && x < p.kv_slots;
+    bad |= !ok;
+    return ok;
+  };
+  for (int b = warp / team; b < n && warp < warps / team * team; b += warps / team) {
+    if (S.fresh[b] != kNone) continue;
+    const int32_t* const own = p.table_in + (int64_t)b * p.max_pages;
+    const int32_t* const from = p.table_in + (int64_t)S.source[b] * p.max_pages;
+    const int lost = pages_of(length(b)), kept = S.keep[b] >> 6;
+    for (int j = (warp % team) * 32 + lane; j < max(lost, kept); j += team * 32) {
+      const int x = j < lost ? own[j] : -1, y = j < kept ? from[j] : -1;
+      if (j < lost && j < kept && x == y) continue;
+      if (j < lost && valid(x)) atomicSub(p.shares_out + x, 1);
+      if (j < kept && valid(y)) atomicAdd(p.shares_out + y, 1);
+    }
+    if (warp % team == 0 && lane == 0 && (S.keep[b] & 63)) {
+      const int x = from[kept];
+      if (valid(x)) {
+        atomicAdd(p.open + x, 1);
+        atomicMin(p.first + x, b);
+      }
+    }
+  }
+  parts_meet();
+
+  // ---- slots: who keeps an open page, and which pages nobody holds
+  auto freed = [&](int i) { return __ldcg(p.shares_out + i) < 0 && __ldcg(p.open + i) == 0; };
+  int count = 0;
+  for (int i = mine.begin + tid; i < mine.end; i += kPartThreads) count += freed(i);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) count += __shfl_xor_sync(0xffffffffu, count, d);
+  if (lane == 0) S.counts[tid >> 5] = count;
+  __syncthreads();
+  if (tid < 32) {
+    int sum = S.counts[tid];
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (tid == 0) p.counts[part] = sum;
+  }
+  parts_meet();
+  const int all = before_part(p.counts, kParts);
+  // the highest is pushed first: those before are above
+  int at = all - before_part(p.counts, part + 1);
+  for (int i0 = mine.end; i0 > mine.begin; i0 -= kPartThreads) {
+    const int i = i0 - 1 - tid;
+    const bool here = i >= mine.begin, gone = here && freed(i);
+    int total;
+    const int rank = rank_in_block(gone, S.counts, total);
+    if (gone) p.pushed[at + rank] = i;
+    at += total;
+    if (!here) continue;
+    const int base = __ldcg(p.shares_out + i) + 1;
+    bad |= base < 0;
+    if (base <= 0) p.shares_out[i] = 0;
+    else p.first[i] = -1;  // others hold it: nobody writes on
+  }
+  parts_meet();
+
+  // ---- new slots for the pages that are copied, in request order (every part for itself)
+  const int there = min(n_free + all, p.free_cap);
+  int taken = 0;
+  for (int b0 = 0; b0 < n; b0 += kPartThreads) {
+    const int b = b0 + tid;
+    bool asks = false, lost = false;
+    int x = -1;
+    if (b < n && S.fresh[b] == kNone && (S.keep[b] & 63)) {
+      x = p.table_in[(int64_t)S.source[b] * p.max_pages + (S.keep[b] >> 6)];
+      if (valid(x)) asks = __ldcg(p.first + x) != b;
+      else lost = true;
+    }
+    int total;
+    const int rank = taken + rank_in_block(asks, S.counts, total);
+    taken += total;
+    // the stack's entries that this call pushed are not in free_slots yet
+    const int from = there - 1 - rank;
+    int got = kNone;
+    if (asks && rank < there) got = from < n_free ? p.free_slots[from] : __ldcg(p.pushed + from - n_free);
+    lost |= asks && rank >= there;
+    if (b >= n) continue;
+    const bool copied = asks && !lost, refused = lost || S.fresh[b] == kRefused;
+    if (lost) S.keep[b] &= ~63;
+    if (S.fresh[b] == kNone || lost) S.fresh[b] = copied ? got : kNone;
+    if (part == 0) {
+      p.len_out[b] = S.keep[b];
+      p.granted[b] = !refused;
+      p.copy_src[b] = copied ? x : -1;
+      p.copy_dst[b] = copied ? got : -1;
+    }
+  }
+  const int left = there - min(taken, there);
+  for (int i = n_free + part * kPartThreads + tid; i < left; i += kParts * kPartThreads)
+    p.free_slots[i] = __ldcg(p.pushed + i - n_free);
+  if (part == 0 && tid == 0) {
+    *p.n_free_out = left;
+    bad |= n_free + all > p.free_cap;
+  }
+  __syncthreads();
+
+  // ---- the new table rows
+  for (int b = warp / team; b < n && warp < warps / team * team; b += warps / team) {
+    const int32_t* const from = p.table_in + (int64_t)S.source[b] * p.max_pages;
+    int32_t* const to = p.table_out + (int64_t)b * p.max_pages;
+    const int pages = pages_of(S.keep[b]), fresh = S.fresh[b];
+    for (int j = (warp % team) * 32 + lane; j < pages; j += team * 32)
+      to[j] = fresh >= 0 && j == pages - 1 ? fresh : from[j];
+  }
+  if (bad) atomicOr(p.status, kStatusBadSlot);
+}
+
+// ------------------------------------------------------------- compaction
+// The r-th lowest free slot takes the page of the r-th highest slot in use, while that is above it
+// and r is below max_copies.  Then the stack holds the free slots, the lowest on top.
+constexpr int kHeld = 0, kFree = 1, kTaken = 2;  // marks: in use, free, free and taken by a page
+
+__global__ void __launch_bounds__(kPartThreads, 1) compact_kernel(const CompactParams p) {
+  __shared__ int counts[kPartWarps];
+  const int tid = threadIdx.x, lane = tid & 31, part = my_part(), slots = p.kv_slots;
+  const int step = kParts * kPartThreads, thread = part * kPartThreads + tid;
+  wait_before();
+  const int n_free = min(max(*p.n_free_in, 0), p.free_cap);
+  bool bad = false;
+  for (int i = thread; i < slots; i += step) p.mark[i] = kHeld;
+  for (int i = thread; i < p.max_copies; i += step) p.copy_src[i] = p.copy_dst[i] = -1;
+  parts_meet();
+  for (int i = thread; i < n_free; i += step) {
+    const int x = p.free_in[i];
+    if (x >= 0 && x < slots) p.mark[x] = kFree; else bad = true;
+  }
+  parts_meet();
+
+  // ---- both lists: free slots from the bottom, slots in use from the top
+  const Stretch mine(slots, part);
+  auto add_up = [&](int count, int* to) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) count += __shfl_xor_sync(0xffffffffu, count, d);
+    __syncthreads();
+    if (lane == 0) counts[tid >> 5] = count;
+    __syncthreads();
+    if (tid < 32) {
+      int sum = counts[tid];
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (tid == 0) to[part] = sum;
+    }
+  };
+  int count = 0;
+  for (int i = mine.begin + tid; i < mine.end; i += kPartThreads) count += __ldcg(p.mark + i) == kFree;
+  add_up(count, p.counts);
+  parts_meet();
+  const int all_free = before_part(p.counts, kParts), held = slots - all_free;
+  int low = before_part(p.counts, part);  // free slots below
+  for (int i0 = mine.begin; i0 < mine.end; i0 += kPartThreads) {
+    const int i = i0 + tid;
+    const bool here = i < mine.end, is_free = here && __ldcg(p.mark + i) == kFree;
+    int total;
+    const int below = low + rank_in_block(is_free, counts, total);
+    low += total;
+    if (!here) continue;
+    p.new_slot[i] = is_free ? -1 : i;
+    const int above = held - (i - below) - 1;  // slots in use above this one
+    if (is_free && below < p.max_copies) p.copy_dst[below] = i;
+    if (!is_free && above < p.max_copies) p.copy_src[above] = i;
+  }
+  parts_meet();
+
+  // ---- the moves: those of the front of both lists
+  auto goes = [&](int r) {
+    const int s = __ldcg(p.copy_src + r), d = __ldcg(p.copy_dst + r);
+    return d >= 0 && d < s;
+  };
+  if (thread == 0 && (p.max_copies == 0 || !goes(0))) *p.n_copies = 0;
+  for (int r = thread; r < p.max_copies; r += step) {
+    if (goes(r)) {
+      const int s = __ldcg(p.copy_src + r), d = __ldcg(p.copy_dst + r);
+      p.new_slot[s] = d;
+      p.mark[d] = kTaken;
+      // (an entry of the lists' rest is no move before and after it is cleared)
+      if (r + 1 == p.max_copies || !goes(r + 1)) *p.n_copies = r + 1;
+    } else {
+      p.copy_src[r] = p.copy_dst[r] = -1;
+    }
+  }
+  parts_meet();
+
+  // ---- holders and the stack
+  auto empty = [&](int i) {
+    const int m = __ldcg(p.mark + i);
+    return m == kFree || (m == kHeld && __ldcg(p.new_slot + i) != i);
+  };
+  count = 0;
+  for (int i = mine.begin + tid; i < mine.end; i += kPartThreads) count += empty(i);
+  add_up(count, p.counts + kParts);
+  parts_meet();
+  const int left = before_part(p.counts + kParts, kParts);
+  int at = left - before_part(p.counts + kParts, part + 1);  // the highest at the bottom
+  for (int i0 = mine.end; i0 > mine.begin; i0 -= kPartThreads) {
+    const int i = i0 - 1 - tid;
+    const bool here = i >= mine.begin, is_empty = here && empty(i);
+    int total;
+    const int rank = rank_in_block(is_empty, counts, total);
+    if (is_empty && at + rank < p.free_cap) p.free_out[at + rank] = i;
+    at += total;
+    if (!here) continue;
+    const int m = __ldcg(p.mark + i), to = __ldcg(p.new_slot + i);
+    // each slot in use brings its own holders along: no slot that is read here is written by another
+    if (m == kHeld && to != i) p.shares_out[to] = p.shares_in[i];
+    if (is_empty) p.shares_out[i] = 0;
+    else if (m == kHeld && p.shares_in != p.shares_out) p.shares_out[i] = p.shares_in[i];
+  }
+  if (thread == 0) {
+    *p.n_free_out = min(left, p.free_cap);
+    bad |= left > p.free_cap;
+  }
+
+  // ---- the table rows
+  const int cap = (int)min((int64_t)p.max_pages * kPageTokens, (int64_t)INT_MAX);
+  const int warp = thread >> 5, warps = step / 32, team = max(1, warps / p.n_req);
+  for (int b = warp / team; b < p.n_req && warp < warps / team * team; b += warps / team) {
+    const int v = p.n_tokens[b], c = min(max(v, 0), cap);
+    bad |= v != c;
+    const int64_t row = (int64_t)b * p.max_pages;
+    for (int j = (warp % team) * 32 + lane; j < pages_of(c); j += team * 32) {
+      const int x = p.table_in[row + j], y = x >= 0 && x < slots ? __ldcg(p.new_slot + x) : -1;
+      bad |= y < 0;  // out of the pool, or on the stack: left as it is
+      p.table_out[row + j] = y < 0 ? x : y;
+    }
+  }
+  if (bad) atomicOr(p.status, kStatusBadSlot);
+}
+
+// ------------------------------------------------------------------ copies
+// A block finds the pairs that are copies (kList entries at a time), then takes every gridDim-th
+// piece of their pages in all pools: kCopyBytes together, each thread's loads in flight at once.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 8;
+constexpr int kCopyBytes = kCopyThreads * kCopyUnroll * 16;
+constexpr int kList = 2048;
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ PagesCopyParams p) {
+  __shared__ int2 list[kList];
+  __shared__ int warp_counts[kCopyThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pieces = (int)((p.page_bytes + kCopyBytes - 1) / kCopyBytes);
+  wait_before();
+  int64_t turn = blockIdx.x;  // the block's next piece, counted from the current entries' first
+  for (int e0 = 0; e0 < p.n_pages; e0 += kList) {
+    const int n = min(kList, p.n_pages - e0);
+    int found = 0;
+    for (int i0 = 0; i0 < n; i0 += kCopyThreads) {
+      const int i = i0 + tid;
+      int s = -1, d = -1;
+      if (i < n) {
+        s = p.src[e0 + i];
+        d = p.dst[e0 + i];
+      }
+      bool live = s >= 0 && d >= 0 && s != d;
+      if (live && (s >= p.kv_slots || d >= p.kv_slots)) {
+        live = false;
+        if (blockIdx.x == 0) atomicOr(p.status, kStatusBadSlot);
+      }
+      const unsigned votes = __ballot_sync(0xffffffffu, live);
+      __syncthreads();
+      if (lane == 0) warp_counts[warp] = __popc(votes);
+      __syncthreads();
+      int before = found;
+      for (int w = 0; w < kCopyThreads / 32; ++w) {
+        if (w < warp) before += warp_counts[w];
+        found += warp_counts[w];
+      }
+      if (live) list[before + __popc(votes & ((1u << lane) - 1))] = make_int2(s, d);
+    }
+    __syncthreads();
+    const int64_t units = (int64_t)found * p.n_pools * pieces;
+    for (; turn < units; turn += gridDim.x) {
+      // neighbouring blocks take neighbouring pieces of a page
+      const int piece = (int)(turn % pieces), rest = (int)(turn / pieces);
+      const int2 pair = list[rest / p.n_pools];
+      uint8_t* const pool = p.pools[rest % p.n_pools];
+      const int64_t from = (int64_t)piece * kCopyBytes;
+      const int words = (int)min((int64_t)kCopyBytes, p.page_bytes - from) / 16;
+      const uint4* const src = reinterpret_cast<const uint4*>(pool + pair.x * p.page_bytes + from);
+      uint4* const dst = reinterpret_cast<uint4*>(pool + pair.y * p.page_bytes + from);
+      uint4 v[kCopyUnroll];
+#pragma unroll
+      for (int u = 0; u < kCopyUnroll; ++u)
+        if (u * kCopyThreads + tid < words) v[u] = src[u * kCopyThreads + tid];
+#pragma unroll
+      for (int u = 0; u < kCopyUnroll; ++u)
+        if (u * kCopyThreads + tid < words) dst[u * kCopyThreads + tid] = v[u];
+    }
+    turn -= units;
+    __syncthreads();  // the list has been read
+  }
+}
+
+// One cluster of kParts blocks.
+template <typename P>
+static cudaError_t launch_parts(void (*kernel)(P), size_t smem, cudaStream_t stream, const P& p) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kParts;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kParts);
+  cfg.blockDim = dim3(kPartThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
+  static DeviceOnce once;
+  const cudaError_t e = once.run(
+      [] { return cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(ForkShared)); });
+  return e != cudaSuccess ? e : launch_parts(fork_kernel, sizeof(ForkShared), stream, p);
+}
+
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
+  return launch_parts(compact_kernel, 0, stream, p);
+}
+
+int device_sms();
+
+cudaError_t launch_pages_copy(const PagesCopyParams& p, cudaStream_t stream) {
+  // four blocks an SM keep 128 KB of loads in flight there
+  const int64_t pieces = (p.page_bytes + kCopyBytes - 1) / kCopyBytes * p.n_pools * p.n_pages;
+  const int blocks = (int)min(pieces, (int64_t)4 * device_sms());
+  return launch_early(pages_copy_kernel, blocks, kCopyThreads, 0, stream, p);
+}
+
+}  // namespace tpk

@@ -29,6 +29,61 @@ struct TablesParams {
 };
 cudaError_t launch_tables(const TablesParams& p, cudaStream_t stream);
 
+// ------------------------------------------------------------ shared pages
+struct ForkParams {
+  const int32_t* source;
+  const int32_t* len_in;
+  const int32_t* len_keep;  // null: whole histories
+  const int32_t* table_in;
+  int32_t* table_out;
+  const int32_t* shares_in;
+  int32_t* shares_out;
+  int32_t* free_slots;
+  const int32_t* n_free_in;
+  int32_t* n_free_out;
+  int32_t* len_out;
+  int32_t* granted;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* open;    // workspace [kv_slots]: requests whose open page a slot is
+  int32_t* first;   // workspace [kv_slots]: the first of them
+  int32_t* pushed;  // workspace [kv_slots]: slots that nobody holds any more
+  int32_t* counts;  // workspace: of the parts
+  int* status;
+  int n_req, max_pages, kv_slots, free_cap;
+};
+struct CompactParams {
+  const int32_t* n_tokens;
+  const int32_t* table_in;
+  int32_t* table_out;
+  const int32_t* shares_in;
+  int32_t* shares_out;
+  const int32_t* free_in;
+  int32_t* free_out;
+  const int32_t* n_free_in;
+  int32_t* n_free_out;
+  int32_t* new_slot;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* n_copies;
+  int32_t* mark;    // workspace [kv_slots]
+  int32_t* counts;  // workspace: of the parts
+  int* status;
+  int n_req, max_pages, kv_slots, free_cap, max_copies;
+};
+constexpr int kCopyPools = 128;  // pools of one launch
+struct PagesCopyParams {
+  uint8_t* pools[kCopyPools];
+  const int32_t* src;
+  const int32_t* dst;
+  int* status;
+  int64_t page_bytes, kv_slots;
+  int n_pools, n_pages;
+};
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream);
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+cudaError_t launch_pages_copy(const PagesCopyParams& p, cudaStream_t stream);
+
 // ------------------------------------------------------------ rotary store
 struct RopeParams {
   const uint16_t* q;  // null: no queries
