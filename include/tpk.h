@@ -695,6 +695,35 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
                                 int64_t o_stride, float* lse, void* ws, size_t ws_bytes, tpk_stream_t stream);
 
 /*
+ * Attention through a sliding window whose first tokens stay visible, over a request's own
+ * pages: one new token per request, prompts, or parts of prompts behind what is there
+ * already.  Query tokens q_off[b] .. q_off[b + 1] - 1 are request b's last ones: with c of
+ * them, token i of these stands at position x = n_tokens[b] - c + i and sees the tokens
+ * t <= x of its request with t > x - window or t < n_sinks.  window 0: no limit (a causal
+ * prompt); n_sinks 0: a plain window.  A query token in front of its request's first one
+ * (c > n_tokens[b]) sees nothing: o = 0, lse = -inf.
+ *   q          dev [n_q] rows of q_stride elements, [H*G][D]
+ *   q_off      dev int32 [n_req + 1] as for tpk_cross_attn_paged; NULL: one query token per
+ *              request (n_q = n_req)
+ *   n_tokens   dev int32 [n_req], the query tokens counted in (clamped as above)
+ *   o, lse     as for tpk_cross_attn_paged
+ * Only pages with a token that is seen are read: the table's entries of the others may be
+ * anything, so that pages behind a window may be given back.  In the pages that are read,
+ * the keys and values of all tokens below n_tokens[b] must be finite; rows past it may hold
+ * anything.  NaN queries, scores that are too large, errors, strides and capture as for
+ * tpk_cross_attn_paged.
+ * ws: dev workspace of tpk_window_paged_workspace_bytes(shape, n_req, n_q) bytes (no
+ * initialisation), which is enough for every call of the same shape with no more requests
+ * and no more query tokens, whatever its window; calls sharing one must not overlap on the
+ * GPU.  window and n_sinks >= 0.
+ */
+size_t tpk_window_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_q);
+tpk_status tpk_window_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q, int window, int n_sinks, const void* q,
+                                 int64_t q_stride, const int32_t* q_off, const void* k_pool, const void* v_pool,
+                                 const int32_t* page_table, const int32_t* n_tokens, void* o, int64_t o_stride,
+                                 float* lse, void* ws, size_t ws_bytes, tpk_stream_t stream);
+
+/*
  * Measurement hook: while set, every decode-kernel launch of the library (the
  * partial calls and the decode launch of the multi-request call, not its fold) is
  * preceded by a record of `before` and followed by a record of `after` on the

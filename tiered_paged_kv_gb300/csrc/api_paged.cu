@@ -126,7 +126,7 @@ struct CrossPlan {
     return groups * s->kv_heads * splits * tiles * kTileRows;
   }
 };
-CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
+CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q, int max_pages) {
   const int64_t H = s->kv_heads, per_tile = kTileRows / s->group;
   // The split kernel spreads single pages over the device, the tiles read a page once for
   // 128 rows.  It wins:
@@ -146,9 +146,9 @@ CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
   const int64_t rows = (int64_t)n_q * s->group, items = (n_q / per_tile + n_req) * H;
   auto runs = [&](int run_rows) { return (rows / run_rows + n_req) * H; };
   const int64_t wave = split_blocks(s->head_dim) * kTileBlocks;
-  const bool whole = split_whole(true, n_req, n_req * H, s->max_pages);
+  const bool whole = split_whole(true, n_req, n_req * H, max_pages);
   if (rows <= 8 * (int64_t)n_req || (!wide && rows <= 16 * (int64_t)n_req && (whole || items > 4 * kTileBlocks)) ||
-      (whole && s->max_pages <= kWholePages && runs(wide ? 8 : kRowTile) <= wave) || split_few(runs(8), s->max_pages))
+      (whole && max_pages <= kWholePages && runs(wide ? 8 : kRowTile) <= wave) || split_few(runs(8), max_pages))
     return {0, 0, 1};
   // Two tiles share the keys and values and take about 1.5 times one tile's time, so one
   // is better where it needs at most 1.5 times the waves (four requests of 128 tokens,
@@ -161,7 +161,7 @@ CrossPlan cross_plan(const tpk_paged_shape* s, int n_req, int n_q) {
   };
   const int tiles = s->head_dim == 256 || 2 * waves(1) <= 3 * waves(2) ? 1 : 2;  // 256: TMEM holds one
   const int64_t groups = n_q / (tiles * per_tile) + n_req;
-  const int64_t splits = std::min<int64_t>(kTileBlocks / (groups * H), (s->max_pages + 3) / 4);  // two key tiles a part
+  const int64_t splits = std::min<int64_t>(kTileBlocks / (groups * H), (max_pages + 3) / 4);  // two key tiles a part
   return {tiles, groups, std::max<int64_t>(splits, 1)};
 }
 
@@ -172,8 +172,7 @@ size_t tile_ws_bytes(const tpk_paged_shape* s, size_t rows) {
   return kGroupBytes + align256(rows * 8) + rows * s->head_dim * 4;
 }
 
-size_t cross_ws_bytes(const tpk_paged_shape* s, int n_req, int n_q) {
-  const CrossPlan c = cross_plan(s, n_req, n_q);
+size_t cross_ws_bytes(const tpk_paged_shape* s, const CrossPlan& c) {
   if (c.groups == 0) return split_ws_bytes(s);
   if (c.splits == 1) return 256;
   return tile_ws_bytes(s, (size_t)c.rows(s));
@@ -340,6 +339,21 @@ tpk_status rope_append(const tpk_paged_shape* shape, int n_tokens, const void* q
   p.rot = rot_dim;
   const cudaError_t e = (norms ? launch_norm_rope : launch_rope)(p, shape->dtype, interleaved, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? TPK_OK : cuda_fail(e, "rotary store launch");
+}
+
+// What a launch over row tiles needs besides: the queries' map and the workspace.
+tpk_status place_tiles(PagedParams& p, const tpk_paged_shape* s, const CrossPlan& plan, int n_q, const void* q, int64_t q_stride,
+                       void* ws) {
+  const int64_t rows = plan.rows(s);
+  if (rows > 0x7fffffffLL) return fail(TPK_ERR_UNSUPPORTED, "too many query rows");
+  const cuuint64_t dims[3] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->kv_heads * s->group, (cuuint64_t)n_q};
+  const cuuint64_t strides[2] = {(cuuint64_t)s->head_dim * 2, (cuuint64_t)q_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)s->group, (cuuint32_t)(kTileRows / s->group)};
+  const tpk_status st = make_map(&p.qmap, s->dtype, 3, q, dims, strides, box);
+  p.cuts = static_cast<RunCut*>(ws);
+  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kGroupBytes);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kGroupBytes + align256((size_t)rows * 8));
+  return st;
 }
 
 }  // namespace
@@ -571,14 +585,15 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
   if (!q_off) return fail(TPK_ERR_INVALID, "null pointer argument");
   if (!aligned_to(4, q_off, kv_range)) return fail(TPK_ERR_INVALID, "q_off and kv_range must be 4-byte aligned");
   if (n_q == 0) return check_counts(shape, n_req);  // empty rows have no address
+  if (n_req < 1) return check_counts(shape, n_req);
+  const CrossPlan plan = cross_plan(shape, n_req, n_q, shape->max_pages);
   PagedParams p;
   st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
-                       sized(shape, n_req) ? cross_ws_bytes(shape, n_req, n_q) : 0);
+                       sized(shape, n_req) ? cross_ws_bytes(shape, plan) : 0);
   if (st != TPK_OK) return st;
   p.q_off = q_off;
   p.range = kv_range;
   p.n_q = n_q;
-  const CrossPlan plan = cross_plan(shape, n_req, n_q);
   st = make_maps(p, shape, k_pool, v_pool, plan.groups == 0);
   if (st != TPK_OK) return st;
   cudaError_t e;
@@ -586,20 +601,56 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
     place_ws(p, ws);
     e = launch_paged_split(p, shape->head_dim, shape->dtype, reinterpret_cast<cudaStream_t>(stream));
   } else {
-    const int64_t rows = plan.rows(shape);
-    if (rows > 0x7fffffffLL) return fail(TPK_ERR_UNSUPPORTED, "too many query rows");
-    const cuuint64_t dims[3] = {(cuuint64_t)shape->head_dim, (cuuint64_t)shape->kv_heads * shape->group, (cuuint64_t)n_q};
-    const cuuint64_t strides[2] = {(cuuint64_t)shape->head_dim * 2, (cuuint64_t)q_stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)shape->group, (cuuint32_t)(kTileRows / shape->group)};
-    st = make_map(&p.qmap, shape->dtype, 3, q, dims, strides, box);
+    st = place_tiles(p, shape, plan, n_q, q, q_stride, ws);
     if (st != TPK_OK) return st;
-    p.cuts = static_cast<RunCut*>(ws);
-    p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kGroupBytes);
-    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kGroupBytes + align256((size_t)rows * 8));
     e = launch_cross_tiles(p, shape->head_dim, shape->dtype, plan.tiles, (int)plan.groups, (int)plan.splits,
                            reinterpret_cast<cudaStream_t>(stream));
   }
   return e == cudaSuccess ? TPK_OK : cuda_fail(e, "cross attention launch");
+}
+
+size_t tpk_window_paged_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_q) {
+  return tpk_cross_paged_workspace_bytes(shape, n_req, n_q);
+}
+
+tpk_status tpk_window_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q, int window, int n_sinks, const void* q,
+                                 int64_t q_stride, const int32_t* q_off, const void* k_pool, const void* v_pool,
+                                 const int32_t* page_table, const int32_t* n_tokens, void* o, int64_t o_stride,
+                                 float* lse, void* ws, size_t ws_bytes, tpk_stream_t stream) {
+  tpk_status st = check_paged(shape);
+  if (st != TPK_OK) return st;
+  if (n_q < 0 || (int64_t)n_q * shape->kv_heads * shape->group > 0x7fffffffLL)
+    return fail(TPK_ERR_INVALID, "n_q %d (at most 2^31 query rows)", n_q);
+  if (window < 0) return fail(TPK_ERR_INVALID, "window %d < 0", window);
+  if (n_sinks < 0) return fail(TPK_ERR_INVALID, "n_sinks %d < 0", n_sinks);
+  if (!q_off && n_q != n_req) return fail(TPK_ERR_INVALID, "%d query tokens of %d requests without q_off", n_q, n_req);
+  if (!aligned_to(4, q_off)) return fail(TPK_ERR_INVALID, "q_off must be 4-byte aligned");
+  if (n_q == 0 || n_req < 1 || n_req > kMaxPagedReq) return check_counts(shape, n_req);  // empty rows have no address
+  // pages that the queries of a request see, at most: requests count as having equally many
+  const int64_t seen = window == 0 ? shape->max_pages
+                                   : ((int64_t)window + n_q / n_req + 126) / 64 + ((int64_t)n_sinks + 63) / 64;
+  const int span = (int)std::min<int64_t>(shape->max_pages, seen);
+  const CrossPlan plan = q_off ? cross_plan(shape, n_req, n_q, span) : CrossPlan{0, 0, 1};
+  PagedParams p;
+  st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
+                       cross_ws_bytes(shape, plan));
+  if (st == TPK_OK) st = make_maps(p, shape, k_pool, v_pool, plan.groups == 0);
+  if (st != TPK_OK) return st;
+  p.q_off = q_off;
+  p.n_q = n_q;
+  p.window = window == 0 ? 0x7fffffff : window;
+  p.sinks = n_sinks;
+  cudaError_t e;
+  if (plan.groups == 0) {
+    place_ws(p, ws);
+    e = launch_window_split(p, span, shape->head_dim, shape->dtype, reinterpret_cast<cudaStream_t>(stream));
+  } else {
+    st = place_tiles(p, shape, plan, n_q, q, q_stride, ws);
+    if (st != TPK_OK) return st;
+    e = launch_window_tiles(p, shape->head_dim, shape->dtype, plan.tiles, (int)plan.groups, (int)plan.splits,
+                            reinterpret_cast<cudaStream_t>(stream));
+  }
+  return e == cudaSuccess ? TPK_OK : cuda_fail(e, "window attention launch");
 }
 
 }  // extern "C"

@@ -243,6 +243,29 @@ static PyObject* cross_attn_paged(PyObject* self, PyObject* const* args, Py_ssiz
   return done(&r, st);
 }
 
+static PyObject* window_attn_paged(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  (void)self;
+  reader r = {args, n, 0, 0};
+  Py_buffer sb;
+  const tpk_paged_shape* shape = shape_of(&r, &sb);
+  const int n_req = narrow(&r), n_q = narrow(&r), window = narrow(&r), n_sinks = narrow(&r);
+  const void* q = pointer(&r);
+  const int64_t q_stride = wide(&r);
+  const int32_t* q_off = pointer(&r);
+  const void *k_pool = pointer(&r), *v_pool = pointer(&r);
+  const int32_t *table = pointer(&r), *n_tokens = pointer(&r);
+  void* o = pointer(&r);
+  const int64_t o_stride = wide(&r);
+  float* lse = pointer(&r);
+  void* ws = pointer(&r);
+  const int64_t ws_bytes = wide(&r);
+  const tpk_stream_t s = stream(&r);
+  RUN(r, tpk_window_attn_paged(shape, n_req, n_q, window, n_sinks, q, q_stride, q_off, k_pool, v_pool, table, n_tokens, o,
+                               o_stride, lse, ws, ws_bytes < 0 ? 0 : (size_t)ws_bytes, s));
+  if (sb.obj) PyBuffer_Release(&sb);
+  return done(&r, st);
+}
+
 static PyObject* kv_pages_fork(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   (void)self;
   reader r = {args, n, 0, 0};
@@ -346,7 +369,7 @@ static PyObject* set_shape_type(PyObject* self, PyObject* type) {
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(kv_tables_update), METHOD(kv_rope_append), METHOD(kv_norm_rope_append), METHOD(decode_attn_paged),
                                 METHOD(cross_attn_paged), METHOD(kv_pages_fork), METHOD(kv_pages_compact),
-                                METHOD(kv_pages_copy), {"set_shape_type", set_shape_type, METH_O, NULL},
+                                METHOD(kv_pages_copy), METHOD(window_attn_paged), {"set_shape_type", set_shape_type, METH_O, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tpk_call", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -1,0 +1,11 @@
+// The attention of many query rows through windows (cross_tile.cuh).
+#include "cross_tile.cuh"
+
+namespace tpk {
+
+cudaError_t launch_window_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
+                               cudaStream_t stream) {
+  return launch_tiles_of<kWindowed>(p, D, dtype, tiles, groups, splits, stream);
+}
+
+}  // namespace tpk

@@ -138,6 +138,7 @@ struct PagedParams {
   uint64_t wait_ns;
   float qscale;  // sm_scale * log2(e)
   int n_req, n_q, max_pages, H, G, o_f32;
+  int window, sinks;  // windows: tokens that a query sees up to its own, and first ones that it always sees
   int run_rows;  // query rows of a run, 8 or 16 (set at launch)
   int whole;     // a block per run (set at launch)
   int stall_unit;  // test hook: this block's first page, or key tile, is neither copied nor signalled (-1: none)
@@ -147,6 +148,8 @@ constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row
 constexpr int kPagedMaxBlocks = 512;  // blocks of a split launch; each owns two partial slots
 constexpr int kRowTile = 16;          // query rows of a split run, at most
 cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream);
+// The same through windows; span_pages: pages that a request's queries see, at most (a hint).
+cudaError_t launch_window_split(PagedParams& p, int span_pages, int D, int dtype, cudaStream_t stream);
 
 constexpr int split_blocks(int D) { return D == 256 ? 1 : D == 128 ? 2 : 3; }  // resident per SM
 constexpr int kScanned = 128;  // requests that one warp numbers: lane i has 4 i .. 4 i + 3
@@ -176,6 +179,8 @@ inline bool read_twice(int64_t runs, int max_pages, int D) {
 constexpr int kTileRows = 128;    // query rows of a tile; a block takes `tiles` (1 or 2) of them
 cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
                                cudaStream_t stream);
+cudaError_t launch_window_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
+                                cudaStream_t stream);
 
 // ------------------------------------------------------------------- types
 // kWeightBits: weights, at most 1, enter the product with the values times 2^kWeightBits.  float16
@@ -298,6 +303,10 @@ __device__ __forceinline__ void request_span(const PagedParams& p, int b, int& l
   }
   if (bad) atomicOr(p.status, kStatusBadSlot);
 }
+
+// What the queries of a launch see of their request: all of it (or [begin, n)), or its last tokens
+// and its first ones.
+enum : int { kWholeHistory = 0, kWindowed = 1 };
 
 // Request b's query rows: tokens [first, first + count) of q.
 __device__ __forceinline__ void request_rows(const PagedParams& p, int b, int& first, int& count) {
