@@ -695,6 +695,36 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
                                 int64_t o_stride, float* lse, void* ws, size_t ws_bytes, tpk_stream_t stream);
 
 /*
+ * tpk_decode_attn_paged for requests that share prefixes.  Requests grp_off[g] ..
+ * grp_off[g + 1] - 1 form group g: their first n_shared[g] tokens are the same (pages that
+ * their table rows name together, as tpk_kv_pages_fork leaves them, and the rows of a page in
+ * which the prefix ends, of which each has a copy).  The prefix is read once for the whole
+ * group, from the row of its first request that has the most of it; what a request has
+ * beyond it, from its own row.  Results are those of tpk_decode_attn_paged without
+ * tok_begin, to rounding (the prefix's weights are rounded once to the pools' type before
+ * the product with the values), and bit-reproducible.
+ *   n_tokens   dev int32 [n_req], the prefix counted in; a request with fewer tokens than
+ *              n_shared[g] sees those it has, one with none gets o = 0, lse = -inf
+ *   grp_off    dev int32 [n_grp + 1], not decreasing (values are clamped into [0, n_req]);
+ *              requests in no group share nothing
+ *   n_shared   dev int32 [n_grp] (clamped as n_tokens)
+ *   q, o, lse  as for tpk_decode_attn_paged
+ * Pages are read as far as some request's n_tokens reach; keys and values of all tokens
+ * below them must be finite, rows past them may hold anything.  NaN queries, errors, strides
+ * and capture as for tpk_decode_attn_paged, scores that are too large as for
+ * tpk_cross_attn_paged.
+ * ws: dev workspace of tpk_decode_shared_workspace_bytes(shape, n_req, n_grp) bytes (no
+ * initialisation; enough for fewer requests, and any number of groups, too); calls sharing
+ * one must not overlap on the GPU.  n_req in [1, 4096], n_grp in [1, 4096].
+ */
+size_t tpk_decode_shared_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_grp);
+tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n_grp, const void* q, int64_t q_stride,
+                                  const void* k_pool, const void* v_pool, const int32_t* page_table,
+                                  const int32_t* n_tokens, const int32_t* grp_off, const int32_t* n_shared, void* o,
+                                  int64_t o_stride, int o_f32, float* lse, void* ws, size_t ws_bytes,
+                                  tpk_stream_t stream);
+
+/*
  * Attention through a sliding window whose first tokens stay visible, over a request's own
  * pages: one new token per request, prompts, or parts of prompts behind what is there
  * already.  Query tokens q_off[b] .. q_off[b + 1] - 1 are request b's last ones: with c of

@@ -31,6 +31,7 @@ __all__ = [
     "PagedShape", "BF16", "F16", "kv_tables_update", "kv_rope_append", "kv_norm_rope_append", "kv_pages_workspace_bytes",
     "kv_pages_fork", "kv_pages_compact", "kv_pages_copy", "decode_paged_workspace_bytes",
     "decode_attn_paged", "cross_paged_workspace_bytes", "cross_attn_paged", "window_paged_workspace_bytes", "window_attn_paged",
+    "decode_shared_workspace_bytes", "decode_attn_shared",
 ]
 
 RECORD_BYTES = 35072
@@ -159,7 +160,10 @@ def lib():
         L.tpk_window_paged_workspace_bytes.argtypes = [gp, i32, i32]
         L.tpk_window_paged_workspace_bytes.restype = sz
         L.tpk_window_attn_paged.argtypes = [gp, i32, i32, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp, vp, sz, vp]
-        for name in ("tpk_window_attn_paged", "tpk_kv_tables_update", "tpk_kv_rope_append", "tpk_kv_norm_rope_append", "tpk_decode_attn_paged",
+        L.tpk_decode_shared_workspace_bytes.argtypes = [gp, i32, i32]
+        L.tpk_decode_shared_workspace_bytes.restype = sz
+        L.tpk_decode_attn_shared.argtypes = [gp, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, i32, vp, vp, sz, vp]
+        for name in ("tpk_window_attn_paged", "tpk_decode_attn_shared", "tpk_kv_tables_update", "tpk_kv_rope_append", "tpk_kv_norm_rope_append", "tpk_decode_attn_paged",
                      "tpk_cross_attn_paged", "tpk_kv_pages_fork", "tpk_kv_pages_compact", "tpk_kv_pages_copy"):
             getattr(L, name).restype = i32
         for name in ("tpk_kv_quantize_pages", "tpk_kv_quantize_pages_given_scales", "tpk_kv_pack13_pages",
@@ -428,6 +432,20 @@ def window_attn_paged(shape, n_req, n_q, window, n_sinks, q, q_stride, q_off, k_
     visible (see tpk_window_attn_paged); q_off None: one token per request."""
     st = (_call or _calls()).window_attn_paged(shape, n_req, n_q, window, n_sinks, q, q_stride, q_off, k_pool, v_pool,
                                                page_table, n_tokens, o, o_stride, lse, ws, ws_bytes, stream)
+    if st:
+        _check(st)
+
+
+def decode_shared_workspace_bytes(shape, n_req, n_grp):
+    return int(lib().tpk_decode_shared_workspace_bytes(ctypes.byref(shape), n_req, n_grp))
+
+
+def decode_attn_shared(shape, n_req, n_grp, q, q_stride, k_pool, v_pool, page_table, n_tokens, grp_off, n_shared, o, o_stride,
+                       o_f32, lse, ws, ws_bytes, stream=None):
+    """decode_attn_paged for groups of requests that share a prefix, read once for each group
+    (see tpk_decode_attn_shared)."""
+    st = (_call or _calls()).decode_attn_shared(shape, n_req, n_grp, q, q_stride, k_pool, v_pool, page_table, n_tokens, grp_off,
+                                                n_shared, o, o_stride, o_f32, lse, ws, ws_bytes, stream)
     if st:
         _check(st)
 

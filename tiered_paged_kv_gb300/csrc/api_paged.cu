@@ -341,19 +341,65 @@ tpk_status rope_append(const tpk_paged_shape* shape, int n_tokens, const void* q
   return e == cudaSuccess ? TPK_OK : cuda_fail(e, "rotary store launch");
 }
 
+// The queries of row tiles.
+tpk_status make_query_map(PagedParams& p, const tpk_paged_shape* s, int n_q, const void* q, int64_t q_stride) {
+  const cuuint64_t dims[3] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->kv_heads * s->group, (cuuint64_t)n_q};
+  const cuuint64_t strides[2] = {(cuuint64_t)s->head_dim * 2, (cuuint64_t)q_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)s->group, (cuuint32_t)(kTileRows / s->group)};
+  return make_map(&p.qmap, s->dtype, 3, q, dims, strides, box);
+}
+
 // What a launch over row tiles needs besides: the queries' map and the workspace.
 tpk_status place_tiles(PagedParams& p, const tpk_paged_shape* s, const CrossPlan& plan, int n_q, const void* q, int64_t q_stride,
                        void* ws) {
   const int64_t rows = plan.rows(s);
   if (rows > 0x7fffffffLL) return fail(TPK_ERR_UNSUPPORTED, "too many query rows");
-  const cuuint64_t dims[3] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->kv_heads * s->group, (cuuint64_t)n_q};
-  const cuuint64_t strides[2] = {(cuuint64_t)s->head_dim * 2, (cuuint64_t)q_stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)s->group, (cuuint32_t)(kTileRows / s->group)};
-  const tpk_status st = make_map(&p.qmap, s->dtype, 3, q, dims, strides, box);
+  const tpk_status st = make_query_map(p, s, n_q, q, q_stride);
   p.cuts = static_cast<RunCut*>(ws);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kGroupBytes);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kGroupBytes + align256((size_t)rows * 8));
   return st;
+}
+
+// How the prefixes of n_grp groups of n_req requests are cut: row tiles of each group, one or two at
+// a time, and `splits` parts of the prefix.  Groups count as equally large; `groups` bounds the tile
+// groups of one KV head whatever their sizes.
+struct SharedPlan {
+  int tiles;
+  int64_t groups, splits;
+};
+constexpr int kSharedWaves = 3, kSharedSplits = 64;
+SharedPlan shared_plan(const tpk_paged_shape* s, int n_req, int n_grp) {
+  const int64_t H = s->kv_heads, per_tile = kTileRows / s->group, each = ((int64_t)n_req + n_grp - 1) / n_grp;
+  const int tiles = s->head_dim < 256 && each > per_tile ? 2 : 1;
+  const int64_t per = tiles * per_tile, items = n_grp * ((each + per - 1) / per) * H;
+  // One group's parts are equally long: one wave of them.  Several groups' are not: some waves.
+  const int64_t parts = n_grp == 1 ? kTileBlocks / items : (kSharedWaves * kTileBlocks + items - 1) / items;
+  const int64_t splits = std::min({parts, ((int64_t)s->max_pages + 3) / 4, (int64_t)kSharedSplits});
+  return {tiles, n_req / per + n_grp, std::max<int64_t>(splits, 1)};
+}
+
+// Rows of the prefixes' parts, bounded for all calls with no more requests: with more than one part
+// there are at most kSharedWaves * kTileBlocks + items of them, of at most two tiles' rows each.
+int64_t shared_rows(const tpk_paged_shape* s, int n_req) {
+  const int64_t rows = (int64_t)n_req * s->kv_heads * s->group;
+  return std::min(rows * kSharedSplits, 2 * rows + (int64_t)kSharedWaves * kTileBlocks * 2 * kTileRows);
+}
+
+struct SharedWs {
+  size_t part_ml, part_o, own_o, own_lse, own_begin, split, bytes;
+};
+SharedWs shared_ws(const tpk_paged_shape* s, int n_req) {
+  const size_t rows = (size_t)n_req * s->kv_heads * s->group, parts = (size_t)shared_rows(s, n_req);
+  SharedWs w;
+  w.part_ml = 0;
+  w.part_o = w.part_ml + align256(parts * 8);
+  w.own_o = w.part_o + align256(parts * s->head_dim * 4);
+  w.own_lse = w.own_o + align256(rows * s->head_dim * 4);
+  w.own_begin = w.own_lse + align256(rows * 4);
+  w.split = w.own_begin + align256((size_t)n_req * 4);
+  w.bytes = w.split + split_ws_bytes(s);
+  return w;
 }
 
 }  // namespace
@@ -651,6 +697,74 @@ tpk_status tpk_window_attn_paged(const tpk_paged_shape* shape, int n_req, int n_
                             reinterpret_cast<cudaStream_t>(stream));
   }
   return e == cudaSuccess ? TPK_OK : cuda_fail(e, "window attention launch");
+}
+
+size_t tpk_decode_shared_workspace_bytes(const tpk_paged_shape* shape, int n_req, int n_grp) {
+  return sized(shape, n_req) && n_grp >= 1 && n_grp <= kMaxPagedReq && shape->kv_heads > 0 && shape->kv_heads <= kMaxHeads &&
+                 shape->group > 0 && shape->group <= kMaxGroup
+             ? shared_ws(shape, n_req).bytes
+             : 0;
+}
+
+tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n_grp, const void* q, int64_t q_stride,
+                                  const void* k_pool, const void* v_pool, const int32_t* page_table,
+                                  const int32_t* n_tokens, const int32_t* grp_off, const int32_t* n_shared, void* o,
+                                  int64_t o_stride, int o_f32, float* lse, void* ws, size_t ws_bytes,
+                                  tpk_stream_t stream) {
+  tpk_status st = check_paged(shape);
+  if (st != TPK_OK) return st;
+  if (o_f32 != 0 && o_f32 != 1) return fail(TPK_ERR_INVALID, "o_f32 %d (0 or 1)", o_f32);
+  if (n_grp < 1 || n_grp > kMaxPagedReq) return fail(TPK_ERR_INVALID, "n_grp %d out of [1, %d]", n_grp, kMaxPagedReq);
+  if (!grp_off || !n_shared) return fail(TPK_ERR_INVALID, "null pointer argument");
+  if (!aligned_to(4, grp_off, n_shared)) return fail(TPK_ERR_INVALID, "grp_off and n_shared must be 4-byte aligned");
+  PagedParams p;
+  st = begin_attention(p, shape, n_req, q, q_stride, k_pool, v_pool, page_table, n_tokens, o, o_stride, lse, ws, ws_bytes,
+                       tpk_decode_shared_workspace_bytes(shape, n_req, n_grp));
+  if (st != TPK_OK) return st;
+  const SharedPlan plan = shared_plan(shape, n_req, n_grp);
+  const SharedWs w = shared_ws(shape, n_req);
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  auto at = [&](size_t offset) { return static_cast<uint8_t*>(ws) + offset; };
+  p.n_q = n_req;
+  p.own_begin = reinterpret_cast<int32_t*>(at(w.own_begin));
+  // the prefixes: the groups are the requests
+  PagedParams g = p;
+  st = make_maps(g, shape, k_pool, v_pool, false);
+  if (st == TPK_OK) st = make_query_map(g, shape, n_req, q, q_stride);
+  // what the requests do not share
+  if (st == TPK_OK) st = make_maps(p, shape, k_pool, v_pool, true);
+  if (st != TPK_OK) return st;
+  g.n_req = n_grp;
+  g.q_off = grp_off;
+  g.lens = n_shared;
+  g.own_lens = n_tokens;
+  g.part_ml = reinterpret_cast<float*>(at(w.part_ml));
+  g.part_o = reinterpret_cast<float*>(at(w.part_o));
+  cudaError_t e = launch_shared_tiles(g, shape->head_dim, shape->dtype, plan.tiles, (int)plan.groups, (int)plan.splits, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
+  place_ws(p, at(w.split));
+  p.begin = p.own_begin;
+  p.o = at(w.own_o);
+  p.o_f32 = 1;
+  p.o_stride = (int64_t)shape->kv_heads * shape->group * shape->head_dim;
+  p.lse = reinterpret_cast<float*>(at(w.own_lse));
+  e = launch_paged_split(p, shape->head_dim, shape->dtype, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+  SharedJoinParams j;
+  j.part_o = g.part_o;
+  j.part_ml = g.part_ml;
+  j.own_o = static_cast<const float*>(p.o);
+  j.own_lse = p.lse;
+  j.own_begin = p.own_begin;
+  j.o = o;
+  j.lse = lse;
+  j.o_stride = o_stride;
+  j.n_q = n_req;
+  j.HQ = shape->kv_heads * shape->group;
+  j.splits = (int)plan.splits;
+  j.o_f32 = o_f32;
+  e = launch_shared_join(j, shape->head_dim, shape->dtype, cs);
+  return e == cudaSuccess ? TPK_OK : cuda_fail(e, "shared join launch");
 }
 
 }  // extern "C"

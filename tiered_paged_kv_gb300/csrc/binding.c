@@ -266,6 +266,29 @@ static PyObject* window_attn_paged(PyObject* self, PyObject* const* args, Py_ssi
   return done(&r, st);
 }
 
+static PyObject* decode_attn_shared(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  (void)self;
+  reader r = {args, n, 0, 0};
+  Py_buffer sb;
+  const tpk_paged_shape* shape = shape_of(&r, &sb);
+  const int n_req = narrow(&r), n_grp = narrow(&r);
+  const void* q = pointer(&r);
+  const int64_t q_stride = wide(&r);
+  const void *k_pool = pointer(&r), *v_pool = pointer(&r);
+  const int32_t *table = pointer(&r), *n_tokens = pointer(&r), *grp_off = pointer(&r), *n_shared = pointer(&r);
+  void* o = pointer(&r);
+  const int64_t o_stride = wide(&r);
+  const int o_f32 = narrow(&r);
+  float* lse = pointer(&r);
+  void* ws = pointer(&r);
+  const int64_t ws_bytes = wide(&r);
+  const tpk_stream_t s = stream(&r);
+  RUN(r, tpk_decode_attn_shared(shape, n_req, n_grp, q, q_stride, k_pool, v_pool, table, n_tokens, grp_off, n_shared, o,
+                                o_stride, o_f32, lse, ws, ws_bytes < 0 ? 0 : (size_t)ws_bytes, s));
+  if (sb.obj) PyBuffer_Release(&sb);
+  return done(&r, st);
+}
+
 static PyObject* kv_pages_fork(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   (void)self;
   reader r = {args, n, 0, 0};
@@ -369,7 +392,8 @@ static PyObject* set_shape_type(PyObject* self, PyObject* type) {
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(kv_tables_update), METHOD(kv_rope_append), METHOD(kv_norm_rope_append), METHOD(decode_attn_paged),
                                 METHOD(cross_attn_paged), METHOD(kv_pages_fork), METHOD(kv_pages_compact),
-                                METHOD(kv_pages_copy), METHOD(window_attn_paged), {"set_shape_type", set_shape_type, METH_O, NULL},
+                                METHOD(kv_pages_copy), METHOD(window_attn_paged),
+                                METHOD(decode_attn_shared), {"set_shape_type", set_shape_type, METH_O, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tpk_call", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -82,24 +82,52 @@ struct TileCfg {
   static constexpr int kThreads = (kQuery + 1 + kTwoLoaders) * 32;
 };
 
+// Windowed: the position of the first query token; key tiles [0, sinks) are those of the first
+// pages, from sink_page on, up to sink_end; 16-token groups of the last of them.
+template <int kSpan>
+struct SinkTiles {};
+template <>
+struct SinkTiles<kWindowed> {
+  int pos, sinks, sink_page, sink_end, sink_last;
+};
+
 // One tile group of one (request, KV head), or one part of its keys.
 template <int kSpan>
-struct Item {
+struct Item : SinkTiles<kSpan> {
   int id;       // its block number; -1: no more
   int first;    // its first query token
   int tokens;   // and how many of them it has: `per_tile` fill a row tile
   int h, len, b;
   int page0, page_end, nk;  // key tiles [0, nk) begin at page page0
   int last;     // 16-token groups of the last key tile that hold any token
-  // windowed: the position of the first query token; key tiles [0, sinks) are those of the first
-  // pages, from sink_page on, up to sink_end; 16-token groups of the last of them
-  int pos, sinks, sink_page, sink_end, sink_last;
 
   // first page of key tile j, and the page where its stretch of pages ends
   __device__ __forceinline__ int page(int j) const {
-    return kSpan == kWindowed && j < sinks ? sink_page + 2 * j : page0 + 2 * (kSpan == kWindowed ? j - sinks : j);
+    if constexpr (kSpan == kWindowed)
+      if (j < this->sinks) return this->sink_page + 2 * j; else return page0 + 2 * (j - this->sinks);
+    else
+      return page0 + 2 * j;
   }
-  __device__ __forceinline__ int end(int j) const { return kSpan == kWindowed && j < sinks ? sink_end : page_end; }
+  __device__ __forceinline__ int end(int j) const {
+    if constexpr (kSpan == kWindowed)
+      if (j < this->sinks) return this->sink_end;
+    return page_end;
+  }
+  // the page of lane i of a warp that holds those of key tiles j, j + 1, ...; false past the last
+  __device__ __forceinline__ bool page_of_lane(int j, int i, int& pg) const {
+    if constexpr (kSpan == kWindowed) {
+      pg = page(j + (i >> 1)) + (i & 1);
+      return pg < end(j + (i >> 1));
+    }
+    pg = page0 + 2 * j + i;
+    return pg < page_end;
+  }
+  // 16-token groups of key tile j that hold any token
+  __device__ __forceinline__ int groups(int j) const {
+    if constexpr (kSpan == kWindowed)
+      if (j + 1 == this->sinks) return this->sink_last;
+    return j + 1 < nk ? 8 : last;
+  }
 };
 
 template <int kSpan>
@@ -264,6 +292,7 @@ struct Requests {
   int base = -64, begin = 0, end = 0;  // groups [begin, end) are those of the 64 held
   int first[2], count[2], len[2], groups[2], before[2];
 
+  template <int kSpan>
   __device__ __forceinline__ void load(const PagedParams& p, int lane) {
     int sum = 0;
 #pragma unroll
@@ -274,6 +303,7 @@ struct Requests {
       if (b < p.n_req) {
         request_rows(p, b, first[x], count[x]);
         request_span(p, b, lo, len[x]);
+        if (kSpan == kSharedPrefix && count[x] < 2) len[x] = 0;  // nobody to share with
       }
       groups[x] = (count[x] + per_group - 1) / per_group;
       int inc = groups[x];
@@ -306,14 +336,14 @@ struct Requests {
   __device__ __forceinline__ bool find(const PagedParams& p, int lane, bool sorted, int want, Item<kSpan>& it) {
     if (base < 0 || want < begin) {
       base = begin = 0;
-      load(p, lane);
+      load<kSpan>(p, lane);
       if (sorted) sort(p, lane);
     }
     while (want >= end) {
       if (base + 64 >= p.n_req) return false;
       base += 64;
       begin = end;
-      load(p, lane);
+      load<kSpan>(p, lane);
     }
     const uint32_t m0 = __ballot_sync(0xffffffffu, want >= before[0] && want < before[0] + groups[0]);
     const uint32_t m1 = __ballot_sync(0xffffffffu, want >= before[1] && want < before[1] + groups[1]);
@@ -325,7 +355,18 @@ struct Requests {
     it.first = __shfl_sync(0xffffffffu, second ? first[1] : first[0], src) + t;
     it.tokens = min(all - t, per_group);
     it.len = __shfl_sync(0xffffffffu, second ? len[1] : len[0], src);
-    if (kSpan == kWindowed) it.pos = it.len - all + t;
+    if constexpr (kSpan == kWindowed) it.pos = it.len - all + t;
+    if constexpr (kSpan == kSharedPrefix) {
+      // the prefix is read from the row of the first request that has the most of it
+      const int lead = it.first - t;
+      int most = 0, row = 0x7fffffff;
+      for (int i = lead + lane; i < lead + all; i += 32) most = max(most, min(p.own_lens[i], it.len));
+      most = __reduce_max_sync(0xffffffffu, most);
+      for (int i = lead + lane; i < lead + all; i += 32)
+        if (min(p.own_lens[i], it.len) == most) row = min(row, i);
+      it.len = most;
+      it.b = __reduce_min_sync(0xffffffffu, row);
+    }
     return true;
   }
 };
@@ -403,8 +444,8 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
     };
     if (j >> 4 > w.window) {
       w.window = j >> 4;
-      const int t = 16 * w.window + (lane >> 1), pg = it.page(t) + (lane & 1);
-      w.entry = pg < it.end(t) ? p.table[(int64_t)it.b * p.max_pages + pg] : -1;
+      int pg;
+      w.entry = it.page_of_lane(16 * w.window, lane, pg) ? p.table[(int64_t)it.b * p.max_pages + pg] : -1;
     }
     const int slot0 = __shfl_sync(0xffffffffu, w.entry, 2 * j & 31);
     const int slot1 = __shfl_sync(0xffffffffu, w.entry, (2 * j & 31) + 1);
@@ -546,12 +587,9 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       for (int k = 0; ok; ++k) {
         wait(&S.item_full[k & 1], k >> 1);
         if (!ok) break;
-        const int id = S.item[k & 1].id, nk = S.item[k & 1].nk, tail = S.item[k & 1].last;
-        const int sinks = kSpan == kWindowed ? S.item[k & 1].sinks : 0;
-        const int sink_tail = kSpan == kWindowed ? S.item[k & 1].sink_last : 0;
-        // 16-token groups of key tile j that hold any token
-        auto groups = [&](int j) { return kSpan == kWindowed && j + 1 == sinks ? sink_tail : j + 1 < nk ? 8 : tail; };
-        const bool two = C::kTiles == 2 && S.item[k & 1].tokens > per_tile;
+        const Item it = S.item[k & 1];
+        const int id = it.id, nk = it.nk;
+        const bool two = C::kTiles == 2 && it.tokens > per_tile;
         mbar_arrive(&S.item_empty[k & 1]);
         if (id < 0) break;
         if (nk == 0) continue;
@@ -568,11 +606,11 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
             const bool more = j + 1 < nk;
             if (more) ka = take();
             if (!ok) break;
-            pv(0, 0, va, j > 0, !two, groups(j));
+            pv(0, 0, va, j > 0, !two, it.groups(j));
             if (!ok) break;
             if (more) qk(0, 0, ka, !two); else tc_commit(o_full);
             if (two) {
-              pv(1, 1, va, j > 0, true, groups(j));
+              pv(1, 1, va, j > 0, true, it.groups(j));
               if (!ok) break;
               if (more) qk(1, 1, ka, true); else tc_commit(o_full + 8);
             }
@@ -592,7 +630,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
             const bool more = j + 2 < nk;
             if (more) ka = take();
             if (!ok) break;
-            pv(0, b0 ^ (j & 1), va, j > 0, true, groups(j));
+            pv(0, b0 ^ (j & 1), va, j > 0, true, it.groups(j));
             if (!ok) break;
             tc_commit(pv_done);
             if (j + 1 == nk) tc_commit(o_full);
@@ -638,8 +676,15 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       it.h = id / splits % p.H;
       const bool found = requests.find(p, lane, sorted, id / splits / p.H, it);
       // the join's record, by the block of the group's first part
-      if (splits > 1 && part == 0 && lane == 0) p.cuts[id / splits] = {it.first, found ? it.tokens : 0, it.h, 0, splits};
+      if (kSpan != kSharedPrefix && splits > 1 && part == 0 && lane == 0) p.cuts[id / splits] = {it.first, found ? it.tokens : 0, it.h, 0, splits};
+      if (kSpan == kSharedPrefix && id == 0) {  // requests in no group share nothing
+        const int end = min(max(p.q_off[p.n_req], 0), p.n_q);
+        for (int b = lane; b < p.n_q; b += 32)
+          if (b < p.q_off[0] || b >= end) p.own_begin[b] = 0;
+      }
       if (found) {
+        if (kSpan == kSharedPrefix && part == 0 && it.h == 0)
+          for (int t = lane; t < it.tokens; t += 32) p.own_begin[it.first + t] = it.len;
         int clo = 0, chi = it.len;
         if (p.range) {  // what any of its rows sees
           clo = 0x7fffffff;
@@ -654,14 +699,14 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
           clo = __reduce_min_sync(0xffffffffu, clo);
           chi = __reduce_max_sync(0xffffffffu, chi);
         }
-        if (kSpan == kWindowed) {
+        int sinks = 0;  // key tiles of the first tokens
+        if constexpr (kSpan == kWindowed) {
           chi = max(min(it.len, it.pos + it.tokens), 0);
           clo = min(max(max(it.pos + 1, 0) - p.window, 0), chi);
         }
         it.page0 = chi > clo ? clo >> 6 : 0;
         it.page_end = (chi + 63) >> 6;
-        int sinks = 0;  // key tiles of the first tokens
-        if (kSpan == kWindowed) {
+        if constexpr (kSpan == kWindowed) {
           const int tokens = min(p.sinks, clo);
           it.sink_end = (tokens + 63) >> 6;
           if (it.sink_end >= it.page0) it.page0 = it.sink_end = 0;  // no page lies between
@@ -671,14 +716,12 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         const int nk = chi > clo ? sinks + ((it.page_end - it.page0 + 1) >> 1) : 0;
         const int k0 = (int)((unsigned)nk * (unsigned)part / (unsigned)splits);  // splits <= kTileBlocks, nk < 2^24
         const int k1 = (int)((unsigned)nk * (unsigned)(part + 1) / (unsigned)splits);
+        it.page0 += 2 * max(k0 - sinks, 0);
         it.nk = k1 - k0;
-        if (kSpan == kWindowed) {
+        if constexpr (kSpan == kWindowed) {
           it.sink_page = 2 * k0;
           it.sinks = max(min(k1, sinks) - k0, 0);
           if (k1 < sinks) it.sink_last = 8;  // the last of them is in a later part
-          it.page0 += 2 * max(k0 - sinks, 0);
-        } else {
-          it.page0 += 2 * k0;
         }
         it.last = min(8, (min(it.len, it.page_end * kPageTokens) - it.page(it.nk - 1) * kPageTokens + 15) >> 4);
         if (k >= 2) wait(&S.item_empty[k & 1], (k >> 1) - 1);
@@ -794,7 +837,8 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
           see_lo = max(0, p.range[2 * (int64_t)token]);
           see_hi = max(0, min(see_hi, p.range[2 * (int64_t)token + 1]));
         }
-        if (kSpan == kWindowed) {
+        if (kSpan == kSharedPrefix) see_hi = max(0, min(see_hi, p.own_lens[token]));
+        if constexpr (kSpan == kWindowed) {
           see_hi = max(0, min(see_hi, it.pos + tile * per_tile + t_row + 1));
           see_lo = max(0, see_hi - p.window);
         }
@@ -807,8 +851,8 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       for (int n = 0; n < nk; ++n, ++step) {
         const int buf = C::kTiles == 2 ? tile : step & 1, parity = (C::kTiles == 2 ? step : step >> 1) & 1;
         if ((n & 15) == 0) {
-          const int t = n + (lane >> 1), pg = it.page(t) + (lane & 1);
-          const int32_t e = pg < it.end(t) ? table[pg] : -1;
+          int pg;
+          const int32_t e = it.page_of_lane(n, lane, pg) ? table[pg] : -1;
           pages_ok = __ballot_sync(0xffffffffu, e >= 0 && e < p.kv_slots);
         }
         const int k0 = (it.page(n) + half) * kPageTokens;
@@ -910,12 +954,15 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[tile], items++ & 1, p.status, p.wait_ns)) != 0;
         tc_fence_after();
       }
-      const int64_t at = (int64_t)it.id * C::kRows + hrow;  // this part's row in the workspace
-      const float inv = splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      // this part's row in the workspace
+      const int64_t at = kSpan == kSharedPrefix ? ((int64_t)(it.id % splits) * p.n_q + token) * HQ + head
+                                                : (int64_t)it.id * C::kRows + hrow;
+      const bool partial = kSpan == kSharedPrefix || splits > 1;
+      const float inv = partial ? 1.f : l == 0.f ? 0.f : 1.f / l;
       // the fold does not use an empty part (by its sum: one of NaN scores has no maximum either)
-      const bool write = live && ok && !(splits > 1 && l == 0.f);
+      const bool write = live && ok && !(partial && l == 0.f);
       if (live && ok && half == 0) {
-        if (splits > 1) {
+        if (partial) {
           p.part_ml[2 * at] = m;
           p.part_ml[2 * at + 1] = l;
         } else {
@@ -939,7 +986,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
         const int ch = half * (D / 2) + c;
-        if (write && splits > 1) {
+        if (write && partial) {
           float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + ch);
 #pragma unroll
           for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -1047,7 +1094,7 @@ cudaError_t launch_tiles(const PagedParams& p, int groups, int splits, cudaStrea
   });
   if (e != cudaSuccess) return e;
   e = launch_early(tile_kernel<T, D, kT, kSpan>, groups * p.H * splits, C::kThreads, C::kSmem, stream, p, splits);
-  if (e != cudaSuccess || splits == 1) return e;
+  if (e != cudaSuccess || splits == 1 || kSpan == kSharedPrefix) return e;
   // the fold's blocks may start while the last parts still run: they wait for them
   return launch_early(tile_fold_kernel<T, D, kT>, groups * p.H * (C::kRows / 8), 256, 0, stream, p, splits);
 }

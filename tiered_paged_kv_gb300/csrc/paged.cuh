@@ -138,6 +138,8 @@ struct PagedParams {
   uint64_t wait_ns;
   float qscale;  // sm_scale * log2(e)
   int n_req, n_q, max_pages, H, G, o_f32;
+  const int32_t* own_lens;  // shared prefixes: tokens of each query token's own request
+  int32_t* own_begin;       // and where what it does not share begins (written)
   int window, sinks;  // windows: tokens that a query sees up to its own, and first ones that it always sees
   int run_rows;  // query rows of a run, 8 or 16 (set at launch)
   int whole;     // a block per run (set at launch)
@@ -179,6 +181,21 @@ inline bool read_twice(int64_t runs, int max_pages, int D) {
 constexpr int kTileRows = 128;    // query rows of a tile; a block takes `tiles` (1 or 2) of them
 cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
                                cudaStream_t stream);
+// Row tiles over the prefixes of groups; their parts stay in the workspace, for launch_shared_join:
+// p.part_o [split][n_q][H * G][D] beside p.part_ml, and what the requests do not share, normalised.
+cudaError_t launch_shared_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits, cudaStream_t stream);
+struct SharedJoinParams {
+  const float* part_o;
+  const float* part_ml;
+  const float* own_o;  // [n_q][H * G][D], and its log-sums
+  const float* own_lse;
+  const int32_t* own_begin;  // 0: nothing shared
+  void* o;
+  float* lse;
+  int64_t o_stride;
+  int n_q, HQ, splits, o_f32;
+};
+cudaError_t launch_shared_join(const SharedJoinParams& p, int D, int dtype, cudaStream_t stream);
 cudaError_t launch_window_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
                                 cudaStream_t stream);
 
@@ -305,8 +322,8 @@ __device__ __forceinline__ void request_span(const PagedParams& p, int b, int& l
 }
 
 // What the queries of a launch see of their request: all of it (or [begin, n)), or its last tokens
-// and its first ones.
-enum : int { kWholeHistory = 0, kWindowed = 1 };
+// and its first ones; or, a request being a group of decoding requests, the prefix that they share.
+enum : int { kWholeHistory = 0, kWindowed = 1, kSharedPrefix = 2 };
 
 // Request b's query rows: tokens [first, first + count) of q.
 __device__ __forceinline__ void request_rows(const PagedParams& p, int b, int& first, int& count) {
