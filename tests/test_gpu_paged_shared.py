@@ -126,17 +126,25 @@ def test_heads(G, D, dtype):
     run([(200, [230, 260, 201])], 2 if G < 100 else 1, G, D, dtype, seed=G)
 
 
+# Few rows a group go through one launch in runs, many as row tiles: both
+FEW_AND_MANY = pytest.mark.parametrize("G", [2, 20])
+
+
+@FEW_AND_MANY
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("prefix", [0, 1, 63, 64, 65, 128, 1000])
-def test_prefix_lengths(prefix, D):
+def test_prefix_lengths(prefix, D, G):
     """Also one that ends inside a page, requests with nothing of their own, and with less than it."""
-    run([(prefix, [prefix + 3, prefix, prefix + 64, prefix + 200])], 1, 2, D, "bf16")
-    run([(prefix, [prefix + 3, prefix // 2, 0, prefix])], 1, 2, D, "bf16")
+    run([(prefix, [prefix + 3, prefix, prefix + 64, prefix + 200])], 1, G, D, "bf16")
+    run([(prefix, [prefix + 3, prefix // 2, 0, prefix])], 1, G, D, "bf16")
 
 
+@FEW_AND_MANY
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_groups_of_all_sizes(D):
-    run([(300, [320] * 2 + [0]), (40, [41]), (700, []), (130, [130 + i for i in range(70)]), (64, [0, 0])], 2, 2, D, "f16",
+def test_groups_of_all_sizes(D, G):
+    run([(300, [320] * 2 + [0]), (40, [41]), (700, []), (130, [130 + i for i in range(70)]), (64, [0, 0])], 2, G, D, "f16",
+        alone=(70, 0, 333, 1))
+    run([(300, [320] * 2 + [0]), (40, [41]), (700, []), (130, [130 + i for i in range(7)]), (64, [0, 0])], 1, G, D, "bf16",
         alone=(70, 0, 333, 1))
 
 
@@ -146,34 +154,39 @@ def test_more_rows_than_a_tile(G, n):
     run([(500, [500 + (i * 7) % 90 for i in range(n)])], 1, G, 256, "f16")
 
 
-def test_long_prefixes():
+@FEW_AND_MANY
+def test_long_prefixes(G):
     """Cut into many parts; own parts cut into ranges."""
-    run([(9000, [9100, 9003, 9000, 12000])], 1, 4, 128, "bf16")
-    run([(6000, [6100, 6003]), (3000, [3000, 8000, 3500])], 1, 8, 256, "bf16")
+    run([(9000, [9100, 9003, 9000, 12000])], 1, G, 128, "bf16")
+    run([(6000, [6100, 6003]), (3000, [3000, 8000, 3500])], 1, G, 256, "bf16")
 
 
-def test_nobody_has_the_whole_prefix():
+@FEW_AND_MANY
+def test_nobody_has_the_whole_prefix(G):
     """The row with the most of it is read, whichever that is."""
-    run([(500, [0, 130, 300, 300, 20]), (200, [0, 199])], 1, 3, 128, "bf16")
+    run([(500, [0, 130, 300, 300, 20]), (200, [0, 199])], 1, G, 128, "bf16")
 
 
-def test_strides_scale_and_output_type():
-    run([(100, [150, 120])], 2, 2, 64, "f16", f32=True, q_gap=16, o_gap=24, scale=0.4)
-    run([(100, [150, 120])], 2, 2, 256, "bf16", q_gap=8, o_gap=8, scale=-0.05, alone=(30,))
-    run([(100, [150, 120])], 2, 2, 128, "bf16", f32=True)
+@FEW_AND_MANY
+def test_strides_scale_and_output_type(G):
+    run([(100, [150, 120])], 2, G, 64, "f16", f32=True, q_gap=16, o_gap=24, scale=0.4)
+    run([(100, [150, 120])], 2, G, 256, "bf16", q_gap=8, o_gap=8, scale=-0.05, alone=(30,))
+    run([(100, [150, 120])], 2, G, 128, "bf16", f32=True)
 
 
+@FEW_AND_MANY
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_large_scores(D):
-    run([(300, [350, 420])], 1, 2, D, "bf16", scale=4.0)
+def test_large_scores(D, G):
+    run([(300, [350, 420])], 1, G, D, "bf16", scale=4.0)
 
 
 def test_many_requests_and_groups():
     run([(64 * (i % 4), [64 * (i % 4) + j * 9 for j in range(1 + i % 7)]) for i in range(90)], 1, 2, 64, "bf16")
 
 
-def test_nan_queries_stay_in_their_row():
-    c = Shared([(200, [230, 260, 201])], 2, 4, 128, "bf16")
+@FEW_AND_MANY
+def test_nan_queries_stay_in_their_row(G):
+    c = Shared([(200, [230, 260, 201])], 2, G, 128, "bf16")
     c.dq[1, 128:256] = float("nan")
     c.call()
     torch.cuda.synchronize()
@@ -182,9 +195,10 @@ def test_nan_queries_stay_in_their_row():
     assert torch.isfinite(c.o).all() and torch.isfinite(c.lse).all()
 
 
-def test_bad_entries_and_counts():
+@FEW_AND_MANY
+def test_bad_entries_and_counts(G):
     """A page of the prefix that is not there is left out for everybody; values out of range are cut."""
-    c = Shared([(300, [320, 330])], 1, 2, 64, "bf16")
+    c = Shared([(300, [320, 330])], 1, G, 64, "bf16")
     c.table[0, 1] = c.slots  # the row that is read for the group
     c.keys = [torch.cat([k[:64], k[128:]]) for k in c.keys]
     c.values = [torch.cat([v[:64], v[128:]]) for v in c.values]
@@ -192,7 +206,7 @@ def test_bad_entries_and_counts():
     c.call()
     c.check()
     assert tpk.get_device_status(reset=True) == (4, 1)
-    c = Shared([(128, [128, 128])], 1, 2, 64, "bf16")
+    c = Shared([(128, [128, 128])], 1, G, 64, "bf16")
     c.shared.fill_(5000)
     c.off.copy_(torch.tensor([-3, 9], dtype=torch.int32))
     c.call()
@@ -200,8 +214,9 @@ def test_bad_entries_and_counts():
     assert tpk.get_device_status(reset=True) == (4, 1)
 
 
-def test_other_stream_captured_and_grown():
-    c = Shared([(300, [320, 330]), (64, [100, 70])], 2, 4, 128, "bf16", alone=(40, 50))
+@FEW_AND_MANY
+def test_other_stream_captured_and_grown(G):
+    c = Shared([(300, [320, 330]), (64, [100, 70])], 2, G, 128, "bf16", alone=(40, 50))
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(st):
@@ -237,7 +252,8 @@ def test_one_workspace_for_fewer_requests():
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("groups,H,G", [([(3000, [3100, 3300])], 1, 4), ([(300, [310] * 70)], 2, 8),
-                                        ([(500, [600, 700]), (80, [90] * 5)], 1, 2)])
+                                        ([(500, [600, 700]), (80, [90] * 5)], 1, 2),
+                                        ([(500, [600, 700]), (80, [90] * 5)], 1, 20)])
 def test_waits_are_bounded(groups, H, G, D):
     stalled(Shared(groups, H, G, D, "bf16"))
 

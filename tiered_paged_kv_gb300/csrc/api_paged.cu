@@ -379,6 +379,19 @@ SharedPlan shared_plan(const tpk_paged_shape* s, int n_req, int n_grp) {
   return {tiles, n_req / per + n_grp, std::max<int64_t>(splits, 1)};
 }
 
+// Whether prefixes and the rest go through one split launch, which reads a prefix once for every 16
+// rows of a group, rather than once for 128 and two launches more: with up to 16 rows (one group of 16,
+// 8 heads of 128, 2,000 tokens: 13.7 us and 23.0 as tiles; 30,000: 33.5 and 53.9; four groups of 30,000:
+// 87 and 114); with up to 32 for as long as two readers mostly meet in L2 (four groups of 8,000: 45 and
+// 59; of 30,000: 153 and 115); with up to 64 where prefixes are short (one of 2,000: 17.6 and 24.6; four
+// of 8,000: 75 and 65).  Lengths are on the device: the table's width stands for them.
+bool shared_split(const tpk_paged_shape* s, int n_req, int n_grp) {
+  const int64_t each = ((int64_t)n_req + n_grp - 1) / n_grp, runs = (each * s->group + kRowTile - 1) / kRowTile;
+  const int64_t read = runs * n_grp * s->max_pages * s->kv_heads * (kPageTokens * 4 * s->head_dim);
+  return shared_split_fits(n_req, n_grp) &&
+         (runs == 1 || (runs == 2 && read <= (int64_t)320 << 20) || (runs <= 4 && read <= (int64_t)100 << 20));
+}
+
 // Rows of the prefixes' parts, bounded for all calls with no more requests: with more than one part
 // there are at most kSharedWaves * kTileBlocks + items of them, of at most two tiles' rows each.
 int64_t shared_rows(const tpk_paged_shape* s, int n_req) {
@@ -394,9 +407,10 @@ SharedWs shared_ws(const tpk_paged_shape* s, int n_req) {
   SharedWs w;
   w.part_ml = 0;
   w.part_o = w.part_ml + align256(parts * 8);
+  // results of the prefixes (where they are no parts), then of what is not shared
   w.own_o = w.part_o + align256(parts * s->head_dim * 4);
-  w.own_lse = w.own_o + align256(rows * s->head_dim * 4);
-  w.own_begin = w.own_lse + align256(rows * 4);
+  w.own_lse = w.own_o + align256(2 * rows * s->head_dim * 4);
+  w.own_begin = w.own_lse + align256(2 * rows * 4);
   w.split = w.own_begin + align256((size_t)n_req * 4);
   w.bytes = w.split + split_ws_bytes(s);
   return w;
@@ -727,41 +741,63 @@ tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n
   auto at = [&](size_t offset) { return static_cast<uint8_t*>(ws) + offset; };
   p.n_q = n_req;
   p.own_begin = reinterpret_cast<int32_t*>(at(w.own_begin));
-  // the prefixes: the groups are the requests
-  PagedParams g = p;
-  st = make_maps(g, shape, k_pool, v_pool, false);
-  if (st == TPK_OK) st = make_query_map(g, shape, n_req, q, q_stride);
-  // what the requests do not share
-  if (st == TPK_OK) st = make_maps(p, shape, k_pool, v_pool, true);
-  if (st != TPK_OK) return st;
-  g.n_req = n_grp;
-  g.q_off = grp_off;
-  g.lens = n_shared;
-  g.own_lens = n_tokens;
-  g.part_ml = reinterpret_cast<float*>(at(w.part_ml));
-  g.part_o = reinterpret_cast<float*>(at(w.part_o));
-  cudaError_t e = launch_shared_tiles(g, shape->head_dim, shape->dtype, plan.tiles, (int)plan.groups, (int)plan.splits, cs);
-  if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
-  place_ws(p, at(w.split));
-  p.begin = p.own_begin;
-  p.o = at(w.own_o);
-  p.o_f32 = 1;
-  p.o_stride = (int64_t)shape->kv_heads * shape->group * shape->head_dim;
-  p.lse = reinterpret_cast<float*>(at(w.own_lse));
-  e = launch_paged_split(p, shape->head_dim, shape->dtype, cs);
-  if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+  const int64_t HQ = (int64_t)shape->kv_heads * shape->group, rows = n_req * HQ;
+  float* const own_o = reinterpret_cast<float*>(at(w.own_o));
+  float* const own_lse = reinterpret_cast<float*>(at(w.own_lse));
   SharedJoinParams j;
-  j.part_o = g.part_o;
-  j.part_ml = g.part_ml;
-  j.own_o = static_cast<const float*>(p.o);
-  j.own_lse = p.lse;
+  std::memset(&j, 0, sizeof j);
+  // what the requests do not share
+  st = make_maps(p, shape, k_pool, v_pool, true);
+  if (st != TPK_OK) return st;
+  place_ws(p, at(w.split));
+  p.o = own_o;
+  p.o_f32 = 1;
+  p.o_stride = HQ * shape->head_dim;
+  p.lse = own_lse;
+  cudaError_t e;
+  if (shared_split(shape, n_req, n_grp)) {  // and the prefixes, in front of it
+    p.own_lens = n_tokens;
+    p.q_off = grp_off;
+    p.lens = n_shared;
+    p.n_grp = n_grp;
+    p.n_req = n_grp + n_req;
+    const int64_t each = ((int64_t)n_req + n_grp - 1) / n_grp;
+    p.run_rows = each * shape->group <= 8 ? 8 : kRowTile;
+    e = launch_shared_split(p, shape->head_dim, shape->dtype, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "shared decode launch");
+    j.whole_o = own_o;
+    j.whole_lse = own_lse;
+    j.own_o = own_o + rows * shape->head_dim;
+    j.own_lse = own_lse + rows;
+  } else {
+    // the prefixes: the groups are the requests
+    PagedParams g = p;
+    st = make_maps(g, shape, k_pool, v_pool, false);
+    if (st == TPK_OK) st = make_query_map(g, shape, n_req, q, q_stride);
+    if (st != TPK_OK) return st;
+    g.n_req = n_grp;
+    g.q_off = grp_off;
+    g.lens = n_shared;
+    g.own_lens = n_tokens;
+    g.part_ml = reinterpret_cast<float*>(at(w.part_ml));
+    g.part_o = reinterpret_cast<float*>(at(w.part_o));
+    e = launch_shared_tiles(g, shape->head_dim, shape->dtype, plan.tiles, (int)plan.groups, (int)plan.splits, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
+    p.begin = p.own_begin;
+    e = launch_paged_split(p, shape->head_dim, shape->dtype, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+    j.part_o = g.part_o;
+    j.part_ml = g.part_ml;
+    j.splits = (int)plan.splits;
+    j.own_o = own_o;
+    j.own_lse = own_lse;
+  }
   j.own_begin = p.own_begin;
   j.o = o;
   j.lse = lse;
   j.o_stride = o_stride;
   j.n_q = n_req;
-  j.HQ = shape->kv_heads * shape->group;
-  j.splits = (int)plan.splits;
+  j.HQ = (int)HQ;
   j.o_f32 = o_f32;
   e = launch_shared_join(j, shape->head_dim, shape->dtype, cs);
   return e == cudaSuccess ? TPK_OK : cuda_fail(e, "shared join launch");

@@ -74,37 +74,70 @@ struct Seen {
   int sink_pages, skip;  // pages between the first ones and the span's
   // page i of them
   __device__ __forceinline__ int page(int i) const {
-    return kSpan == kWholeHistory ? (lo >> 6) + i : i < sink_pages ? i : i + skip;
+    return kSpan != kWindowed ? (lo >> 6) + i : i < sink_pages ? i : i + skip;
   }
 };
 
-// Runs and pages of request b.
-__device__ __forceinline__ int request_runs(const PagedParams& p, int b) {
-  int first, count;
-  request_rows(p, b, first, count);
-  return p.H * (int)(((int64_t)count * p.G + p.run_rows - 1) >> (p.run_rows == 8 ? 3 : 4));
-}
-template <int kSpan>
-__device__ __forceinline__ int request_pages(const PagedParams& p, int b, Seen<kSpan>& s) {
-  request_span(p, b, s.lo, s.hi);
-  s.sink_pages = 0;
-  if (kSpan == kWindowed) {  // from the first query token's window on
-    int first, count;
-    request_rows(p, b, first, count);
-    s.lo = min(max(max(s.hi - count + 1, 0) - p.window, 0), s.hi);
-    s.sink_pages = min((min(p.sinks, s.lo) + 63) >> 6, s.lo >> 6);
-  }
-  s.skip = (s.lo >> 6) - s.sink_pages;
-  return s.hi > s.lo ? s.sink_pages + ((s.hi + 63) >> 6) - (s.lo >> 6) : 0;
-}
 constexpr int kRunCost = 3;
-// Units of request b.
+
+// Shared prefixes: a request of the numbering is a group's prefix, or what a request does not share.
+struct VirtualReq {
+  int lo, hi;                 // tokens [lo, hi) of the table row
+  uint8_t first, count, row;  // whose queries these are, and that row
+};
+constexpr int kVirtual = 96;  // of them; query rows and table rows fit a byte
+
+// The requests of a launch: their query rows, runs, pages and units.
 template <int kSpan>
-__device__ __forceinline__ int64_t request_units(const PagedParams& p, int b) {
-  Seen<kSpan> seen;
-  const int pages = request_pages<kSpan>(p, b, seen);
-  return pages > 0 ? (int64_t)(pages + kRunCost) * request_runs(p, b) : 0;
-}
+struct Batch {
+  const PagedParams& p;
+  const VirtualReq* v;  // shared prefixes only
+
+  __device__ __forceinline__ void rows(int b, int& first, int& count) const {
+    if (kSpan == kSharedPrefix) {
+      first = v[b].first;
+      count = v[b].count;
+    } else {
+      request_rows(p, b, first, count);
+    }
+  }
+  __device__ __forceinline__ int runs(int b) const {
+    int first, count;
+    rows(b, first, count);
+    return p.H * (int)(((int64_t)count * p.G + p.run_rows - 1) >> (p.run_rows == 8 ? 3 : 4));
+  }
+  __device__ __forceinline__ int pages(int b, Seen<kSpan>& s) const {
+    if (kSpan == kSharedPrefix) {
+      s.lo = v[b].lo;
+      s.hi = v[b].hi;
+    } else {
+      request_span(p, b, s.lo, s.hi);
+    }
+    s.sink_pages = 0;
+    if (kSpan == kWindowed) {  // from the first query token's window on
+      int first, count;
+      rows(b, first, count);
+      s.lo = min(max(max(s.hi - count + 1, 0) - p.window, 0), s.hi);
+      s.sink_pages = min((min(p.sinks, s.lo) + 63) >> 6, s.lo >> 6);
+    }
+    s.skip = (s.lo >> 6) - s.sink_pages;
+    return s.hi > s.lo ? s.sink_pages + ((s.hi + 63) >> 6) - (s.lo >> 6) : 0;
+  }
+  __device__ __forceinline__ int64_t units(int b) const {
+    Seen<kSpan> seen;
+    const int n = pages(b, seen);
+    return n > 0 ? (int64_t)(n + kRunCost) * runs(b) : 0;
+  }
+  __device__ __forceinline__ const int32_t* table(int b) const {
+    return p.table + (int64_t)(kSpan == kSharedPrefix ? v[b].row : b) * p.max_pages;
+  }
+  // where the results of its first query token go: behind a launch over shared prefixes those of the
+  // prefixes come first, then those of what is not shared
+  __device__ __forceinline__ int out(int b, int first) const {
+    return kSpan == kSharedPrefix && b >= p.n_grp ? first + p.n_q : first;
+  }
+};
+
 __device__ __forceinline__ int64_t per_block(int64_t total, int blocks) {
   const int64_t per = (total + blocks - 1) / blocks;
   return per < kRunCost + 1 ? kRunCost + 1 : per;
@@ -162,11 +195,11 @@ template <int kSpan>
 struct Walk {
   int64_t at, end, base;
   int b;
-  __device__ __forceinline__ bool next(const PagedParams& p, Segment<kSpan>& s) {
+  __device__ __forceinline__ bool next(const Batch<kSpan>& batch, Segment<kSpan>& s) {
     while (at < end) {
-      s.pages = request_pages<kSpan>(p, b, s.seen);
+      s.pages = batch.pages(b, s.seen);
       const int units = s.pages + kRunCost;
-      const int64_t work = s.pages > 0 ? (int64_t)units * request_runs(p, b) : 0;
+      const int64_t work = s.pages > 0 ? (int64_t)units * batch.runs(b) : 0;
       if (at >= base + work) {
         base += work;
         ++b;
@@ -256,6 +289,7 @@ struct Rows {
         see_lo[e] = max(tok_lo, p.range[2 * (int64_t)token]);
         see_hi[e] = min(tok_hi, p.range[2 * (int64_t)token + 1]);
       }
+      if (kSpan == kSharedPrefix && live) see_hi[e] = min(tok_hi, max(p.own_lens[token], 0));
       if (kSpan == kWindowed) {  // the query token's position is its place among the request's last ones
         see_hi[e] = live ? max(tok_hi - count + (token - first) + 1, 0) : 0;
         see_lo[e] = max(see_hi[e] - p.window, 0);
@@ -402,6 +436,44 @@ struct Rows {
   }
 };
 
+// The numbering's requests of a launch over shared prefixes: the p.n_grp groups (p.q_off their first
+// requests, p.lens their prefixes), then what each of the p.n_q requests has of its own.  A prefix
+// is read from the row of the first request that has the most of it.  For the whole block.
+__device__ __forceinline__ void shared_requests(const PagedParams& p, VirtualReq* v) {
+  const int cap = p.max_pages * 64;
+  bool bad = false;
+  auto tokens = [&](int b) {
+    const int n = p.own_lens[b], c = min(max(n, 0), cap);
+    bad |= n != c;
+    return c;
+  };
+  for (int g = threadIdx.x; g < p.n_grp; g += kPagedThreads) {
+    int first, count, most = 0, row = 0;
+    request_rows(p, g, first, count);
+    const int shared = p.lens[g], n = min(max(shared, 0), cap);
+    bad |= shared != n;
+    if (count < 2) count = 0;  // nobody to share with
+    for (int i = 0; i < count; ++i) {
+      const int own = min(tokens(first + i), n);
+      if (own > most) {
+        most = own;
+        row = first + i;
+      }
+    }
+    v[g] = {0, most, (uint8_t)first, (uint8_t)count, (uint8_t)row};
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.n_q; b += kPagedThreads) {
+    int begin = 0;
+    for (int g = 0; g < p.n_grp; ++g)
+      if (b >= v[g].first && b < v[g].first + v[g].count) begin = v[g].hi;
+    v[p.n_grp + b] = {begin, tokens(b), (uint8_t)b, 1, (uint8_t)b};
+    if (blockIdx.x == 0) p.own_begin[b] = begin;
+  }
+  if (bad) atomicOr(p.status, kStatusBadSlot);
+  __syncthreads();
+}
+
 // The second bound asks for the registers of kBlocksPerSm blocks.  In the wide form at
 // D = 128 two fit without it (167 registers); with it the compiler spills (96 requests of
 // 1000 tokens, 16 rows: 73 us without, 80 with; asking for one block, which takes 214, 91).
@@ -434,6 +506,9 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
     fence_mbar_init();
   }
   wait_before();
+  VirtualReq* const virtuals = reinterpret_cast<VirtualReq*>(stages + C::kStages * C::kStageBytes + C::kJoinBytes + C::kSharedBytes);
+  if (kSpan == kSharedPrefix) shared_requests(p, virtuals);
+  const Batch<kSpan> batch{p, virtuals};
   Walk<kSpan> walk;
   int64_t per = 0;  // numbers of a range
   if (p.whole) {
@@ -441,29 +516,29 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
     int64_t run;
     if (p.q_off) {
       Numbers numbers;
-      numbers.load(p, request_runs);
+      numbers.load(p, [&](const PagedParams&, int b) { return batch.runs(b); });
       if (blockIdx.x >= numbers.total) return;  // the grid is an upper bound
       numbers.find(blockIdx.x, walk.b, run);
       run = blockIdx.x - run;
     } else {
-      const int runs = request_runs(p, 0);
+      const int runs = batch.runs(0);
       walk.b = blockIdx.x / runs;
       run = blockIdx.x - walk.b * runs;
     }
     __syncthreads();
     int first, count;
     Seen<kSpan> seen;
-    const int runs = request_runs(p, walk.b);
-    const int pages = request_pages<kSpan>(p, walk.b, seen);
+    const int runs = batch.runs(walk.b);
+    const int pages = batch.pages(walk.b, seen);
     walk.base = 0;
     walk.at = run * (pages + kRunCost);
     walk.end = walk.at + pages + kRunCost;
     if (pages == 0) {
-      request_rows(p, walk.b, first, count);
+      batch.rows(walk.b, first, count);
       const int tiles = runs / p.H, h = (int)run / tiles;
       for (int i = tid; i < p.run_rows * (D / 2); i += kPagedThreads) {
         int token, head;
-        if (!run_row(p, first, count, h, (int)run - h * tiles, i / (D / 2), token, head)) continue;
+        if (!run_row(p, batch.out(walk.b, first), count, h, (int)run - h * tiles, i / (D / 2), token, head)) continue;
         store_pair<T>(p, token, head, D, i % (D / 2) * 2, 0.f, 0.f);
         if (i % (D / 2) == 0) p.lse[(int64_t)token * p.H * p.G + head] = kEmpty;
       }
@@ -474,7 +549,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
     int64_t lo, hi;
     if (p.n_req <= kScanned) {
       Numbers numbers;
-      numbers.load(p, request_units<kSpan>);
+      numbers.load(p, [&](const PagedParams&, int b) { return batch.units(b); });
       per = per_block(numbers.total, gridDim.x);
       lo = min(per * blockIdx.x, numbers.total);
       hi = min(lo + per, numbers.total);
@@ -484,7 +559,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
       const int each = (p.n_req + kPagedThreads - 1) / kPagedThreads;
       const int b0 = min(tid * each, p.n_req), b1 = min(b0 + each, p.n_req);
       int64_t mine = 0;
-      for (int b = b0; b < b1; ++b) mine += request_units<kSpan>(p, b);
+      for (int b = b0; b < b1; ++b) mine += batch.units(b);
       int64_t inc = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -505,7 +580,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
       if (lo < hi && lo >= before && lo < before + mine) {
         int64_t at = before;
         for (int b = b0; b < b1; ++b) {
-          const int64_t work = request_units<kSpan>(p, b);
+          const int64_t work = batch.units(b);
           if (lo >= at && lo < at + work) {
             S.first = b;
             S.base = at;
@@ -525,8 +600,9 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
   for (int b = blockIdx.x; b < p.n_req; b += gridDim.x) {
     int first, count;
     Seen<kSpan> seen;
-    if (request_pages<kSpan>(p, b, seen) > 0) continue;
-    request_rows(p, b, first, count);
+    if (batch.pages(b, seen) > 0) continue;
+    batch.rows(b, first, count);
+    first = batch.out(b, first);
     const int HQ = p.H * p.G;
     for (int64_t i = tid; i < (int64_t)count * HQ * (D / 2); i += kPagedThreads) {
       const int64_t r = i / (D / 2);
@@ -543,10 +619,10 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
     const bool stalled = (int)blockIdx.x == p.stall_unit;
     int item = 0;
     bool dead = false;
-    while (!dead && walk.next(p, s)) {
-      const int tiles = request_runs(p, s.b) / p.H;
+    while (!dead && walk.next(batch, s)) {
+      const int tiles = batch.runs(s.b) / p.H;
       const int h = s.run / tiles;
-      const int32_t* row = p.table + (int64_t)s.b * p.max_pages;
+      const int32_t* row = batch.table(s.b);
       for (int j0 = 0; j0 < s.count && !dead; j0 += 32) {
         const int entry = j0 + lane < s.count ? row[s.seen.page(s.page + j0 + lane)] : 0;
         const int n = min(32, s.count - j0);
@@ -599,13 +675,14 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
   Rows<T, D, kSmall, kSpan> rows(lane);
   bool dead = false;
   int item = 0;  // pages of this block so far
-  while (walk.next(p, s)) {
+  while (walk.next(batch, s)) {
     const int tok_lo = s.seen.lo, tok_hi = s.seen.hi;
     // tokens that no row sees: their rows in the pages may hold anything
     auto hidden = [&](int t) { return (t < tok_lo && !(kSpan == kWindowed && t < p.sinks)) || t >= tok_hi; };
     int first, count;
-    request_rows(p, s.b, first, count);
-    const int tiles = request_runs(p, s.b) / p.H;
+    batch.rows(s.b, first, count);
+    const int out = batch.out(s.b, first);  // its rows in the output
+    const int tiles = batch.runs(s.b) / p.H;
     const int h = s.run / tiles, tile = s.run - h * tiles;
     rows.start(p, first, count, h, tile, s.seen);
 
@@ -672,11 +749,11 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) L += exp2f(S.m[w][r] - (M == kEmpty ? 0.f : M)) * S.l[w][r];
       int token, head;
-      const bool write = run_row(p, first, count, h, tile, r, token, head) && !dead;
+      const bool write = run_row(p, out, count, h, tile, r, token, head) && !dead;
       const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
       // the join's record: this block has the run's first page and not its last
       if (tid == 0 && pass == 0 && !whole && s.page == 0)
-        p.cuts[blockIdx.x] = {first, count, h, tile, (int)((s.pages - s.count - 1) / per) + 2};
+        p.cuts[blockIdx.x] = {out, count, h, tile, (int)((s.pages - s.count - 1) / per) + 2};
       if (write && tid % kPer == 0) {
         if (whole) {
           p.lse[(int64_t)token * HQ + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
@@ -794,19 +871,22 @@ int device_sms();
 // Runs of a launch: a decode's, an upper bound of cross attention's.
 inline int64_t most_runs(const PagedParams& p) {
   const int64_t each = (p.G + p.run_rows - 1) / p.run_rows;
+  if (p.n_grp > 0) return p.H * ((int64_t)p.n_q * p.G / p.run_rows + p.n_grp + p.n_q * each);
   return p.H * (p.q_off ? (int64_t)p.n_q * p.G / p.run_rows + p.n_req : p.n_req * each);
 }
 
 template <typename T, int D, bool kSmall, bool kMany, int kSpan>
 cudaError_t launch_split(const PagedParams& p, cudaStream_t stream) {
   using C = SplitCfg<D, kMany>;
+  constexpr int extra = kSpan == kSharedPrefix ? kVirtual * (int)sizeof(VirtualReq) : 0;
+  static_assert(C::kBlocksPerSm * (C::kSmem + extra + 1024) <= 228 * 1024, "blocks per SM");
   static DeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(split_kernel<T, D, kSmall, kMany, kSpan>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return cudaFuncSetAttribute(split_kernel<T, D, kSmall, kMany, kSpan>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem + extra);
   });
   if (e != cudaSuccess) return e;
   const int blocks = p.whole ? (int)most_runs(p) : min(device_sms() * C::kBlocksPerSm, kPagedMaxBlocks);
-  e = launch_early(split_kernel<T, D, kSmall, kMany, kSpan>, blocks, kPagedThreads, C::kSmem, stream, p);
+  e = launch_early(split_kernel<T, D, kSmall, kMany, kSpan>, blocks, kPagedThreads, C::kSmem + extra, stream, p);
   if (e != cudaSuccess || p.whole || blocks == 1) return e;
   // the fold's blocks may start while the last ranges still run: they wait for them
   const int rows = p.q_off ? p.run_rows : min(p.G, p.run_rows);
@@ -815,7 +895,7 @@ cudaError_t launch_split(const PagedParams& p, cudaStream_t stream) {
 
 template <typename T, int D, int kSpan>
 cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
-  if constexpr (D <= 128) {
+  if constexpr (D <= 128 && kSpan != kSharedPrefix) {
     // A block per SM more, of a stage less, for whole runs: 40 requests of 1500 tokens, 8 heads of
     // 128, one wave instead of two, 51 -> 41 us; 64 of 1500, heads of 64, 44 -> 34; 400 of 250, 128,
     // 84 -> 75; not where its waves leave more of the device idle (64 of 1500, 128: 62 and 74),

@@ -23,11 +23,18 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const SharedJoinParams
   wait_before();  // nothing is read before it
   if (r >= rows) return;
   const int b = (int)(r / p.HQ);
-  float2 own[D / 64], v[kJoined][D / 64];
+  float2 own[D / 64], all[D / 64], v[kJoined][D / 64];
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) own[e] = *reinterpret_cast<const float2*>(p.own_o + r * D + e * 64 + 2 * lane);
   const float own_lse = p.own_lse[r];
-  const int splits = p.own_begin[b] > 0 ? p.splits : 0;
+  const bool shares = p.own_begin[b] > 0;
+  const int splits = shares ? p.splits : 0;
+  float all_lse = kNone;
+  if (p.whole_o && shares) {
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) all[e] = *reinterpret_cast<const float2*>(p.whole_o + r * D + e * 64 + 2 * lane);
+    all_lse = p.whole_lse[r];
+  }
   float2 ml = make_float2(kNone, 0.f);
   if (lane < splits) ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (lane * rows + r));
   auto load = [&](int k0) {
@@ -39,9 +46,10 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const SharedJoinParams
           v[j][e] = *reinterpret_cast<const float2*>(p.part_o + ((k0 + j) * rows + r) * D + e * 64 + 2 * lane);
   };
   load(0);
-  // the request's own part is normalised: its sum is 1 at the maximum log2(e) lse (a NaN stays one)
+  // what is normalised has the sum 1 at the maximum log2(e) lse (a NaN stays one)
   const float own_m = own_lse * kLog2e, own_l = own_lse == kNone ? 0.f : 1.f;
-  float M = fmaxf(ml.y == 0.f ? kNone : ml.x, own_m);
+  const float all_m = all_lse * kLog2e, all_l = all_lse == kNone ? 0.f : 1.f;
+  float M = fmaxf(fmaxf(ml.y == 0.f ? kNone : ml.x, own_m), all_m);
   for (int k = lane + 32; k < splits; k += 32) {
     const float2 x = *reinterpret_cast<const float2*>(p.part_ml + 2 * (k * rows + r));
     if (x.y != 0.f) M = fmaxf(M, x.x);
@@ -71,6 +79,7 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const SharedJoinParams
       add(__shfl_sync(0xffffffffu, ml.x, (k0 + j) & 31), __shfl_sync(0xffffffffu, ml.y, (k0 + j) & 31), v[j]);
     }
   }
+  add(all_m, all_l, all);
   add(own_m, own_l, own);
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const int64_t at = b * p.o_stride + (r - (int64_t)b * p.HQ) * D;

@@ -140,6 +140,7 @@ struct PagedParams {
   int n_req, n_q, max_pages, H, G, o_f32;
   const int32_t* own_lens;  // shared prefixes: tokens of each query token's own request
   int32_t* own_begin;       // and where what it does not share begins (written)
+  int n_grp;          // groups that share prefixes, in a split launch; 0: none
   int window, sinks;  // windows: tokens that a query sees up to its own, and first ones that it always sees
   int run_rows;  // query rows of a run, 8 or 16 (set at launch)
   int whole;     // a block per run (set at launch)
@@ -150,6 +151,10 @@ constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row
 constexpr int kPagedMaxBlocks = 512;  // blocks of a split launch; each owns two partial slots
 constexpr int kRowTile = 16;          // query rows of a split run, at most
 cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream);
+// The same over prefixes of groups and what each request has of its own, at most kVirtual of both, each
+// with results of its own (p.o and p.lse of [2][n_q] rows); run_rows: rows of a run.
+cudaError_t launch_shared_split(PagedParams& p, int D, int dtype, cudaStream_t stream);
+bool shared_split_fits(int n_req, int n_grp);
 // The same through windows; span_pages: pages that a request's queries see, at most (a hint).
 cudaError_t launch_window_split(PagedParams& p, int span_pages, int D, int dtype, cudaStream_t stream);
 
@@ -187,7 +192,9 @@ cudaError_t launch_shared_tiles(const PagedParams& p, int D, int dtype, int tile
 struct SharedJoinParams {
   const float* part_o;
   const float* part_ml;
-  const float* own_o;  // [n_q][H * G][D], and its log-sums
+  const float* whole_o;  // the prefix's result, where it is not in parts
+  const float* whole_lse;
+  const float* own_o;    // [n_q][H * G][D], and its log-sums
   const float* own_lse;
   const int32_t* own_begin;  // 0: nothing shared
   void* o;
