@@ -62,7 +62,13 @@ __device__ __forceinline__ bool far_off(float m) {
 constexpr int kKeys = 128;     // tokens of a key tile
 constexpr uint32_t kTmemCols = 512;
 
-template <int D, int kT>
+// Threads that share a row's softmax.  With one row tile the steps follow each other: four threads do
+// one faster than two (64 requests' queries over a prefix of 32,768 tokens, 4 x 8 heads of 256: 73 us
+// with two).  Whole histories keep two, and their order of sums.
+template <int D, int kT, int kSpan>
+constexpr int kRowThreads = kSpan != kWholeHistory && kT == 1 && D >= 128 ? 4 : 2;
+
+template <int D, int kT, int kShare>
 struct TileCfg {
   static constexpr int kTiles = kT;
   static constexpr int kRows = kTiles * kTileRows;
@@ -73,7 +79,7 @@ struct TileCfg {
   static constexpr int kQBytes = kTileRows * D * 2;  // one tile
   static constexpr int kSharedBytes = 3 * 1024;      // TileShared
   static constexpr int kSmem = kSharedBytes + kTiles * kQBytes + kSlots * kSlotBytes;
-  static constexpr int kSoftWarps = kTiles * 8;  // softmax: two threads per row
+  static constexpr int kSoftWarps = kTiles * 4 * kShare;  // softmax: kShare threads per row
   static constexpr int kMma = kSoftWarps, kLoad = kMma + 1, kQuery = kLoad + 1;
   // At D = 256 one loader issues more slowly than the tensor core takes the tiles, and the
   // values get a warp of their own (72 -> 70 us at the clips); at 128 it costs 2 %.
@@ -144,8 +150,8 @@ struct TileShared {
   // what the block must see land before it ends: by slot, the copies that complete its `full`; those
   // that complete `tail` and `q_full`
   int laps[8], tails, loads;
-  int fine[2][8][2];               // [item parity][pair of warps][half]: waits met so far
-  float half[4 * kTileRows];       // what the two threads of a row tell each other
+  int fine[2][16];                 // [item parity][softmax warp]: waits met so far
+  float half[4 * kTileRows];       // what the threads of a row tell each other
 };
 
 // ------------------------------------------------------------ tcgen05 wrappers
@@ -242,6 +248,9 @@ __device__ __forceinline__ constexpr uint32_t instruction(bool bf16, bool b_rows
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_rows_reduced ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
          (uint32_t)(kTileRows >> 4) << 24;
 }
+
+// The n lowest bits, none below 0 and all from 32 on.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0 : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 
 template <typename T>
 struct IsBf16 {
@@ -359,11 +368,17 @@ struct Requests {
     if constexpr (kSpan == kSharedPrefix) {
       // the prefix is read from the row of the first request that has the most of it
       const int lead = it.first - t;
-      int most = 0, row = 0x7fffffff;
-      for (int i = lead + lane; i < lead + all; i += 32) most = max(most, min(p.own_lens[i], it.len));
+      int most = -1, row = 0x7fffffff;
+      for (int i = lead + lane; i < lead + all; i += 32) {
+        const int n = min(max(p.own_lens[i], 0), it.len);
+        if (n > most) {
+          most = n;
+          row = i;
+        }
+      }
+      const int mine = most;
       most = __reduce_max_sync(0xffffffffu, most);
-      for (int i = lead + lane; i < lead + all; i += 32)
-        if (min(p.own_lens[i], it.len) == most) row = min(row, i);
+      if (mine != most) row = 0x7fffffff;
       it.len = most;
       it.b = __reduce_min_sync(0xffffffffu, row);
     }
@@ -372,9 +387,10 @@ struct Requests {
 };
 
 template <typename T, int D, int kT, int kSpan>
-__global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
+__global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kThreads, 1)
     tile_kernel(const __grid_constant__ PagedParams p, int splits) {
-  using C = TileCfg<D, kT>;
+  constexpr int kShare = kRowThreads<D, kT, kSpan>;
+  using C = TileCfg<D, kT, kShare>;
   using Item = ::tpk::Item<kSpan>;
   extern __shared__ __align__(1024) uint8_t raw[];
   static_assert(sizeof(TileShared<kSpan>) <= C::kSharedBytes, "TileShared");
@@ -401,7 +417,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       mbar_init(&S.p_half[i], 256);
       mbar_init(&S.p_full[i], 256);
       mbar_init(&S.o_full[i], 1);
-      mbar_init(&S.o_empty[i], 256);
+      mbar_init(&S.o_empty[i], kTileRows * kShare);
       mbar_init(&S.item_full[i], 1);
       mbar_init(&S.item_empty[i], C::kSoftWarps + 2 + C::kTwoLoaders);
     }
@@ -577,7 +593,8 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
             for (int y = 0; y < 4; ++y) {
               const int i = (y >> 1) * 4 + 2 * s + (y & 1);  // 16 tokens: two 8-row groups
               if (i < groups)
-                tc_mma_ts(tmem + 256 + x * 128 + c * 128, tmem + buf * kKeys + i / 4 * (kKeys / 2) + i % 4 * 8,
+                tc_mma_ts(tmem + 256 + x * 128 + c * 128,
+                          tmem + buf * kKeys + i / (8 / kShare) * (kKeys / kShare) + i % (8 / kShare) * 8,
                           v + i * 128, id_pv, more || s > 0 || y > 0);
             }
             if (last && s == 1) tc_commit(empty + 8 * nth(at, c));
@@ -798,35 +815,38 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
     }
   } else {
     // ----------------------------------------------------------------- softmax
-    // Warp w has rows 32 (w mod 4) .. of tile w / 8 (a warp reaches the TMEM rows of its
-    // number mod 4 only) and keys 64 (w / 4 mod 2) .. of each key tile.
-    const int tile = warp >> 3, half = warp >> 2 & 1, row = (warp & 3) * 32 + lane, hrow = tile * kTileRows + row;
+    // Warp w has rows 32 (w mod 4) .. of tile w / (4 kShare) (a warp reaches the TMEM rows of its
+    // number mod 4 only) and kMine keys of each key tile.
+    constexpr int kMine = kKeys / kShare;  // keys of this thread's part
+    const int tile = warp / (4 * kShare), half = warp / 4 % kShare, row = (warp & 3) * 32 + lane, hrow = tile * kTileRows + row;
     const float qscale = fabsf(p.qscale);  // its sign goes to the scores
-    constexpr int kMine = kKeys / 2;       // keys of this thread's half
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's TMEM rows
-    const uint32_t o_addr = tmem + 256 + tile * 128 + half * (D / 2) + lanes;
-    const int pair = tile * 4 + (warp & 3);  // the two warps of the same rows
+    const uint32_t o_addr = tmem + 256 + tile * 128 + half * (D / kShare) + lanes;
+    const int pair = tile * 4 + (warp & 3);  // the warps of the same rows
     const int HQ = p.H * G;
     const int t_row = row / G, g_row = row - t_row * G;  // token and head of this row in its tile
     const bool neg = p.qscale < 0.f;
     const bool sectors = ((reinterpret_cast<uintptr_t>(p.o) | (uintptr_t)p.o_stride * 2) & 31) == 0;
     int step = 0, items = 0;  // steps and items of this row tile so far
     bool ok = true;
-    // The exchange of a step.  With one row tile the next step may begin while the other
-    // thread still reads: two places in turn.  With two it begins with scores that wait
-    // for both threads' weights.
+    // The exchange of a step.  With one row tile the next step may begin while another
+    // thread still reads: two places in turn, or, with four threads, a barrier before it.  With two
+    // tiles it begins with scores that wait for both threads' weights.
     auto told = [&](int s, int which) -> float& {
       return S.half[C::kTiles == 2 ? which * (2 * kTileRows) + hrow
-                                   : (s & 1) * (2 * kTileRows) + which * kTileRows + row];
+                                   : (kShare == 2 ? (s & 1) * (2 * kTileRows) : 0) + which * kTileRows + row];
     };
+    auto meet = [&] { named_barrier(1 + pair, 32 * kShare); };
     for (int k = 0;; ++k) {
       Item it;
       it.id = -1;
       ok = ok && next_item(k, it);
-      // a wait that ran out ends both warps of a pair at the same place
-      if (lane == 0) S.fine[k & 1][pair][half] = ok;
-      named_barrier(1 + pair, 64);
-      if (!ok || !S.fine[k & 1][pair][half ^ 1] || it.id < 0) break;
+      // a wait that ran out ends all warps of the same rows at the same place
+      if (lane == 0) S.fine[k & 1][warp] = ok;
+      meet();
+#pragma unroll
+      for (int y = 0; y < kShare; ++y) ok = ok && S.fine[k & 1][warp - 4 * half + 4 * y];
+      if (!ok || it.id < 0) break;
       if (tile * per_tile >= it.tokens) continue;  // no rows in this tile
       const bool live = t_row < per_tile && tile * per_tile + t_row < it.tokens;
       const int token = it.first + tile * per_tile + t_row, head = it.h * G + g_row;
@@ -855,8 +875,9 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
           const int32_t e = it.page_of_lane(n, lane, pg) ? table[pg] : -1;
           pages_ok = __ballot_sync(0xffffffffu, e >= 0 && e < p.kv_slots);
         }
-        const int k0 = (it.page(n) + half) * kPageTokens;
-        const bool there = pages_ok >> (2 * (n & 15) + half) & 1;
+        const int page = half * kMine / kPageTokens;  // of the tile's two
+        const int k0 = it.page(n) * kPageTokens + half * kMine;
+        const bool there = pages_ok >> (2 * (n & 15) + page) & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[buf], parity, p.status, p.wait_ns)) != 0;
         tc_fence_after();
         const uint32_t s_addr = tmem + buf * kKeys + half * kMine + lanes;
@@ -870,31 +891,50 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
           tc_ld32(x, s_addr + c);
           tc_wait_ld();
           tc_loaded(x);
-          if (!plain) {
+          if (kSpan != kWholeHistory && !plain) {
+            // a bit for each of them that is seen
+            uint32_t bits = below(hi - c);
+            if (kSpan == kWindowed) bits &= ~below(lo - c) | below(first - c);
+            if (!there) bits = 0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1 ? (neg ? -x[e] : x[e]) : kNone;
+          } else if (!plain) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               x[e] = neg ? -x[e] : x[e];
-              if ((c + e < lo && !(kSpan == kWindowed && c + e < first)) || c + e >= hi || !there) x[e] = kNone;
+              if (c + e < lo || c + e >= hi || !there) x[e] = kNone;
             }
           }
         };
         float top[4] = {kNone, kNone, kNone, kNone};
+        float kept[32];  // four threads have no more than these scores
 #pragma unroll (C::kTiles == 2 ? 2 : 1)
         for (int c = 0; c < kMine; c += 32) {
           float x[32];
           scores(x, c);
+          if (kShare == 4)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) kept[e] = x[e];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) top[e >> 1 & 3] = fmaxf(fmaxf(top[e >> 1 & 3], x[e]), x[e + 1]);
         }
         // the row's other half; both then take the same decisions (a wait that ran out
         // is told as NaN, which no maximum is)
         const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (kShare == 4) meet();
         told(step, half) = ok ? mine : __int_as_float(0x7fffffff);
-        named_barrier(1 + pair, 64);
-        const float other = told(step, half ^ 1);
-        ok = ok && !__any_sync(0xffffffffu, other != other);
+        meet();
+        float most = mine;
+        bool all_fine = true;
+#pragma unroll
+        for (int y = 1; y < kShare; ++y) {
+          const float other = told(step, half ^ y);
+          all_fine = all_fine && other == other;
+          most = fmaxf(most, other);
+        }
+        ok = ok && __all_sync(0xffffffffu, all_fine);
         if (!ok) break;
-        const float mt = fmaxf(mine, other) * qscale;
+        const float mt = most * qscale;
         const bool grow = mt - m > kLift<T> + kSlack<T>;  // not where both are -inf
         if (__any_sync(0xffffffffu, grow)) {
           const float to = mt - kLift<T>, f = !grow ? 1.f : far_off<T>(m) ? __int_as_float(0x7fffffff) : ex2(m - to);
@@ -907,7 +947,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
             if (C::kTiles == 1) done = __all_sync(0xffffffffu, mbar_wait(&S.pv_done, (step - 1) & 1, p.status, p.wait_ns)) != 0;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 2 && done; c += 32) {
+            for (int c = 0; c < D / kShare && done; c += 32) {
               float o[32];
               tc_ld32(o, o_addr + c);
               tc_wait_ld();
@@ -926,7 +966,11 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         for (int c = 0; c < kMine; c += 32) {
           float x[32];
           uint32_t w[16];
-          scores(x, c);
+          if (kShare == 4)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = kept[e];
+          else
+            scores(x, c);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float2 v = unpair(fma2(::tpk::pair(x[e], x[e + 1]), q2, ref2));
@@ -938,7 +982,8 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
           tc_st16(s_addr + (c >> 1), w);  // over scores of this half already used
           tc_wait_st();
           tc_fence_before();
-          mbar_arrive(c == 0 ? &S.p_half[buf] : &S.p_full[buf]);
+          // (a row's pieces: two of two halves, or one of each quarter)
+          mbar_arrive((kShare == 2 ? c == 0 : half % 2 == 0) ? &S.p_half[buf] : &S.p_full[buf]);
         }
         const float2 both = unpair(add2(sum[0], sum[1]));
         l += both.x + both.y;
@@ -946,10 +991,16 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
       if (!ok) continue;
       // ---- the rows' results
       if (nk > 0) {
-        named_barrier(1 + pair, 64);
+        meet();
         told(0, half) = l;
-        named_barrier(1 + pair, 64);
-        l += told(0, half ^ 1);
+        meet();
+        if (kShare == 2) {
+          l += told(0, half ^ 1);
+        } else {  // one order of sums for all of a row's threads
+          l = 0.f;
+#pragma unroll
+          for (int y = 0; y < kShare; ++y) l += told(0, y);
+        }
         if (far_off<T>(m)) l = __int_as_float(0x7fffffff);
         ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[tile], items++ & 1, p.status, p.wait_ns)) != 0;
         tc_fence_after();
@@ -970,14 +1021,14 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
         }
       }
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += 32) {
+      for (int c = 0; c < D / kShare; c += 32) {
         float o[32];
         __syncwarp();
         if (nk > 0) {
           tc_ld32(o, o_addr + c);
           tc_wait_ld();
           tc_loaded(o);
-          if (c + 32 == D / 2) {
+          if (c + 32 == D / kShare) {
             tc_fence_before();
             mbar_arrive(&S.o_empty[tile]);
           }
@@ -985,7 +1036,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        const int ch = half * (D / 2) + c;
+        const int ch = half * (D / kShare) + c;
         if (write && partial) {
           float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + ch);
 #pragma unroll
@@ -1027,7 +1078,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT>::kThreads, 1)
 constexpr int kJoined = 4;
 template <typename T, int D, int kT>
 __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ PagedParams p, int splits) {
-  using C = TileCfg<D, kT>;
+  using C = TileCfg<D, kT, 2>;
   const int lane = threadIdx.x & 31, per_tile = kTileRows / p.G;
   // 32 bits do: keys are split only where all items together are at most kTileBlocks
   const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -1087,7 +1138,7 @@ int device_sms();
 
 template <typename T, int D, int kT, int kSpan>
 cudaError_t launch_tiles(const PagedParams& p, int groups, int splits, cudaStream_t stream) {
-  using C = TileCfg<D, kT>;
+  using C = TileCfg<D, kT, kRowThreads<D, kT, kSpan>>;
   static DeviceOnce once;
   cudaError_t e = once.run([] {
     return cudaFuncSetAttribute(tile_kernel<T, D, kT, kSpan>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
