@@ -33,8 +33,9 @@
 // order.  Bound: the tensor cores (4 D operations per score); for D = 64 the exponentials, for
 // D = 256 the arrival of keys and values (128 rows use 128 KB in 2,048 matrix cycles).
 //
-// Through windows (kWindowed) the key tiles are those of the first tokens, if the group's windows
-// leave a gap behind them, then those from its first query's window on.
+// Through windows (kWindowed) an item's pages are those of the first tokens, then, behind a gap,
+// those from its first query's window on; a key tile is any two that follow each other in that list,
+// so that a few first tokens share a tile with the window's start.
 //
 // Measured: two requests of 4,096 tokens, 8,192 states, 8 x 4 heads: 922, 1,546 and 1,332
 // TFLOP/s at D = 64, 128, 256; eight requests of 300 to 1,500 tokens, 1,601 to 6,404
@@ -88,51 +89,34 @@ struct TileCfg {
   static constexpr int kThreads = (kQuery + 1 + kTwoLoaders) * 32;
 };
 
-// Windowed: the position of the first query token; key tiles [0, sinks) are those of the first
-// pages, from sink_page on, up to sink_end; 16-token groups of the last of them.
+// Windowed: the position of the first query token; pages [0, sinks) of the item's list are the table
+// row's first ones, the others `skip` further on; this part's tiles begin at page `from` of the list.
 template <int kSpan>
-struct SinkTiles {};
+struct SinkPages {};
 template <>
-struct SinkTiles<kWindowed> {
-  int pos, sinks, sink_page, sink_end, sink_last;
+struct SinkPages<kWindowed> {
+  int pos, sinks, skip, from;
 };
 
 // One tile group of one (request, KV head), or one part of its keys.
 template <int kSpan>
-struct Item : SinkTiles<kSpan> {
+struct Item : SinkPages<kSpan> {
   int id;       // its block number; -1: no more
   int first;    // its first query token
   int tokens;   // and how many of them it has: `per_tile` fill a row tile
   int h, len, b;
-  int page0, page_end, nk;  // key tiles [0, nk) begin at page page0
+  int page0, page_end, nk;  // key tiles [0, nk) begin at page page0 (windowed: of page_end in the list)
   int last;     // 16-token groups of the last key tile that hold any token
 
-  // first page of key tile j, and the page where its stretch of pages ends
-  __device__ __forceinline__ int page(int j) const {
-    if constexpr (kSpan == kWindowed)
-      if (j < this->sinks) return this->sink_page + 2 * j; else return page0 + 2 * (j - this->sinks);
-    else
-      return page0 + 2 * j;
-  }
-  __device__ __forceinline__ int end(int j) const {
-    if constexpr (kSpan == kWindowed)
-      if (j < this->sinks) return this->sink_end;
-    return page_end;
-  }
-  // the page of lane i of a warp that holds those of key tiles j, j + 1, ...; false past the last
-  __device__ __forceinline__ bool page_of_lane(int j, int i, int& pg) const {
+  // page e (0, 1) of key tile j; false: there is none
+  __device__ __forceinline__ bool page(int j, int e, int& pg) const {
     if constexpr (kSpan == kWindowed) {
-      pg = page(j + (i >> 1)) + (i & 1);
-      return pg < end(j + (i >> 1));
+      const int i = this->from + 2 * j + e;
+      pg = i < this->sinks ? i : i + this->skip;
+      return i < page_end;
     }
-    pg = page0 + 2 * j + i;
+    pg = page0 + 2 * j + e;
     return pg < page_end;
-  }
-  // 16-token groups of key tile j that hold any token
-  __device__ __forceinline__ int groups(int j) const {
-    if constexpr (kSpan == kWindowed)
-      if (j + 1 == this->sinks) return this->sink_last;
-    return j + 1 < nk ? 8 : last;
   }
 };
 
@@ -461,20 +445,23 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
     if (j >> 4 > w.window) {
       w.window = j >> 4;
       int pg;
-      w.entry = it.page_of_lane(16 * w.window, lane, pg) ? p.table[(int64_t)it.b * p.max_pages + pg] : -1;
+      w.entry = it.page(16 * w.window, lane, pg) ? p.table[(int64_t)it.b * p.max_pages + pg] : -1;
     }
     const int slot0 = __shfl_sync(0xffffffffu, w.entry, 2 * j & 31);
     const int slot1 = __shfl_sync(0xffffffffu, w.entry, (2 * j & 31) + 1);
     const unsigned n_slots = (unsigned)p.kv_slots;
     const bool there0 = (unsigned)slot0 < n_slots, there1 = (unsigned)slot1 < n_slots;
     const int n = there0 + there1;
-    const bool second = it.page(j) + 1 < it.end(j);  // the tile has a second page
-    const int tok0 = it.page(j) * kPageTokens;
+    int page0, page1;
+    it.page(j, 0, page0);
+    const bool second = it.page(j, 1, page1);  // the tile has a second page
+    // rows of the tile that hold tokens: it is all of them, but for the request's end
+    const int filled = !second || kSpan != kWindowed ? it.len - page0 * kPageTokens : kPageTokens + it.len - page1 * kPageTokens;
     const bool bad = !there0 || (!there1 && second);
     if (bad && lane == 0) atomicOr(p.status, kStatusBadSlot);
     // values whose weight is 0 must not be NaN: rows past the last token in its 16-token
     // group (later groups are not multiplied), and pages not there
-    const bool clear = values && (bad || (it.len - tok0 < kKeys && (it.len & 15)));
+    const bool clear = values && (bad || (filled < (second || kSpan != kWindowed ? kKeys : kPageTokens) && (it.len & 15)));
     const int y0 = (slot0 * p.H + it.h) * kPageTokens, y1 = (slot1 * p.H + it.h) * kPageTokens;
     const CUtensorMap* map = values ? &p.vmap : &p.kmap;
 #pragma unroll
@@ -500,7 +487,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
         wait(&S.tail, tails++);
         constexpr int kPieces = C::kSlotChannels / 8;
         const int piece = lane % kPieces;
-        const int end = min(kKeys, max(0, it.len - tok0));  // rows that hold tokens
+        const int end = min(kKeys, max(0, filled));
         const int last = bad ? kKeys : (end + 15) & ~15;
         for (int r = bad ? lane / kPieces : end + lane / kPieces; r < last; r += 32 / kPieces)
           if (r >= end || !(r < kPageTokens ? there0 : there1))
@@ -623,11 +610,11 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
             const bool more = j + 1 < nk;
             if (more) ka = take();
             if (!ok) break;
-            pv(0, 0, va, j > 0, !two, it.groups(j));
+            pv(0, 0, va, j > 0, !two, j + 1 < nk ? 8 : it.last);
             if (!ok) break;
             if (more) qk(0, 0, ka, !two); else tc_commit(o_full);
             if (two) {
-              pv(1, 1, va, j > 0, true, it.groups(j));
+              pv(1, 1, va, j > 0, true, j + 1 < nk ? 8 : it.last);
               if (!ok) break;
               if (more) qk(1, 1, ka, true); else tc_commit(o_full + 8);
             }
@@ -647,7 +634,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
             const bool more = j + 2 < nk;
             if (more) ka = take();
             if (!ok) break;
-            pv(0, b0 ^ (j & 1), va, j > 0, true, it.groups(j));
+            pv(0, b0 ^ (j & 1), va, j > 0, true, j + 1 < nk ? 8 : it.last);
             if (!ok) break;
             tc_commit(pv_done);
             if (j + 1 == nk) tc_commit(o_full);
@@ -716,31 +703,33 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
           clo = __reduce_min_sync(0xffffffffu, clo);
           chi = __reduce_max_sync(0xffffffffu, chi);
         }
-        int sinks = 0;  // key tiles of the first tokens
         if constexpr (kSpan == kWindowed) {
           chi = max(min(it.len, it.pos + it.tokens), 0);
           clo = min(max(max(it.pos + 1, 0) - p.window, 0), chi);
         }
         it.page0 = chi > clo ? clo >> 6 : 0;
         it.page_end = (chi + 63) >> 6;
+        int pages = chi > clo ? it.page_end - it.page0 : 0;
         if constexpr (kSpan == kWindowed) {
-          const int tokens = min(p.sinks, clo);
-          it.sink_end = (tokens + 63) >> 6;
-          if (it.sink_end >= it.page0) it.page0 = it.sink_end = 0;  // no page lies between
-          sinks = (it.sink_end + 1) >> 1;
-          it.sink_last = min(8, (tokens - 2 * (sinks - 1) * kPageTokens + 15) >> 4);
+          it.sinks = min((min(p.sinks, clo) + 63) >> 6, it.page0);
+          it.skip = it.page0 - it.sinks;
+          if (pages > 0) pages += it.sinks;
         }
-        const int nk = chi > clo ? sinks + ((it.page_end - it.page0 + 1) >> 1) : 0;
+        const int nk = (pages + 1) >> 1;
         const int k0 = (int)((unsigned)nk * (unsigned)part / (unsigned)splits);  // splits <= kTileBlocks, nk < 2^24
         const int k1 = (int)((unsigned)nk * (unsigned)(part + 1) / (unsigned)splits);
-        it.page0 += 2 * max(k0 - sinks, 0);
         it.nk = k1 - k0;
         if constexpr (kSpan == kWindowed) {
-          it.sink_page = 2 * k0;
-          it.sinks = max(min(k1, sinks) - k0, 0);
-          if (k1 < sinks) it.sink_last = 8;  // the last of them is in a later part
+          it.from = 2 * k0;
+          it.page_end = pages;
+          int page0, page1;
+          it.page(it.nk - 1, 0, page0);
+          const bool second = it.page(it.nk - 1, 1, page1);
+          it.last = (second ? 4 : 0) + ((min(it.len - (second ? page1 : page0) * kPageTokens, kPageTokens) + 15) >> 4);
+        } else {
+          it.page0 += 2 * k0;
+          it.last = min(8, (min(it.len, it.page_end * kPageTokens) - (it.page0 + 2 * (it.nk - 1)) * kPageTokens + 15) >> 4);
         }
-        it.last = min(8, (min(it.len, it.page_end * kPageTokens) - it.page(it.nk - 1) * kPageTokens + 15) >> 4);
         if (k >= 2) wait(&S.item_empty[k & 1], (k >> 1) - 1);
         if (ok && lane == 0) {
           S.item[k & 1] = it;
@@ -872,12 +861,14 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
         const int buf = C::kTiles == 2 ? tile : step & 1, parity = (C::kTiles == 2 ? step : step >> 1) & 1;
         if ((n & 15) == 0) {
           int pg;
-          const int32_t e = it.page_of_lane(n, lane, pg) ? table[pg] : -1;
+          const int32_t e = it.page(n, lane, pg) ? table[pg] : -1;
           pages_ok = __ballot_sync(0xffffffffu, e >= 0 && e < p.kv_slots);
         }
-        const int page = half * kMine / kPageTokens;  // of the tile's two
-        const int k0 = it.page(n) * kPageTokens + half * kMine;
-        const bool there = pages_ok >> (2 * (n & 15) + page) & 1;
+        const int which = half * kMine / kPageTokens;  // of the tile's pages
+        int page;
+        it.page(n, which, page);
+        const int k0 = page * kPageTokens + half * kMine % kPageTokens;
+        const bool there = pages_ok >> (2 * (n & 15) + which) & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[buf], parity, p.status, p.wait_ns)) != 0;
         tc_fence_after();
         const uint32_t s_addr = tmem + buf * kKeys + half * kMine + lanes;
