@@ -20,13 +20,21 @@ def workspace(kv_slots, n):
     return torch.randint(0, 255, (size,), dtype=torch.uint8, device="cuda"), size
 
 
+# A small pool and table go to one block; the same rows in a wide table, or a pool with more slots, to a cluster
+WIDE = 40000
+
+
 def check_rows(got, before, rows):
     for b, row in enumerate(rows):
         assert got[b].tolist() == row + before[b][len(row):].tolist(), f"row {b}"
 
 
-def fork(source, lens, keep, table, shares, free, n_free, in_place=False, stream=None, graph=False):
+def fork(source, lens, keep, table, shares, free, n_free, in_place=False, stream=None, graph=False, wide=None):
+    if wide is None and len(shares) < 100:  # both forms
+        fork(source, lens, keep, table, shares, free, n_free, in_place, stream, graph, wide=True)
     n, max_pages, slots = len(lens), len(table[0]), len(shares)
+    if wide:  # slots past those of the case: held by nobody here
+        shares, slots = shares + [0] * (9000 - slots), 9000
     want = fork_model(source, lens, keep, table, shares, free, n_free, slots)
     d = {k: i32(v) for k, v in dict(source=source, lens=lens, table=table, shares=shares, free=free, n_free=[n_free]).items()}
     dk = None if keep is None else i32(keep)
@@ -165,7 +173,9 @@ def test_other_stream_and_captured():
     fork(*args, graph=True)
 
 
-def compact(lens, table, shares, free, n_free, max_copies, in_place=False):
+def compact(lens, table, shares, free, n_free, max_copies, in_place=False, wide=None):
+    if wide is None and len(shares) < 100 and all(0 <= n <= 64 * len(table[0]) for n in lens):  # both forms
+        compact(lens, [r + [-1] * (-(-WIDE // len(lens)) - len(r)) for r in table], shares, free, n_free, max_copies, in_place, wide=True)
     n, max_pages, slots = len(lens), len(table[0]), len(shares)
     want = compact_model(lens, table, shares, free, n_free, slots, max_copies)
     d = {k: i32(v) for k, v in dict(lens=lens, table=table, shares=shares, n_free=[n_free]).items()}

@@ -2,12 +2,13 @@
 // copies that these ask for.
 //
 // Forks and compaction are bookkeeping on whole numbers: a few bytes for each page-table entry
-// and each slot, in phases that each need all of the phase before.  Each call is one launch of one
-// cluster of kParts blocks, whose barrier separates the phases: a batch of 64 beams or a pool of
-// ten thousand slots is bound by the latency of its phases, not by what eight SMs can read, and a
-// barrier of a cluster costs less than a launch.  Sums and counts go by integer atomics, which
-// give the same in any order; ranks go by scans, so that the result is the one that the
-// definition's order gives.
+// and each slot, in phases that each need all of the phase before.  A small pool and table go to one
+// block, which keeps what it counts in shared memory (a beam step of 64 rows, 367 slots: 11.3 us
+// as a cluster, 6.6 so; compaction of 900 slots 12.6 and 5.1).  Others go to one cluster of kParts
+// blocks, whose barrier separates the phases: they are bound by the latency of their phases, not
+// by what eight SMs can read, and a barrier of a cluster costs less than a launch.  Sums and counts
+// go by integer atomics, which give the same in any order; ranks go by scans, so that the result
+// is the one that the definition's order gives.
 //
 // Bound: latency for those two, HBM for the copies (two bytes moved for each byte of a page).
 #include <climits>
@@ -19,16 +20,27 @@ namespace tpk {
 constexpr int kParts = 8;  // blocks of the cluster (as many as every device takes)
 constexpr int kPartThreads = 1024;
 constexpr int kPartWarps = kPartThreads / 32;
+constexpr int kLocalSlots = 8192, kLocalEntries = 32768;  // of a pool, and of a table, that one block takes
 
-// All blocks of the cluster have come here, and see what the others wrote before.
-__device__ __forceinline__ void parts_meet() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ int my_part() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return (int)r;
-}
+// What differs between one block and a cluster.  Arrays that the threads share lie in shared memory,
+// or in global memory, where what another block wrote must not come from this SM's L1.
+template <bool kLocal>
+struct Team {
+  static constexpr int parts = kLocal ? 1 : kParts;
+  // All threads have come here, and see what the others wrote before.
+  static __device__ __forceinline__ void meet() {
+    if (kLocal)
+      __syncthreads();
+    else
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  static __device__ __forceinline__ int get(const int32_t* p) { return kLocal ? *p : __ldcg(p); }
+  static __device__ __forceinline__ int part() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return kLocal ? 0 : (int)r;
+  }
+};
 __device__ __forceinline__ int pages_of(int tokens) { return (tokens >> 6) + ((tokens & 63) != 0); }
 
 // How many of the block's threads below this one have the flag, and how many in all.
@@ -52,18 +64,41 @@ __device__ __forceinline__ int rank_in_block(bool flag, int* warp_counts, int& t
 // The slots, cut into equal stretches for the parts; within a stretch tiles of a block's width.
 struct Stretch {
   int begin, end;
-  __device__ __forceinline__ Stretch(int n, int part) {
-    const int per = (int)(((int64_t)n + kParts - 1) / kParts);
+  __device__ __forceinline__ Stretch(int n, int part, int parts) {
+    const int per = (int)(((int64_t)n + parts - 1) / parts);
     begin = (int)min((int64_t)per * part, (int64_t)n);
     end = min(begin + per, n);
   }
 };
 
-// Counts of all parts, in global memory: what each part adds up before a barrier.
-__device__ __forceinline__ int before_part(const int* counts, int part) {
-  int sum = 0;
-  for (int i = 0; i < part; ++i) sum += __ldcg(counts + i);
-  return sum;
+// How many slots of the stretches before and behind this part's have the flag, and how many in all.
+// For all threads; the parts meet in it.
+template <bool kLocal, typename F>
+__device__ __forceinline__ void count_flags(const Stretch& mine, int part, int* warp_counts, int32_t* counts, F flag, int& before,
+                                            int& behind, int& all) {
+  int count = 0;
+  for (int i = mine.begin + (int)threadIdx.x; i < mine.end; i += kPartThreads) count += flag(i);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) count += __shfl_xor_sync(0xffffffffu, count, d);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warp_counts[threadIdx.x >> 5] = count;
+  __syncthreads();
+  int sum = warp_counts[threadIdx.x & 31];
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  before = behind = 0;
+  all = sum;
+  if (kLocal) return;
+  if (threadIdx.x == 0) counts[part] = sum;
+  Team<kLocal>::meet();
+  all = 0;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    const int n = __ldcg(counts + i);
+    all += n;
+    if (i < part) before += n;
+    if (i > part) behind += n;
+  }
 }
 
 // ------------------------------------------------------------------- fork
@@ -78,14 +113,24 @@ struct ForkShared {
   int counts[kPartWarps];
   int source[kMostReq];  // whose table row the request's pages come from
   int keep[kMostReq];    // tokens it keeps
+  int page[kMostReq];    // its open page
   int fresh[kMostReq];   // the slot of its copied page; -1: none; -2: nothing to do, -3: refused
 };
 constexpr int kNone = -1, kSame = -2, kRefused = -3;
 
+template <bool kLocal>
 __global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams p) {
+  using Team = ::tpk::Team<kLocal>;
   extern __shared__ __align__(16) uint8_t raw[];
   ForkShared& S = *reinterpret_cast<ForkShared*>(raw);
-  const int tid = threadIdx.x, part = my_part(), n = p.n_req;
+  int32_t* const local = reinterpret_cast<int32_t*>(raw + sizeof(ForkShared));
+  // of each slot: its holders but one, the requests whose open page it is, the first of these; and the
+  // slots that nobody holds any more
+  int32_t* const shares = kLocal ? local : p.shares_out;
+  int32_t* const open = kLocal ? local + p.kv_slots : p.open;
+  int32_t* const first = kLocal ? local + 2 * p.kv_slots : p.first;
+  int32_t* const pushed = kLocal ? local + 3 * p.kv_slots : p.pushed;
+  const int tid = threadIdx.x, part = Team::part(), n = p.n_req;
   const int lane = tid & 31, warp = part * kPartWarps + (tid >> 5);
   wait_before();
   const int cap = (int)min((int64_t)p.max_pages * kPageTokens, (int64_t)INT_MAX);
@@ -96,6 +141,12 @@ __global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams 
     return c;
   };
   const int n_free = min(max(*p.n_free_in, 0), p.free_cap);
+  const Stretch mine(p.kv_slots, part, Team::parts);
+  for (int i = mine.begin + tid; i < mine.end; i += kPartThreads) {
+    if (kLocal || p.shares_in != p.shares_out) shares[i] = p.shares_in[i];
+    open[i] = 0;
+    first[i] = INT_MAX;
+  }
   // ---- what each request asks for (every part for itself)
   for (int b = tid; b < n; b += kPartThreads) {
     const int own = length(b);
@@ -105,8 +156,8 @@ __global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams 
     } else if (s < 0 || s >= n) {
       state = kRefused;
     } else {
-      const int len = length(s);
-      keep = p.len_keep ? p.len_keep[b] : len;
+      const int asked = p.len_keep ? p.len_keep[b] : INT_MAX, len = length(s);
+      keep = p.len_keep ? asked : len;
       if (keep < 0 || keep > len) state = kRefused;
     }
     if (state == kRefused) {
@@ -118,18 +169,13 @@ __global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams 
     S.source[b] = s;
     S.keep[b] = keep;
     S.fresh[b] = state;
-  }
-  const Stretch mine(p.kv_slots, part);
-  for (int i = mine.begin + tid; i < mine.end; i += kPartThreads) {
-    if (p.shares_in != p.shares_out) p.shares_out[i] = p.shares_in[i];
-    p.open[i] = 0;
-    p.first[i] = INT_MAX;
+    S.page[b] = state == kNone && (keep & 63) ? p.table_in[(int64_t)s * p.max_pages + (keep >> 6)] : -1;
   }
   __syncthreads();
-  parts_meet();
+  Team::meet();
 
   // ---- holders: some warps to a request, or some requests to a warp
-  const int warps = kParts * kPartWarps, team = max(1, warps / n);
+  const int warps = Team::parts * kPartWarps, team = max(1, warps / n);
   auto valid = [&](int x) {
     const bool ok = x >= 0 && x < p.kv_slots;
     bad |= !ok;
@@ -143,51 +189,38 @@ __global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams 
     for (int j = (warp % team) * 32 + lane; j < max(lost, kept); j += team * 32) {
       const int x = j < lost ? own[j] : -1, y = j < kept ? from[j] : -1;
       if (j < lost && j < kept && x == y) continue;
-      if (j < lost && valid(x)) atomicSub(p.shares_out + x, 1);
-      if (j < kept && valid(y)) atomicAdd(p.shares_out + y, 1);
+      if (j < lost && valid(x)) atomicSub(shares + x, 1);
+      if (j < kept && valid(y)) atomicAdd(shares + y, 1);
     }
-    if (warp % team == 0 && lane == 0 && (S.keep[b] & 63)) {
-      const int x = from[kept];
-      if (valid(x)) {
-        atomicAdd(p.open + x, 1);
-        atomicMin(p.first + x, b);
-      }
+    if (warp % team == 0 && lane == 0 && (S.keep[b] & 63) && valid(S.page[b])) {
+      atomicAdd(open + S.page[b], 1);
+      atomicMin(first + S.page[b], b);
     }
   }
-  parts_meet();
+  Team::meet();
 
   // ---- slots: who keeps an open page, and which pages nobody holds
-  auto freed = [&](int i) { return __ldcg(p.shares_out + i) < 0 && __ldcg(p.open + i) == 0; };
-  int count = 0;
-  for (int i = mine.begin + tid; i < mine.end; i += kPartThreads) count += freed(i);
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) count += __shfl_xor_sync(0xffffffffu, count, d);
-  if (lane == 0) S.counts[tid >> 5] = count;
-  __syncthreads();
-  if (tid < 32) {
-    int sum = S.counts[tid];
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (tid == 0) p.counts[part] = sum;
-  }
-  parts_meet();
-  const int all = before_part(p.counts, kParts);
+  auto freed = [&](int i) { return Team::get(shares + i) < 0 && Team::get(open + i) == 0; };
+  int before, at, all;
+  if (!kLocal) count_flags<kLocal>(mine, part, S.counts, p.counts, freed, before, at, all);
+  if (kLocal) at = 0;
   // the highest is pushed first: those before are above
-  int at = all - before_part(p.counts, part + 1);
   for (int i0 = mine.end; i0 > mine.begin; i0 -= kPartThreads) {
     const int i = i0 - 1 - tid;
     const bool here = i >= mine.begin, gone = here && freed(i);
     int total;
     const int rank = rank_in_block(gone, S.counts, total);
-    if (gone) p.pushed[at + rank] = i;
+    if (gone) pushed[at + rank] = i;
     at += total;
     if (!here) continue;
-    const int base = __ldcg(p.shares_out + i) + 1;
+    const int base = Team::get(shares + i) + 1;
     bad |= base < 0;
-    if (base <= 0) p.shares_out[i] = 0;
-    else p.first[i] = -1;  // others hold it: nobody writes on
+    if (base <= 0) shares[i] = 0;
+    else first[i] = -1;  // others hold it: nobody writes on
+    if (kLocal) p.shares_out[i] = max(base - 1, 0);
   }
-  parts_meet();
+  if (kLocal) all = at;
+  Team::meet();
 
   // ---- new slots for the pages that are copied, in request order (every part for itself)
   const int there = min(n_free + all, p.free_cap);
@@ -197,8 +230,8 @@ __global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams 
     bool asks = false, lost = false;
     int x = -1;
     if (b < n && S.fresh[b] == kNone && (S.keep[b] & 63)) {
-      x = p.table_in[(int64_t)S.source[b] * p.max_pages + (S.keep[b] >> 6)];
-      if (valid(x)) asks = __ldcg(p.first + x) != b;
+      x = S.page[b];
+      if (valid(x)) asks = Team::get(first + x) != b;
       else lost = true;
     }
     int total;
@@ -207,7 +240,7 @@ __global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams 
     // the stack's entries that this call pushed are not in free_slots yet
     const int from = there - 1 - rank;
     int got = kNone;
-    if (asks && rank < there) got = from < n_free ? p.free_slots[from] : __ldcg(p.pushed + from - n_free);
+    if (asks && rank < there) got = from < n_free ? p.free_slots[from] : Team::get(pushed + from - n_free);
     lost |= asks && rank >= there;
     if (b >= n) continue;
     const bool copied = asks && !lost, refused = lost || S.fresh[b] == kRefused;
@@ -221,8 +254,8 @@ __global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams 
     }
   }
   const int left = there - min(taken, there);
-  for (int i = n_free + part * kPartThreads + tid; i < left; i += kParts * kPartThreads)
-    p.free_slots[i] = __ldcg(p.pushed + i - n_free);
+  for (int i = n_free + part * kPartThreads + tid; i < left; i += Team::parts * kPartThreads)
+    p.free_slots[i] = Team::get(pushed + i - n_free);
   if (part == 0 && tid == 0) {
     *p.n_free_out = left;
     bad |= n_free + all > p.free_cap;
@@ -245,88 +278,84 @@ __global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams 
 // and r is below max_copies.  Then the stack holds the free slots, the lowest on top.
 constexpr int kHeld = 0, kFree = 1, kTaken = 2;  // marks: in use, free, free and taken by a page
 
+template <bool kLocal>
 __global__ void __launch_bounds__(kPartThreads, 1) compact_kernel(const CompactParams p) {
+  using Team = ::tpk::Team<kLocal>;
+  extern __shared__ __align__(16) uint8_t raw[];
+  int32_t* const local = reinterpret_cast<int32_t*>(raw);
   __shared__ int counts[kPartWarps];
-  const int tid = threadIdx.x, lane = tid & 31, part = my_part(), slots = p.kv_slots;
-  const int step = kParts * kPartThreads, thread = part * kPartThreads + tid;
+  // of each slot: its mark, and where its page goes
+  int32_t* const mark = kLocal ? local : p.mark;
+  int32_t* const moved = kLocal ? local + p.kv_slots : p.new_slot;
+  // the lists of the moves
+  int32_t* const src = kLocal ? local + 2 * p.kv_slots : p.copy_src;
+  int32_t* const dst = kLocal ? local + 3 * p.kv_slots : p.copy_dst;
+  const int tid = threadIdx.x, lane = tid & 31, part = Team::part(), slots = p.kv_slots;
+  const int step = Team::parts * kPartThreads, thread = part * kPartThreads + tid;
   wait_before();
   const int n_free = min(max(*p.n_free_in, 0), p.free_cap);
   bool bad = false;
-  for (int i = thread; i < slots; i += step) p.mark[i] = kHeld;
-  for (int i = thread; i < p.max_copies; i += step) p.copy_src[i] = p.copy_dst[i] = -1;
-  parts_meet();
+  for (int i = thread; i < slots; i += step) mark[i] = kHeld;
+  for (int i = thread; i < p.max_copies; i += step) src[i] = dst[i] = -1;
+  Team::meet();
   for (int i = thread; i < n_free; i += step) {
     const int x = p.free_in[i];
-    if (x >= 0 && x < slots) p.mark[x] = kFree; else bad = true;
+    if (x >= 0 && x < slots) mark[x] = kFree; else bad = true;
   }
-  parts_meet();
+  Team::meet();
 
   // ---- both lists: free slots from the bottom, slots in use from the top
-  const Stretch mine(slots, part);
-  auto add_up = [&](int count, int* to) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) count += __shfl_xor_sync(0xffffffffu, count, d);
-    __syncthreads();
-    if (lane == 0) counts[tid >> 5] = count;
-    __syncthreads();
-    if (tid < 32) {
-      int sum = counts[tid];
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (tid == 0) to[part] = sum;
-    }
-  };
-  int count = 0;
-  for (int i = mine.begin + tid; i < mine.end; i += kPartThreads) count += __ldcg(p.mark + i) == kFree;
-  add_up(count, p.counts);
-  parts_meet();
-  const int all_free = before_part(p.counts, kParts), held = slots - all_free;
-  int low = before_part(p.counts, part);  // free slots below
+  const Stretch mine(slots, part, Team::parts);
+  int low, behind, all_free;  // free slots below this stretch, above it, in all
+  count_flags<kLocal>(mine, part, counts, p.counts, [&](int i) { return Team::get(mark + i) == kFree; }, low, behind, all_free);
+  const int held = slots - all_free;
   for (int i0 = mine.begin; i0 < mine.end; i0 += kPartThreads) {
     const int i = i0 + tid;
-    const bool here = i < mine.end, is_free = here && __ldcg(p.mark + i) == kFree;
+    const bool here = i < mine.end, is_free = here && Team::get(mark + i) == kFree;
     int total;
     const int below = low + rank_in_block(is_free, counts, total);
     low += total;
     if (!here) continue;
-    p.new_slot[i] = is_free ? -1 : i;
+    moved[i] = is_free ? -1 : i;
     const int above = held - (i - below) - 1;  // slots in use above this one
-    if (is_free && below < p.max_copies) p.copy_dst[below] = i;
-    if (!is_free && above < p.max_copies) p.copy_src[above] = i;
+    if (is_free && below < p.max_copies) dst[below] = i;
+    if (!is_free && above < p.max_copies) src[above] = i;
   }
-  parts_meet();
+  Team::meet();
 
   // ---- the moves: those of the front of both lists
   auto goes = [&](int r) {
-    const int s = __ldcg(p.copy_src + r), d = __ldcg(p.copy_dst + r);
+    const int s = Team::get(src + r), d = Team::get(dst + r);
     return d >= 0 && d < s;
   };
   if (thread == 0 && (p.max_copies == 0 || !goes(0))) *p.n_copies = 0;
   for (int r = thread; r < p.max_copies; r += step) {
-    if (goes(r)) {
-      const int s = __ldcg(p.copy_src + r), d = __ldcg(p.copy_dst + r);
-      p.new_slot[s] = d;
-      p.mark[d] = kTaken;
+    const bool go = goes(r);
+    if (go) {
+      const int s = Team::get(src + r), d = Team::get(dst + r);
+      moved[s] = d;
+      mark[d] = kTaken;
       // (an entry of the lists' rest is no move before and after it is cleared)
       if (r + 1 == p.max_copies || !goes(r + 1)) *p.n_copies = r + 1;
-    } else {
-      p.copy_src[r] = p.copy_dst[r] = -1;
+    } else if (!kLocal) {
+      src[r] = dst[r] = -1;
+    }
+    if (kLocal) {
+      p.copy_src[r] = go ? src[r] : -1;
+      p.copy_dst[r] = go ? dst[r] : -1;
     }
   }
-  parts_meet();
+  Team::meet();
 
   // ---- holders and the stack
   auto empty = [&](int i) {
-    const int m = __ldcg(p.mark + i);
-    return m == kFree || (m == kHeld && __ldcg(p.new_slot + i) != i);
+    const int m = Team::get(mark + i);
+    return m == kFree || (m == kHeld && Team::get(moved + i) != i);
   };
-  count = 0;
-  for (int i = mine.begin + tid; i < mine.end; i += kPartThreads) count += empty(i);
-  add_up(count, p.counts + kParts);
-  parts_meet();
-  const int left = before_part(p.counts + kParts, kParts);
-  int at = left - before_part(p.counts + kParts, part + 1);  // the highest at the bottom
-  for (int i0 = mine.end; i0 > mine.begin; i0 -= kPartThreads) {
+  int before, at, left;
+  if (!kLocal) count_flags<kLocal>(mine, part, counts, p.counts + kParts, empty, before, at, left);
+  if (kLocal) at = 0;
+  for (int i0 = mine.end; i0 > mine.begin; i0 -= kPartThreads) {  // the highest at the bottom
     const int i = i0 - 1 - tid;
     const bool here = i >= mine.begin, is_empty = here && empty(i);
     int total;
@@ -334,12 +363,14 @@ __global__ void __launch_bounds__(kPartThreads, 1) compact_kernel(const CompactP
     if (is_empty && at + rank < p.free_cap) p.free_out[at + rank] = i;
     at += total;
     if (!here) continue;
-    const int m = __ldcg(p.mark + i), to = __ldcg(p.new_slot + i);
+    const int m = Team::get(mark + i), to = Team::get(moved + i);
     // each slot in use brings its own holders along: no slot that is read here is written by another
     if (m == kHeld && to != i) p.shares_out[to] = p.shares_in[i];
     if (is_empty) p.shares_out[i] = 0;
     else if (m == kHeld && p.shares_in != p.shares_out) p.shares_out[i] = p.shares_in[i];
+    if (kLocal) p.new_slot[i] = to;
   }
+  if (kLocal) left = at;
   if (thread == 0) {
     *p.n_free_out = min(left, p.free_cap);
     bad |= left > p.free_cap;
@@ -353,7 +384,7 @@ __global__ void __launch_bounds__(kPartThreads, 1) compact_kernel(const CompactP
     bad |= v != c;
     const int64_t row = (int64_t)b * p.max_pages;
     for (int j = (warp % team) * 32 + lane; j < pages_of(c); j += team * 32) {
-      const int x = p.table_in[row + j], y = x >= 0 && x < slots ? __ldcg(p.new_slot + x) : -1;
+      const int x = p.table_in[row + j], y = x >= 0 && x < slots ? Team::get(moved + x) : -1;
       bad |= y < 0;  // out of the pool, or on the stack: left as it is
       p.table_out[row + j] = y < 0 ? x : y;
     }
@@ -425,9 +456,10 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
   }
 }
 
-// One cluster of kParts blocks.
-template <typename P>
-static cudaError_t launch_parts(void (*kernel)(P), size_t smem, cudaStream_t stream, const P& p) {
+// One block, or one cluster of kParts.
+template <bool kLocal, typename P>
+static cudaError_t launch_team(void (*kernel)(P), size_t smem, cudaStream_t stream, const P& p) {
+  if (kLocal) return launch_early(kernel, 1, kPartThreads, smem, stream, p);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -445,15 +477,35 @@ static cudaError_t launch_parts(void (*kernel)(P), size_t smem, cudaStream_t str
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Shared memory of one block's arrays: four words for each slot.
+static size_t local_bytes(int64_t slots) { return 4 * sizeof(int32_t) * slots; }
+static bool one_block(int n_req, int max_pages, int kv_slots) {
+  return kv_slots <= kLocalSlots && (int64_t)n_req * max_pages <= kLocalEntries;
+}
+
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
   static DeviceOnce once;
-  const cudaError_t e = once.run(
-      [] { return cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(ForkShared)); });
-  return e != cudaSuccess ? e : launch_parts(fork_kernel, sizeof(ForkShared), stream, p);
+  const cudaError_t e = once.run([] {
+    const cudaError_t x = cudaFuncSetAttribute(fork_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)(sizeof(ForkShared) + local_bytes(kLocalSlots)));
+    return x != cudaSuccess ? x : cudaFuncSetAttribute(fork_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (int)sizeof(ForkShared));
+  });
+  if (e != cudaSuccess) return e;
+  return one_block(p.n_req, p.max_pages, p.kv_slots)
+             ? launch_team<true>(fork_kernel<true>, sizeof(ForkShared) + local_bytes(p.kv_slots), stream, p)
+             : launch_team<false>(fork_kernel<false>, sizeof(ForkShared), stream, p);
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
-  return launch_parts(compact_kernel, 0, stream, p);
+  static DeviceOnce once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(compact_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)local_bytes(kLocalSlots));
+  });
+  if (e != cudaSuccess) return e;
+  return one_block(p.n_req, p.max_pages, p.kv_slots)
+             ? launch_team<true>(compact_kernel<true>, local_bytes(p.kv_slots), stream, p)
+             : launch_team<false>(compact_kernel<false>, 0, stream, p);
 }
 
 int device_sms();
