@@ -887,8 +887,12 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
             uint32_t bits = below(hi - c);
             if (kSpan == kWindowed) bits &= ~below(lo - c) | below(first - c);
             if (!there) bits = 0;
+            if (neg) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1 ? (neg ? -x[e] : x[e]) : kNone;
+              for (int e = 0; e < 32; ++e) x[e] = -x[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1 ? x[e] : kNone;
           } else if (!plain) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
