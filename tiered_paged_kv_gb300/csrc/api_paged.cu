@@ -378,7 +378,7 @@ SharedPlan shared_plan(const tpk_paged_shape* s, int n_req, int n_grp) {
   // six; twelve of 2,000 tokens: 82, 84, 93 and 106).
   const int64_t parts = n_grp == 1 ? kTileBlocks / items : (kSharedWaves * kTileBlocks + items - 1) / items;
   const int64_t splits = std::min({parts, ((int64_t)s->max_pages + 3) / 4, (int64_t)kSharedSplits});
-  return {tiles, n_req / per + n_grp, std::max<int64_t>(splits, 1)};
+  return {tiles, n_req / per + std::min(n_grp, n_req), std::max<int64_t>(splits, 1)};  // groups without requests have no tiles
 }
 
 // Whether prefixes and the rest go through one split launch, which reads a prefix once for every 16

@@ -5,9 +5,8 @@
 // as in kv_rope.cu.  A thread keeps one piece of every token's row: two chunks of 8 channels of one
 // head, chosen so that neighbouring threads have neighbouring chunks and both channels of a pair
 // are in one thread.  (Two chunks side by side instead, 7,001 tokens of 32 + 8 heads of 256: 77 us.)
-// The D / 16 threads of a head lie side by side in a warp, so the
-// sum of squares is a few shuffles over what they hold already, and each row is read and written
-// once.
+// The D / 16 threads of a head lie side by side in a warp, so the sum of squares is a few shuffles
+// over what they hold already, and each row is read and written once.
 //
 // Bound: HBM, (2 HQ + 4 H) D * 2 bytes per token.  A thread's work on a token is a chain (squares,
 // shuffles, root, products), and between its tokens little would be in flight: so the rows of all
@@ -16,15 +15,16 @@
 // loads into registers, one to four tokens ahead, the same prompt took 77 us and more.)  After
 // that instructions count: the two floats of a word run as one packed operation, and the shuffles
 // have their number and their lanes fixed at compile time.
-// Measured: 7,001 tokens of 32 + 8 heads of 256 (287 MB) 52.6 us, 5.5 TB/s; 48 tokens of 32 + 8
-// heads of 128 2.6 us.
+// Measured: 7,001 tokens of 32 + 8 heads of 256, half of each rotated (287 MB), 45.1 us, 6.4 TB/s;
+// 8,200 of 32 + 8 heads of 128 (202 MB) 36.5 us, 5.5 TB/s; 48 tokens 2.1 us.
 #include "rope.cuh"
 
 namespace tpk {
 
-// 7,001 tokens of 32 + 8 heads of 256: 256 threads and 4 tokens 56.4 us, 384 and 2 69.9, 384 and 4
-// 52.6, 384 and 6 55.6, 640 and 4 75.4
-constexpr int kNormThreads = 384;  // at most
+// 8,200 tokens of 32 + 8 heads of 128, 7,001 of 32 + 8 heads of 256: 256 threads 36.4 and 49.4 us, 320
+// 36.5 and 45.1, 512 38.4 and 45.0, 640 37.5 and 56.6 (equal passes of whole warps each).  Two tokens
+// a block took a third more time than four, six a twentieth more (in an earlier form).
+constexpr int kNormThreads = 320;  // at most
 constexpr int kNormTokens = 4;     // of a block, at most
 constexpr int kNormPairs = 1024;  // angles a block holds: tokens * rot / 2
 
@@ -108,6 +108,25 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
   const bool turned_a = normed && ca < p.rot, turned_b = normed && cb < p.rot;
   const int h = query ? head : key ? head - p.HQ : head - p.HQ - kheads;
   wait_before();
+  // What the angles and places are made of is asked for before the rows: behind them it would arrive
+  // with the last of them (8,200 tokens of 32 + 8 heads of 128: 43.1 us behind, 37.3 before).
+  const int angles = nt * half;
+  auto load_angle = [&](int i, float& f, int& pos) {
+    const int t = i / half, x = i - t * half;
+    f = p.inv_freq[x];
+    pos = p.positions[(int64_t)p.axis_of[x] * p.n_tokens + t0 + t];
+  };
+  float freq = 0.f;
+  int pos = 0;
+  int64_t slot = 0;
+  if (tid < angles) load_angle(tid, freq, pos);
+  if (tid < nt && p.slot_map) slot = p.slot_map[t0 + tid];
+  const uint16_t* const weight = mine && normed ? (query ? p.q_weight : p.k_weight) : nullptr;
+  uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
+  if (weight) {
+    wa = *reinterpret_cast<const uint4*>(weight + ca);
+    wb = *reinterpret_cast<const uint4*>(weight + cb);
+  }
   if (mine) {
     const int64_t stride = query ? p.q_stride : key ? p.k_stride : p.v_stride;
     const uint16_t* src = (query ? p.q : key ? p.k : p.v) + t0 * stride + h * D;
@@ -117,26 +136,25 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
       copies_end();
     }
   }
-  uint64_t factor[8];  // of this thread's channels
-  const uint16_t* const weight = mine && normed ? (query ? p.q_weight : p.k_weight) : nullptr;
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    factor[k] = weight ? widen<T>(reinterpret_cast<const uint32_t*>(weight + (k < 4 ? ca : cb))[k & 3]) : pair(1.f, 1.f);
 
   // ---- the tokens' angles and places
-  for (int i = tid; i < nt * half; i += threads) {
+  for (int i = tid; i < angles; i += threads) {
+    if (i != tid) load_angle(i, freq, pos);
     const int t = i / half, x = i - t * half;
-    const float2 cs = turned_by(p.inv_freq[x], p.positions[(int64_t)p.axis_of[x] * p.n_tokens + t0 + t]);
-    const int at = kPairs ? (x >> 1 & 1) * (half >> 2) + (x >> 2) : (x >> 1 & 3) * (half >> 3) + (x >> 3);
-    reinterpret_cast<float2*>(turn + t * (half >> 1) + at)[x & 1] = cs;
+    const int to = kPairs ? (x >> 1 & 1) * (half >> 2) + (x >> 2) : (x >> 1 & 3) * (half >> 3) + (x >> 3);
+    reinterpret_cast<float2*>(turn + t * (half >> 1) + to)[x & 1] = turned_by(freq, pos);
   }
   if (tid < nt) {
-    const int64_t slot = p.slot_map ? p.slot_map[t0 + tid] : 0;
     const bool past = p.slot_map && slot >= p.slot_limit;
     if (past) atomicOr(p.status, kStatusBadSlot);
     place[tid] = past ? -1 : slot;
   }
   __syncthreads();
+  uint64_t factor[8];  // of this thread's channels
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    factor[k] = weight ? widen<T>(reinterpret_cast<const uint32_t*>(k < 4 ? &wa : &wb)[k & 3]) : pair(1.f, 1.f);
+
   uint16_t* const dst = query ? p.q_out + t0 * p.q_out_stride + h * D : key ? p.k_pool : p.v_pool;
   for (int t = 0; t < nt; ++t) {
     copies_landed(nt - 1 - t);
@@ -197,9 +215,9 @@ static cudaError_t launch_t(const RopeParams& p, cudaStream_t stream) {
   // equal passes over a row's pieces, in whole warps
   const int passes = (tasks + kNormThreads - 1) / kNormThreads;
   const int threads = ((tasks + passes - 1) / passes + 31) / 32 * 32;
-  // tokens of a block: as many as leave every SM eight blocks; one where the tokens hardly fill the
+  // tokens of a block: as many as leave every SM four blocks; one where the tokens hardly fill the
   // device
-  int per = (int)min((int64_t)kNormTokens, (int64_t)p.n_tokens * passes / (8 * 152));
+  int per = (int)min((int64_t)kNormTokens, (int64_t)p.n_tokens * passes / (4 * 152));
   if (p.rot > 0) per = min(per, 2 * kNormPairs / p.rot);
   per = max(1, per);
   const int blocks = ((p.n_tokens - 1) / per + 1) * passes;
