@@ -139,6 +139,14 @@ def test_prefix_lengths(prefix, D, G):
     run([(prefix, [prefix + 3, prefix // 2, 0, prefix])], 1, G, D, "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("prefix", [0, 65, 700])
+def test_wide_tables(prefix, D, dtype):
+    """Tables much wider than what they hold: groups of up to 16 rows in runs of 16."""
+    run([(prefix, [prefix + 3, prefix // 2, 0, prefix + 300]), (40, [300, 41])], 2, 4, D, dtype, max_pages=20000, alone=(30, 500))
+
+
 @FEW_AND_MANY
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_groups_of_all_sizes(D, G):
@@ -256,6 +264,11 @@ def test_one_workspace_for_fewer_requests():
                                         ([(500, [600, 700]), (80, [90] * 5)], 1, 20)])
 def test_waits_are_bounded(groups, H, G, D):
     stalled(Shared(groups, H, G, D, "bf16"))
+
+
+def test_waits_are_bounded_in_wide_tables():
+    for D in (64, 128, 256):
+        stalled(Shared([(500, [600, 700, 520])], 1, 4, D, "bf16", max_pages=20000))
 
 
 def test_forked_requests_decode_together():

@@ -387,11 +387,19 @@ SharedPlan shared_plan(const tpk_paged_shape* s, int n_req, int n_grp) {
 // 87 and 114); with up to 32 for as long as two readers mostly meet in L2 (four groups of 8,000: 45 and
 // 59; of 30,000: 153 and 115); with up to 64 where prefixes are short (one of 2,000: 17.6 and 24.6; four
 // of 8,000: 75 and 65).  Lengths are on the device: the table's width stands for them.
-bool shared_split(const tpk_paged_shape* s, int n_req, int n_grp) {
-  const int64_t each = ((int64_t)n_req + n_grp - 1) / n_grp, runs = (each * s->group + kRowTile - 1) / kRowTile;
-  const int64_t read = runs * n_grp * s->max_pages * s->kv_heads * (kPageTokens * 4 * s->head_dim);
-  return shared_split_fits(n_req, n_grp) &&
-         (runs == 1 || (runs == 2 && read <= (int64_t)320 << 20) || (runs <= 4 && read <= (int64_t)100 << 20));
+// (0: no; else the rows of its runs.)  Runs of 8 rows read a prefix twice as often, with less work on each
+// page: for as long as all readers together stay about L2's size (one group of 16 rows, 2,000 tokens:
+// 12.5 us and 13.8 in runs of 16, heads of 256 13.8 and 17.0; four of 8,000: 35.1 and 34.2; 46.5 and 39.1).
+int shared_split(const tpk_paged_shape* s, int n_req, int n_grp) {
+  const int64_t rows = ((int64_t)n_req + n_grp - 1) / n_grp * s->group;  // of a group
+  auto runs = [&](int run_rows) { return (rows + run_rows - 1) / run_rows; };
+  auto read = [&](int run_rows) {
+    return runs(run_rows) * n_grp * s->max_pages * s->kv_heads * (kPageTokens * 4 * s->head_dim);
+  };
+  const int64_t mb = 1 << 20;
+  if (!shared_split_fits(n_req, n_grp) || runs(kRowTile) > 4) return 0;
+  if (rows <= 8 || read(8) <= 100 * mb) return 8;
+  return runs(kRowTile) == 1 || (runs(kRowTile) == 2 && read(kRowTile) <= 320 * mb) || read(kRowTile) <= 100 * mb ? kRowTile : 0;
 }
 
 // Rows of the prefixes' parts, bounded for all calls with no more requests: with more than one part
@@ -757,14 +765,13 @@ tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n
   p.o_stride = HQ * shape->head_dim;
   p.lse = own_lse;
   cudaError_t e;
-  if (shared_split(shape, n_req, n_grp)) {  // and the prefixes, in front of it
+  if (const int run_rows = shared_split(shape, n_req, n_grp)) {  // and the prefixes, in front of it
     p.own_lens = n_tokens;
     p.q_off = grp_off;
     p.lens = n_shared;
     p.n_grp = n_grp;
     p.n_req = n_grp + n_req;
-    const int64_t each = ((int64_t)n_req + n_grp - 1) / n_grp;
-    p.run_rows = each * shape->group <= 8 ? 8 : kRowTile;
+    p.run_rows = run_rows;
     e = launch_shared_split(p, shape->head_dim, shape->dtype, cs);
     if (e != cudaSuccess) return cuda_fail(e, "shared decode launch");
     j.whole_o = own_o;
