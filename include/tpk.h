@@ -428,13 +428,17 @@ tpk_status tpk_tiers_destroy(tpk_tiers* tiers);
 /*
  * A serving step over pages whose lengths live on the device
  * -----------------------------------------------------------
- * The four calls below take request lengths, page tables and token maps from device
+ * The calls below take request lengths, page tables and token maps from device
  * memory, so a step captured once in a CUDA graph is replayed while requests grow,
  * shrink and change places: tpk_kv_tables_update turns old and new lengths into page
  * tables and slot maps, tpk_kv_rope_append rotates the new queries and keys and
- * stores keys and values into the pages, tpk_decode_attn_paged attends one new token
- * per request, tpk_cross_attn_paged attends any number of query tokens per request
- * to paged states of another length (an encoder's, or a prompt's own).  They follow
+ * stores keys and values into the pages (tpk_kv_norm_rope_append norms them first),
+ * tpk_decode_attn_paged attends one new token per request, tpk_cross_attn_paged attends
+ * any number of query tokens per request to paged states of another length (an encoder's,
+ * or a prompt's own), tpk_window_attn_paged a request's last tokens to its own pages
+ * through a window, tpk_decode_attn_shared one new token of requests that share prefixes;
+ * tpk_kv_pages_fork, tpk_kv_pages_compact and tpk_kv_pages_copy keep pages that several
+ * requests share.  They follow
  * the conventions above (ownership, pointers, streams, errors); their pools are
  * [slot][kv_heads][64][head_dim] of bfloat16 or float16, their page table is int32
  * [n_req][max_pages] (row b: the slots of request b's pages in order).  Queries, keys,
