@@ -565,7 +565,8 @@ tpk_status tpk_kv_pages_fork(int n_req, int max_pages, int64_t kv_slots, const i
  *                        tpk_kv_pages_copy moves the pages: no slot is in both lists.
  * Free entries outside the pool, table entries that are on the stack or outside the pool
  * (left as they are), lengths out of range and a full stack set bit 0 of the device status.
- * Workspace, limits and capture as for tpk_kv_pages_fork; max_copies in [0, kv_slots].
+ * Workspace, limits and capture as for tpk_kv_pages_fork; max_copies in
+ * [0, 2^31 - 16384).
  */
 tpk_status tpk_kv_pages_compact(int n_req, int max_pages, int64_t kv_slots, const int32_t* n_tokens,
                                 const int32_t* table_in, int32_t* table_out, const int32_t* shares_in,

@@ -227,6 +227,13 @@ def test_large_pools(slots, held):
     compact(lens, table, shares, order[k:], slots - k, slots)
 
 
+def test_lists_longer_than_the_pool():
+    compact([64, 64], [[3], [0]], [0, 0, 0, 5], [1, 2], 2, 50)
+    compact([64, 64], [[3], [0]], [0, 0, 0, 5], [1, 2], 2, 50, in_place=True)
+    compact([64], [[0]], [0], [], 0, 9)
+    compact([64], [[9000]], [0] * 9001, list(range(9000)), 9000, 20000)
+
+
 def test_compaction_of_odd_inputs():
     compact([64], [[0]], [0], [], 0, 1)                                  # full
     compact([0], [[0]], [0, 0, 0], [2, 0, 1], 3, 3)                      # empty

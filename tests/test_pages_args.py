@@ -53,7 +53,7 @@ def test_fork_arguments_are_refused(L):
 
 
 def test_compact_arguments_are_refused(L):
-    for kw in COMMON + [{"lens": None}, {"fin": None}, {"fout": None}, {"new": None}, {"nc": None}, {"mc": -1}, {"mc": 10}, {"new": 6}]:
+    for kw in COMMON + [{"lens": None}, {"fin": None}, {"fout": None}, {"new": None}, {"nc": None}, {"mc": -1}, {"mc": 0x7fffffff}, {"new": 6}]:
         assert compact(L, **kw) == INVALID, (kw, err(L))
     assert compact(L, nbytes=100) == NOMEM
 
@@ -84,7 +84,7 @@ def test_python_calls_marshal():
     with pytest.raises(tpk.TpkError, match="n_req"):
         tpk.kv_pages_fork(0, 4, 9, x, x, None, x, 32, x, x, x, 8, x, x, x, x, x, x, x, BIG)
     with pytest.raises(tpk.TpkError, match="max_copies"):
-        tpk.kv_pages_compact(1, 4, 9, x, x, x, x, x, x, x, 8, x, x, x, 10, x, x, x, x, BIG)
+        tpk.kv_pages_compact(1, 4, 9, x, x, x, x, x, x, x, 8, x, x, x, -1, x, x, x, x, BIG)
     with pytest.raises(tpk.TpkError, match="workspace"):
         tpk.kv_pages_fork(1, 4, 9, x, x, None, x, 32, x, x, x, 8, x, x, x, x, x, x, x, -1)
 

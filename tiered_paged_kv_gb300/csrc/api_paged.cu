@@ -525,7 +525,7 @@ tpk_status tpk_kv_pages_compact(int n_req, int max_pages, int64_t kv_slots, cons
                                 tpk_stream_t stream) {
   const tpk_status st = check_pages(n_req, max_pages, kv_slots, free_cap, ws, ws_bytes);
   if (st != TPK_OK) return st;
-  if (max_copies < 0 || max_copies > kv_slots) return fail(TPK_ERR_INVALID, "max_copies %d out of [0, kv_slots]", max_copies);
+  if (max_copies < 0 || max_copies > 0x7fffffff - 16384) return fail(TPK_ERR_INVALID, "max_copies %d", max_copies);
   if (!n_tokens || !table_in || !table_out || !shares_in || !shares_out || (free_cap > 0 && (!free_in || !free_out)) ||
       !n_free_in || !n_free_out || !new_slot || !n_copies || (max_copies > 0 && (!copy_src || !copy_dst)))
     return fail(TPK_ERR_INVALID, "null pointer argument");

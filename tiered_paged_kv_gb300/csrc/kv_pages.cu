@@ -294,9 +294,11 @@ __global__ void __launch_bounds__(kPartThreads, 1) compact_kernel(const CompactP
   const int step = Team::parts * kPartThreads, thread = part * kPartThreads + tid;
   wait_before();
   const int n_free = min(max(*p.n_free_in, 0), p.free_cap);
+  const int most = min(p.max_copies, slots);  // entries of the lists that may be moves
   bool bad = false;
   for (int i = thread; i < slots; i += step) mark[i] = kHeld;
-  for (int i = thread; i < p.max_copies; i += step) src[i] = dst[i] = -1;
+  for (int i = thread; i < most; i += step) src[i] = dst[i] = -1;
+  for (int i = most + thread; i < p.max_copies; i += step) p.copy_src[i] = p.copy_dst[i] = -1;
   Team::meet();
   for (int i = thread; i < n_free; i += step) {
     const int x = p.free_in[i];
@@ -318,8 +320,8 @@ __global__ void __launch_bounds__(kPartThreads, 1) compact_kernel(const CompactP
     if (!here) continue;
     moved[i] = is_free ? -1 : i;
     const int above = held - (i - below) - 1;  // slots in use above this one
-    if (is_free && below < p.max_copies) dst[below] = i;
-    if (!is_free && above < p.max_copies) src[above] = i;
+    if (is_free && below < most) dst[below] = i;
+    if (!is_free && above < most) src[above] = i;
   }
   Team::meet();
 
@@ -328,15 +330,15 @@ __global__ void __launch_bounds__(kPartThreads, 1) compact_kernel(const CompactP
     const int s = Team::get(src + r), d = Team::get(dst + r);
     return d >= 0 && d < s;
   };
-  if (thread == 0 && (p.max_copies == 0 || !goes(0))) *p.n_copies = 0;
-  for (int r = thread; r < p.max_copies; r += step) {
+  if (thread == 0 && (most == 0 || !goes(0))) *p.n_copies = 0;
+  for (int r = thread; r < most; r += step) {
     const bool go = goes(r);
     if (go) {
       const int s = Team::get(src + r), d = Team::get(dst + r);
       moved[s] = d;
       mark[d] = kTaken;
       // (an entry of the lists' rest is no move before and after it is cleared)
-      if (r + 1 == p.max_copies || !goes(r + 1)) *p.n_copies = r + 1;
+      if (r + 1 == most || !goes(r + 1)) *p.n_copies = r + 1;
     } else if (!kLocal) {
       src[r] = dst[r] = -1;
     }
