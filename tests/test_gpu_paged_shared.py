@@ -126,17 +126,18 @@ def test_heads(G, D, dtype):
     run([(200, [230, 260, 201])], 2 if G < 100 else 1, G, D, dtype, seed=G)
 
 
-# Few rows a group go through one launch in runs, many as row tiles: both
-FEW_AND_MANY = pytest.mark.parametrize("G", [2, 20])
+# Few rows a group go through one launch in runs of 8 or 16, many (or some behind a wide table) as row
+# tiles: all of these
+FEW_AND_MANY = pytest.mark.parametrize("G,wide", [(2, None), (20, None), (20, 20000)])
 
 
 @FEW_AND_MANY
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("prefix", [0, 1, 63, 64, 65, 128, 1000])
-def test_prefix_lengths(prefix, D, G):
+def test_prefix_lengths(prefix, D, G, wide):
     """Also one that ends inside a page, requests with nothing of their own, and with less than it."""
-    run([(prefix, [prefix + 3, prefix, prefix + 64, prefix + 200])], 1, G, D, "bf16")
-    run([(prefix, [prefix + 3, prefix // 2, 0, prefix])], 1, G, D, "bf16")
+    run([(prefix, [prefix + 3, prefix, prefix + 64, prefix + 200])], 1, G, D, "bf16", max_pages=wide)
+    run([(prefix, [prefix + 3, prefix // 2, 0, prefix])], 1, G, D, "bf16", max_pages=wide)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -149,11 +150,11 @@ def test_wide_tables(prefix, D, dtype):
 
 @FEW_AND_MANY
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_groups_of_all_sizes(D, G):
+def test_groups_of_all_sizes(D, G, wide):
     run([(300, [320] * 2 + [0]), (40, [41]), (700, []), (130, [130 + i for i in range(70)]), (64, [0, 0])], 2, G, D, "f16",
-        alone=(70, 0, 333, 1))
+        alone=(70, 0, 333, 1), max_pages=wide)
     run([(300, [320] * 2 + [0]), (40, [41]), (700, []), (130, [130 + i for i in range(7)]), (64, [0, 0])], 1, G, D, "bf16",
-        alone=(70, 0, 333, 1))
+        alone=(70, 0, 333, 1), max_pages=wide)
 
 
 @pytest.mark.parametrize("G,n", [(8, 40), (1, 300), (5, 60)])
@@ -163,29 +164,29 @@ def test_more_rows_than_a_tile(G, n):
 
 
 @FEW_AND_MANY
-def test_long_prefixes(G):
+def test_long_prefixes(G, wide):
     """Cut into many parts; own parts cut into ranges."""
-    run([(9000, [9100, 9003, 9000, 12000])], 1, G, 128, "bf16")
-    run([(6000, [6100, 6003]), (3000, [3000, 8000, 3500])], 1, G, 256, "bf16")
+    run([(9000, [9100, 9003, 9000, 12000])], 1, G, 128, "bf16", max_pages=wide)
+    run([(6000, [6100, 6003]), (3000, [3000, 8000, 3500])], 1, G, 256, "bf16", max_pages=wide)
 
 
 @FEW_AND_MANY
-def test_nobody_has_the_whole_prefix(G):
+def test_nobody_has_the_whole_prefix(G, wide):
     """The row with the most of it is read, whichever that is."""
-    run([(500, [0, 130, 300, 300, 20]), (200, [0, 199])], 1, G, 128, "bf16")
+    run([(500, [0, 130, 300, 300, 20]), (200, [0, 199])], 1, G, 128, "bf16", max_pages=wide)
 
 
 @FEW_AND_MANY
-def test_strides_scale_and_output_type(G):
-    run([(100, [150, 120])], 2, G, 64, "f16", f32=True, q_gap=16, o_gap=24, scale=0.4)
-    run([(100, [150, 120])], 2, G, 256, "bf16", q_gap=8, o_gap=8, scale=-0.05, alone=(30,))
-    run([(100, [150, 120])], 2, G, 128, "bf16", f32=True)
+def test_strides_scale_and_output_type(G, wide):
+    run([(100, [150, 120])], 2, G, 64, "f16", f32=True, q_gap=16, o_gap=24, scale=0.4, max_pages=wide)
+    run([(100, [150, 120])], 2, G, 256, "bf16", q_gap=8, o_gap=8, scale=-0.05, alone=(30,), max_pages=wide)
+    run([(100, [150, 120])], 2, G, 128, "bf16", f32=True, max_pages=wide)
 
 
 @FEW_AND_MANY
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_large_scores(D, G):
-    run([(300, [350, 420])], 1, G, D, "bf16", scale=4.0)
+def test_large_scores(D, G, wide):
+    run([(300, [350, 420])], 1, G, D, "bf16", scale=4.0, max_pages=wide)
 
 
 def test_many_requests_and_groups():
@@ -193,8 +194,8 @@ def test_many_requests_and_groups():
 
 
 @FEW_AND_MANY
-def test_nan_queries_stay_in_their_row(G):
-    c = Shared([(200, [230, 260, 201])], 2, G, 128, "bf16")
+def test_nan_queries_stay_in_their_row(G, wide):
+    c = Shared([(200, [230, 260, 201])], 2, G, 128, "bf16", max_pages=wide)
     c.dq[1, 128:256] = float("nan")
     c.call()
     torch.cuda.synchronize()
@@ -204,9 +205,9 @@ def test_nan_queries_stay_in_their_row(G):
 
 
 @FEW_AND_MANY
-def test_bad_entries_and_counts(G):
+def test_bad_entries_and_counts(G, wide):
     """A page of the prefix that is not there is left out for everybody; values out of range are cut."""
-    c = Shared([(300, [320, 330])], 1, G, 64, "bf16")
+    c = Shared([(300, [320, 330])], 1, G, 64, "bf16", max_pages=wide)
     c.table[0, 1] = c.slots  # the row that is read for the group
     c.keys = [torch.cat([k[:64], k[128:]]) for k in c.keys]
     c.values = [torch.cat([v[:64], v[128:]]) for v in c.values]
@@ -214,8 +215,8 @@ def test_bad_entries_and_counts(G):
     c.call()
     c.check()
     assert tpk.get_device_status(reset=True) == (4, 1)
-    c = Shared([(128, [128, 128])], 1, G, 64, "bf16")
-    c.shared.fill_(5000)
+    c = Shared([(128, [128, 128])], 1, G, 64, "bf16", max_pages=wide)
+    c.shared.fill_(64 * c.max_pages + 1)  # past the table row
     c.off.copy_(torch.tensor([-3, 9], dtype=torch.int32))
     c.call()
     c.check()
@@ -223,8 +224,8 @@ def test_bad_entries_and_counts(G):
 
 
 @FEW_AND_MANY
-def test_other_stream_captured_and_grown(G):
-    c = Shared([(300, [320, 330]), (64, [100, 70])], 2, G, 128, "bf16", alone=(40, 50))
+def test_other_stream_captured_and_grown(G, wide):
+    c = Shared([(300, [320, 330]), (64, [100, 70])], 2, G, 128, "bf16", alone=(40, 50), max_pages=wide)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(st):

@@ -390,6 +390,10 @@ SharedPlan shared_plan(const tpk_paged_shape* s, int n_req, int n_grp) {
 // (0: no; else the rows of its runs.)  Runs of 8 rows read a prefix twice as often, with less work on each
 // page: for as long as all readers together stay about L2's size (one group of 16 rows, 2,000 tokens:
 // 12.5 us and 13.8 in runs of 16, heads of 256 13.8 and 17.0; four of 8,000: 35.1 and 34.2; 46.5 and 39.1).
+// One group's readers walk side by side, so that it may have more rows (80 rows, 8 heads of 128, 2,000
+// tokens: 20.0 us in runs of 8, 24.3 as tiles; 160 rows, 4 heads of 256, 1,000 tokens: 21.6 and 30.5; in
+// runs of 16, 2,000 tokens: 27.8 and 31.6; 320 rows, 8 heads of 64, 300 tokens: 18.3 and 20.2; 1,000
+// tokens: 25.1 and 21.2; four groups of 80 rows, 1,000 tokens of 8 heads of 128: 35.9 and 31.7).
 int shared_split(const tpk_paged_shape* s, int n_req, int n_grp) {
   const int64_t rows = ((int64_t)n_req + n_grp - 1) / n_grp * s->group;  // of a group
   auto runs = [&](int run_rows) { return (rows + run_rows - 1) / run_rows; };
@@ -397,7 +401,12 @@ int shared_split(const tpk_paged_shape* s, int n_req, int n_grp) {
     return runs(run_rows) * n_grp * s->max_pages * s->kv_heads * (kPageTokens * 4 * s->head_dim);
   };
   const int64_t mb = 1 << 20;
-  if (!shared_split_fits(n_req, n_grp) || runs(kRowTile) > 4) return 0;
+  if (!shared_split_fits(n_req, n_grp)) return 0;
+  if (n_grp == 1 && runs(kRowTile) > 4) {
+    const bool some = rows <= 160;
+    return read(8) <= (some ? 85 : 70) * mb && rows <= 360 ? 8 : some && read(kRowTile) <= 85 * mb ? kRowTile : 0;
+  }
+  if (runs(kRowTile) > 4) return 0;
   if (rows <= 8 || read(8) <= 100 * mb) return 8;
   return runs(kRowTile) == 1 || (runs(kRowTile) == 2 && read(kRowTile) <= 320 * mb) || read(kRowTile) <= 100 * mb ? kRowTile : 0;
 }
