@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kPartThreads, 1) compact_kernel(const CompactP
 // ------------------------------------------------------------------ copies
 // A block finds the pairs that are copies (kList entries at a time), then takes every gridDim-th
 // piece of their pages in all pools: kCopyBytes together, each thread's loads in flight at once.
-// Measured: 2,944 pages of 131 KB in four pools (3.1 GB) 491 us, 6.3 TB/s; 300 copies of 20 sources in
+// Measured: 2,944 pages of 131 KB in four pools (3.1 GB) 491 us, 6.3 TB/s; 300 copies of 80 sources in
 // 16 pools (629 MB written) 149 us.  (Four or sixteen loads a thread, two to eight blocks an SM, and
 // loading a piece once for several copies of it in a row: within 4 %.)
 constexpr int kCopyThreads = 256;
