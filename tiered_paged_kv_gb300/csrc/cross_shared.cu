@@ -6,6 +6,11 @@
 // where n decode calls would read it n times.  What a request does not share is an ordinary decode
 // from its own first token on; both leave a maximum, a sum and an output, joined here in a fixed
 // order: the prefix's parts, then the request's own.
+//
+// Bound: the tensor cores over the prefixes, HBM over the rest, one after the other.  Measured: 64
+// requests behind 32,768 tokens with 30 to 1,500 of their own, 4 x 8 heads of 256, 116 us (tiles 67,
+// decode 27, its fold 3, join 6); 13 groups of 1 to 24 behind 300 to 9,000 tokens with up to 2,500 of
+// their own, 8 x 5 heads of 128 (491 MB), 116 us (61, 40, 3, 5).
 #include "cross_tile.cuh"
 
 namespace tpk {
