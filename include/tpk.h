@@ -523,7 +523,7 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
  * len_keep is out of range (or more than its source has) stays as it was: both have
  * granted[b] = 0.
  *   source, len_in, len_keep  dev int32 [n_req]; len_in: the lengths before the call
- *   table_in, table_out  dev int32 [n_req][max_pages], not the same; entries of table_out
+ *   table_in, table_out  dev int32 [n_req][max_pages], without a common part; entries of table_out
  *                        past a request's pages are left as they were
  *   shares_in, shares_out     dev int32 [kv_slots] (may be the same)
  *   free_slots           dev int32 [free_cap], updated in place (what is not on the stack

@@ -19,7 +19,7 @@ def L():
     return tpk.lib()
 
 
-def fork(L, n=2, mp=4, slots=9, source=16, len_in=16, keep=16, tin=16, tout=32, sin=16, sout=16, free=16, cap=8, nin=16, nout=16,
+def fork(L, n=2, mp=4, slots=9, source=16, len_in=16, keep=16, tin=16, tout=48, sin=16, sout=16, free=16, cap=8, nin=16, nout=16,
          out=16, granted=16, cs=16, cd=16, ws=16, nbytes=BIG):
     return L.tpk_kv_pages_fork(n, mp, slots, source, len_in, keep, tin, tout, sin, sout, free, cap, nin, nout, out, granted, cs, cd,
                                ws, nbytes, None)
@@ -50,12 +50,17 @@ def test_fork_arguments_are_refused(L):
                         {"keep": 2}, {"free": 6}]:
         assert fork(L, **kw) == INVALID, (kw, err(L))
     assert fork(L, nbytes=100) == NOMEM and "required" in err(L)
+    # tables of 32 bytes, holders of 36: a part in common
+    for kw in [{"tin": 48, "tout": 48}, {"tin": 48, "tout": 20}, {"tin": 48, "tout": 76}, {"sout": 20}, {"sin": 48}]:
+        assert fork(L, **kw) == INVALID and "overlaps" in err(L), kw
 
 
 def test_compact_arguments_are_refused(L):
     for kw in COMMON + [{"lens": None}, {"fin": None}, {"fout": None}, {"new": None}, {"nc": None}, {"mc": -1}, {"mc": 0x7fffffff}, {"new": 6}]:
         assert compact(L, **kw) == INVALID, (kw, err(L))
     assert compact(L, nbytes=100) == NOMEM
+    for kw in [{"tout": 20}, {"tin": 44}, {"sout": 48}, {"fout": 44}, {"fin": 44}]:
+        assert compact(L, **kw) == INVALID and "overlaps" in err(L), kw
 
 
 @pytest.mark.parametrize("kw,code", BAD_SHAPES, ids=lambda x: str(x))
@@ -82,11 +87,11 @@ def test_python_calls_marshal():
             tpk.kv_pages_copy(s, *args)
     x = 16
     with pytest.raises(tpk.TpkError, match="n_req"):
-        tpk.kv_pages_fork(0, 4, 9, x, x, None, x, 32, x, x, x, 8, x, x, x, x, x, x, x, BIG)
+        tpk.kv_pages_fork(0, 4, 9, x, x, None, x, 48, x, x, x, 8, x, x, x, x, x, x, x, BIG)
     with pytest.raises(tpk.TpkError, match="max_copies"):
         tpk.kv_pages_compact(1, 4, 9, x, x, x, x, x, x, x, 8, x, x, x, -1, x, x, x, x, BIG)
     with pytest.raises(tpk.TpkError, match="workspace"):
-        tpk.kv_pages_fork(1, 4, 9, x, x, None, x, 32, x, x, x, 8, x, x, x, x, x, x, x, -1)
+        tpk.kv_pages_fork(1, 4, 9, x, x, None, x, 48, x, x, x, 8, x, x, x, x, x, x, x, -1)
 
 
 def test_workspace_sizes(L):

@@ -204,6 +204,12 @@ tpk_status check_counts(const tpk_paged_shape* s, int n_req) {
 constexpr int kMaxLayers = 4096, kPagesCounts = 64;
 size_t pages_ws_bytes(int64_t kv_slots) { return align256((kPagesCounts + 3 * (size_t)kv_slots) * sizeof(int32_t)); }
 
+// Whether arrays of n int32 share a part; `same`: one array in both places does not count.
+bool overlap(const int32_t* a, const int32_t* b, int64_t n, bool same) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b), bytes = (uintptr_t)n * sizeof(int32_t);
+  return !(same && x == y) && x < y + bytes && y < x + bytes;
+}
+
 tpk_status check_pages(int n_req, int max_pages, int64_t kv_slots, int free_cap, const void* ws, size_t ws_bytes) {
   if (n_req < 1 || n_req > kMaxPagedReq) return fail(TPK_ERR_INVALID, "n_req %d out of [1, %d]", n_req, kMaxPagedReq);
   if (max_pages < 1 || max_pages > kMaxTableRow || (int64_t)n_req * max_pages > 0x7fffffffLL)
@@ -496,7 +502,8 @@ tpk_status tpk_kv_pages_fork(int n_req, int max_pages, int64_t kv_slots, const i
   if (!aligned_to(4, source, len_in, len_keep, table_in, table_out, shares_in, shares_out, free_slots, n_free_in, n_free_out,
                   len_out, granted, copy_src, copy_dst))
     return fail(TPK_ERR_INVALID, "an array is not aligned to its elements");
-  if (table_in == table_out) return fail(TPK_ERR_INVALID, "table_out is table_in");
+  if (overlap(table_in, table_out, (int64_t)n_req * max_pages, false)) return fail(TPK_ERR_INVALID, "table_out overlaps table_in");
+  if (overlap(shares_in, shares_out, kv_slots, true)) return fail(TPK_ERR_INVALID, "shares_out overlaps shares_in");
   ForkParams p;
   p.source = source;
   p.len_in = len_in;
@@ -541,6 +548,9 @@ tpk_status tpk_kv_pages_compact(int n_req, int max_pages, int64_t kv_slots, cons
   if (!aligned_to(4, n_tokens, table_in, table_out, shares_in, shares_out, free_in, free_out, n_free_in, n_free_out, new_slot,
                   copy_src, copy_dst, n_copies))
     return fail(TPK_ERR_INVALID, "an array is not aligned to its elements");
+  if (overlap(table_in, table_out, (int64_t)n_req * max_pages, true) || overlap(shares_in, shares_out, kv_slots, true) ||
+      overlap(free_in, free_out, free_cap, true))
+    return fail(TPK_ERR_INVALID, "an output overlaps its input and is not it");
   CompactParams p;
   p.n_tokens = n_tokens;
   p.table_in = table_in;
