@@ -381,7 +381,7 @@ SharedPlan shared_plan(const tpk_paged_shape* s, int n_req, int n_grp) {
   const int64_t per = tiles * per_tile, items = n_grp * ((each + per - 1) / per) * H;
   // One group's parts are equally long: one wave of them.  Several groups' may not be: about two (thirteen
   // groups of 300 to 9,000 tokens, 8 heads of 128: 119, 116, 113 and 124 us with one, two, three and
-  // six; twelve of 2,000 tokens: 82, 84, 93 and 106).
+  // six, before the last step of the tiles; twelve of 2,000 tokens: 82, 84, 93 and 106).
   const int64_t parts = n_grp == 1 ? kTileBlocks / items : (kSharedWaves * kTileBlocks + items - 1) / items;
   const int64_t splits = std::min({parts, ((int64_t)s->max_pages + 3) / 4, (int64_t)kSharedSplits});
   return {tiles, n_req / per + std::min(n_grp, n_req), std::max<int64_t>(splits, 1)};  // groups without requests have no tiles

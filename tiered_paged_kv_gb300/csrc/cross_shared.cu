@@ -8,9 +8,9 @@
 // order: the prefix's parts, then the request's own.
 //
 // Bound: the tensor cores over the prefixes, HBM over the rest, one after the other.  Measured: 64
-// requests behind 32,768 tokens with 30 to 1,500 of their own, 4 x 8 heads of 256, 116 us (tiles 67,
+// requests behind 32,768 tokens with 30 to 1,500 of their own, 4 x 8 heads of 256, 114 us (tiles 65,
 // decode 27, its fold 3, join 6); 13 groups of 1 to 24 behind 300 to 9,000 tokens with up to 2,500 of
-// their own, 8 x 5 heads of 128 (491 MB), 116 us (61, 40, 3, 5).
+// their own, 8 x 5 heads of 128 (491 MB), 115 us (60, 40, 3, 5).
 #include "cross_tile.cuh"
 
 namespace tpk {

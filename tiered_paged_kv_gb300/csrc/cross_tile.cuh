@@ -133,7 +133,7 @@ struct TileShared {
   uint4 next;                      // the work taken over from a block not started
   uint64_t full[8], empty[8];      // ring of key and value slots
   uint64_t s_full[2];              // scores written (by score buffer)
-  uint64_t p_half[2], p_full[2];   // weights of half of each row's pieces written, of all
+  uint64_t p_half[2], p_full[2];   // weights of half of each row's pieces written (two threads a row), of all
   uint64_t pv_done, o_full[2], o_empty[2];  // a product ended (one tile), the last one; o read (by tile)
   uint64_t q_full, q_empty, tail, drain, taken;
   uint64_t item_full[2], item_empty[2];
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_half[i], 256);
-      mbar_init(&S.p_full[i], 256);
+      mbar_init(&S.p_full[i], kShare == 4 ? 4 * kTileRows : 256);
       mbar_init(&S.o_full[i], 1);
       mbar_init(&S.o_empty[i], kTileRows * kShare);
       mbar_init(&S.item_full[i], 1);
@@ -576,23 +576,27 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
           ++used[x];
         }
         const int n = step[buf]++;
+        // Four threads a row have their weights ready at about the same time: one wait for all of them (one
+        // input again and again, 64 answers to a prompt at head size 256: 112.7 us, 114.9 with two; 13 groups
+        // at 128: 114.5, 116.4).
+        constexpr int kWaits = kShare == 4 ? 1 : 2;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          wait(s == 0 ? &S.p_half[buf] : &S.p_full[buf], n);
+        for (int s = 0; s < kWaits; ++s) {
+          wait(s + 1 < kWaits ? &S.p_half[buf] : &S.p_full[buf], n);
           if (!ok) return;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < C::kParts; ++c) {
             const uint64_t v = v_op + nth(at, c) * kSlotStep;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int i = (y >> 1) * 4 + 2 * s + (y & 1);  // 16 tokens: two 8-row groups
+            for (int y = 0; y < 8 / kWaits; ++y) {
+              const int i = kWaits == 1 ? y : (y >> 1) * 4 + 2 * s + (y & 1);  // 16 tokens: two 8-row groups
               if (i < groups)
                 tc_mma_ts(tmem + 256 + x * 128 + c * 128,
                           tmem + buf * kKeys + i / (8 / kShare) * (kKeys / kShare) + i % (8 / kShare) * 8,
                           v + i * 128, id_pv, more || s > 0 || y > 0);
             }
-            if (last && s == 1) tc_commit(empty + 8 * nth(at, c));
+            if (last && s + 1 == kWaits) tc_commit(empty + 8 * nth(at, c));
           }
         }
       };
@@ -985,8 +989,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
           tc_st16(s_addr + (c >> 1), w);  // over scores of this half already used
           tc_wait_st();
           tc_fence_before();
-          // (a row's pieces: two of two halves, or one of each quarter)
-          mbar_arrive((kShare == 2 ? c == 0 : half % 2 == 0) ? &S.p_half[buf] : &S.p_full[buf]);
+          mbar_arrive(kShare == 2 && c == 0 ? &S.p_half[buf] : &S.p_full[buf]);
         }
         const float2 both = unpair(add2(sum[0], sum[1]));
         l += both.x + both.y;
