@@ -425,17 +425,17 @@ int64_t shared_rows(const tpk_paged_shape* s, int n_req) {
 }
 
 struct SharedWs {
-  size_t part_ml, part_o, own_o, own_lse, own_begin, split, bytes;
+  size_t part_ml, part_o, own_o, own_ml, own_begin, split, bytes;
 };
 SharedWs shared_ws(const tpk_paged_shape* s, int n_req) {
   const size_t rows = (size_t)n_req * s->kv_heads * s->group, parts = (size_t)shared_rows(s, n_req);
   SharedWs w;
   w.part_ml = 0;
   w.part_o = w.part_ml + align256(parts * 8);
-  // results of the prefixes (where they are no parts), then of what is not shared
+  // weighted values of the prefixes (where they are no parts), then of what is not shared; their maxima and sums
   w.own_o = w.part_o + align256(parts * s->head_dim * 4);
-  w.own_lse = w.own_o + align256(2 * rows * s->head_dim * 4);
-  w.own_begin = w.own_lse + align256(2 * rows * 4);
+  w.own_ml = w.own_o + align256(2 * rows * s->head_dim * 4);
+  w.own_begin = w.own_ml + align256(2 * rows * sizeof(float2));
   w.split = w.own_begin + align256((size_t)n_req * 4);
   w.bytes = w.split + split_ws_bytes(s);
   return w;
@@ -772,7 +772,7 @@ tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n
   p.own_begin = reinterpret_cast<int32_t*>(at(w.own_begin));
   const int64_t HQ = (int64_t)shape->kv_heads * shape->group, rows = n_req * HQ;
   float* const own_o = reinterpret_cast<float*>(at(w.own_o));
-  float* const own_lse = reinterpret_cast<float*>(at(w.own_lse));
+  float2* const own_ml = reinterpret_cast<float2*>(at(w.own_ml));
   SharedJoinParams j;
   std::memset(&j, 0, sizeof j);
   // what the requests do not share
@@ -782,7 +782,8 @@ tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n
   p.o = own_o;
   p.o_f32 = 1;
   p.o_stride = HQ * shape->head_dim;
-  p.lse = own_lse;
+  p.sums = 1;
+  p.lse = reinterpret_cast<float*>(own_ml);
   cudaError_t e;
   if (const int run_rows = shared_split(shape, n_req, n_grp)) {  // and the prefixes, in front of it
     p.own_lens = n_tokens;
@@ -794,9 +795,9 @@ tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n
     e = launch_shared_split(p, shape->head_dim, shape->dtype, cs);
     if (e != cudaSuccess) return cuda_fail(e, "shared decode launch");
     j.whole_o = own_o;
-    j.whole_lse = own_lse;
+    j.whole_ml = own_ml;
     j.own_o = own_o + rows * shape->head_dim;
-    j.own_lse = own_lse + rows;
+    j.own_ml = own_ml + rows;
   } else {
     // the prefixes: the groups are the requests
     PagedParams g = p;
@@ -818,7 +819,7 @@ tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n
     j.part_ml = g.part_ml;
     j.splits = (int)plan.splits;
     j.own_o = own_o;
-    j.own_lse = own_lse;
+    j.own_ml = own_ml;
   }
   j.own_begin = p.own_begin;
   j.o = o;

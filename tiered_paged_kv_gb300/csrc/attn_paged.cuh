@@ -233,6 +233,14 @@ __device__ __forceinline__ void store_pair(const PagedParams& p, int64_t row, in
   else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at) = T::pack(x, y);
 }
 
+// A row's log-sum; or, with p.sums, its maximum in base 2 and its sum, for a join.
+__device__ __forceinline__ void store_sum(const PagedParams& p, int64_t row, float M, float L) {
+  if (p.sums) reinterpret_cast<float2*>(p.lse)[row] = make_float2(M, L);
+  else p.lse[row] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
+}
+// What a row's weighted values are multiplied by.
+__device__ __forceinline__ float over_sum(const PagedParams& p, float L) { return p.sums ? 1.f : L == 0.f ? 0.f : 1.f / L; }
+
 // Row r of a run: its query token and query head; false past the run's last row.
 __device__ __forceinline__ bool run_row(const PagedParams& p, int first, int count, int h, int tile, int r, int& token,
                                         int& head) {
@@ -347,7 +355,7 @@ struct Rows {
         const int tok = tok0 + (kSmall ? g + 8 * y : 8 * (y >> 1) + 2 * t + (y & 1));
         const int n = kSmall ? 0 : y >> 1, at = kSmall ? 2 * y + e : 2 * e + (y & 1);
         const bool seen = (tok >= see_lo[e] || (kSpan == kWindowed && tok < p.sinks)) && tok < see_hi[e];
-        x[e][y] = seen ? (sc[n][0][at] + sc[n][1][at]) * p.qscale : kEmpty;
+        x[e][y] = seen ? __fmul_rn(sc[n][0][at] + sc[n][1][at], p.qscale) : kEmpty;
         grows = grows || x[e][y] > m[e];
       }
     // Three steps over 8 lanes wait for the vote, two over 4 do not.
@@ -547,7 +555,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
         int token, head;
         if (!run_row(p, batch.out(walk.b, first), count, h, (int)run - h * tiles, i / (D / 2), token, head)) continue;
         store_pair<T>(p, token, head, D, i % (D / 2) * 2, 0.f, 0.f);
-        if (i % (D / 2) == 0) p.lse[(int64_t)token * p.H * p.G + head] = kEmpty;
+        if (i % (D / 2) == 0) store_sum(p, (int64_t)token * p.H * p.G + head, kEmpty, 0.f);
       }
       return;
     }
@@ -615,7 +623,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
       const int64_t r = i / (D / 2);
       store_pair<T>(p, first + r / HQ, (int)(r % HQ), D, (int)(i % (D / 2)) * 2, 0.f, 0.f);
     }
-    for (int64_t i = tid; i < (int64_t)count * HQ; i += kPagedThreads) p.lse[(int64_t)first * HQ + i] = kEmpty;
+    for (int64_t i = tid; i < (int64_t)count * HQ; i += kPagedThreads) store_sum(p, (int64_t)first * HQ + i, kEmpty, 0.f);
   }
     if (lo >= hi) return;
   }
@@ -757,13 +765,13 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
       for (int w = 0; w < kConsumers; ++w) L += exp2f(S.m[w][r] - (M == kEmpty ? 0.f : M)) * S.l[w][r];
       int token, head;
       const bool write = run_row(p, out, count, h, tile, r, token, head) && !dead;
-      const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+      const float inv = whole ? over_sum(p, L) : 1.f;
       // the join's record: this block has the run's first page and not its last
       if (tid == 0 && pass == 0 && !whole && s.page == 0)
         p.cuts[blockIdx.x] = {out, count, h, tile, (int)((s.pages - s.count - 1) / per) + 2};
       if (write && tid % kPer == 0) {
         if (whole) {
-          p.lse[(int64_t)token * HQ + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
+          store_sum(p, (int64_t)token * HQ + head, M, L);
         } else {
           p.part_ml[slot * kRowTile + r] = M;
           p.part_ml[(2 * (int64_t)gridDim.x + slot) * kRowTile + r] = L;
@@ -862,7 +870,7 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
         }
     }
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const float inv = over_sum(p, L);
   if constexpr (kVec == 1) {
     const float x = o[0] * inv, y = __shfl_down_sync(0xffffffffu, x, 1);
     if ((tid & 1) == 0) store_pair<T>(p, token, head, D, c, x, y);
@@ -870,7 +878,7 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
 #pragma unroll
     for (int e = 0; e < kVec; e += 2) store_pair<T>(p, token, head, D, c + e, o[e] * inv, o[e + 1] * inv);
   }
-  if (tid == 0) p.lse[(int64_t)token * p.H * p.G + head] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
+  if (tid == 0) store_sum(p, (int64_t)token * p.H * p.G + head, M, L);
 }
 
 int device_sms();

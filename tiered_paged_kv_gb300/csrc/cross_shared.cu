@@ -4,8 +4,9 @@
 // A group of n requests has n G rows for each KV head, all of which see the prefix: as 128-row tiles
 // they read it once (from HBM; tiles of the same group and keys run side by side and find it in L2)
 // where n decode calls would read it n times.  What a request does not share is an ordinary decode
-// from its own first token on; both leave a maximum, a sum and an output, joined here in a fixed
-// order: the prefix's parts, then the request's own.
+// from its own first token on; both leave a maximum, a sum and weighted values, joined here in a fixed
+// order: the prefix's parts, then the request's own.  (A log-sum in place of the pair would round the
+// sum's logarithm to the maximum's unit: at scores of 2^20, weights off by some hundredths.)
 //
 // Bound: the tensor cores over the prefixes, HBM over the rest, one after the other.  Measured: 64
 // requests behind 32,768 tokens with 30 to 1,500 of their own, 4 x 8 heads of 256, 114 us (tiles 65,
@@ -31,14 +32,14 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const SharedJoinParams
   float2 own[D / 64], all[D / 64], v[kJoined][D / 64];
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) own[e] = *reinterpret_cast<const float2*>(p.own_o + r * D + e * 64 + 2 * lane);
-  const float own_lse = p.own_lse[r];
+  const float2 own_ml = p.own_ml[r];
   const bool shares = p.own_begin[b] > 0;
   const int splits = shares ? p.splits : 0;
-  float all_lse = kNone;
+  float2 all_ml = make_float2(kNone, 0.f);
   if (p.whole_o && shares) {
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) all[e] = *reinterpret_cast<const float2*>(p.whole_o + r * D + e * 64 + 2 * lane);
-    all_lse = p.whole_lse[r];
+    all_ml = p.whole_ml[r];
   }
   float2 ml = make_float2(kNone, 0.f);
   if (lane < splits) ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (lane * rows + r));
@@ -51,13 +52,11 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const SharedJoinParams
           v[j][e] = *reinterpret_cast<const float2*>(p.part_o + ((k0 + j) * rows + r) * D + e * 64 + 2 * lane);
   };
   load(0);
-  // what is normalised has the sum 1 at the maximum log2(e) lse (a NaN stays one)
-  const float own_m = own_lse * kLog2e, own_l = own_lse == kNone ? 0.f : 1.f;
-  const float all_m = all_lse * kLog2e, all_l = all_lse == kNone ? 0.f : 1.f;
-  float M = fmaxf(fmaxf(ml.y == 0.f ? kNone : ml.x, own_m), all_m);
+  auto maximum = [](float2 x) { return x.y == 0.f ? kNone : x.x; };
+  float M = fmaxf(fmaxf(maximum(ml), maximum(own_ml)), maximum(all_ml));
   for (int k = lane + 32; k < splits; k += 32) {
     const float2 x = *reinterpret_cast<const float2*>(p.part_ml + 2 * (k * rows + r));
-    if (x.y != 0.f) M = fmaxf(M, x.x);
+    M = fmaxf(M, maximum(x));
   }
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
@@ -84,8 +83,8 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const SharedJoinParams
       add(__shfl_sync(0xffffffffu, ml.x, (k0 + j) & 31), __shfl_sync(0xffffffffu, ml.y, (k0 + j) & 31), v[j]);
     }
   }
-  add(all_m, all_l, all);
-  add(own_m, own_l, own);
+  add(all_ml.x, all_ml.y, all);
+  add(own_ml.x, own_ml.y, own);
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const int64_t at = b * p.o_stride + (r - (int64_t)b * p.HQ) * D;
 #pragma unroll

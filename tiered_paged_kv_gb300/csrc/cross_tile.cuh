@@ -941,7 +941,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
         }
         ok = ok && __all_sync(0xffffffffu, all_fine);
         if (!ok) break;
-        const float mt = most * qscale;
+        const float mt = kSpan == kSharedPrefix ? __fmul_rn(most, qscale) : most * qscale;
         const bool grow = mt - m > kLift<T> + kSlack<T>;  // not where both are -inf
         if (__any_sync(0xffffffffu, grow)) {
           const float to = mt - kLift<T>, f = !grow ? 1.f : far_off<T>(m) ? __int_as_float(0x7fffffff) : ex2(m - to);
@@ -980,7 +980,11 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
             scores(x, c);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float2 v = unpair(fma2(::tpk::pair(x[e], x[e + 1]), q2, ref2));
+            // Prefixes are joined with what the split kernel leaves: their scores are scaled and rounded as there,
+            // so that equal ones weigh the same wherever they stand (at 2^26 a float32 step is a factor of 2^8).
+            // (One by one: a packed product and a packed sum after it came out as one fused step.)
+            float2 v = unpair(kSpan == kSharedPrefix ? add2(::tpk::pair(__fmul_rn(x[e], qscale), __fmul_rn(x[e + 1], qscale)), ref2)
+                                                     : fma2(::tpk::pair(x[e], x[e + 1]), q2, ref2));
             v.x = ex2(v.x);
             v.y = ex2(v.y);
             sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], ::tpk::pair(v.x, v.y));

@@ -142,6 +142,7 @@ struct PagedParams {
   int32_t* own_begin;       // and where what it does not share begins (written)
   int n_grp;          // groups that share prefixes, in a split launch; 0: none
   int window, sinks;  // windows: tokens that a query sees up to its own, and first ones that it always sees
+  int sums;      // split launches: p.lse takes pairs (maximum in base 2, sum), p.o values that are not divided by it
   int run_rows;  // query rows of a run, 8 or 16 (set at launch)
   int whole;     // a block per run (set at launch)
   int stall_unit;  // test hook: this block's first page, or key tile, is neither copied nor signalled (-1: none)
@@ -187,15 +188,15 @@ constexpr int kTileRows = 128;    // query rows of a tile; a block takes `tiles`
 cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits,
                                cudaStream_t stream);
 // Row tiles over the prefixes of groups; their parts stay in the workspace, for launch_shared_join:
-// p.part_o [split][n_q][H * G][D] beside p.part_ml, and what the requests do not share, normalised.
+// p.part_o [split][n_q][H * G][D] beside p.part_ml.
 cudaError_t launch_shared_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits, cudaStream_t stream);
 struct SharedJoinParams {
   const float* part_o;
   const float* part_ml;
-  const float* whole_o;  // the prefix's result, where it is not in parts
-  const float* whole_lse;
-  const float* own_o;    // [n_q][H * G][D], and its log-sums
-  const float* own_lse;
+  const float* whole_o;  // the prefix, where it is not in parts
+  const float2* whole_ml;
+  const float* own_o;    // [n_q][H * G][D], and each row's maximum and sum
+  const float2* own_ml;
   const int32_t* own_begin;  // 0: nothing shared
   void* o;
   float* lse;
