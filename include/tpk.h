@@ -537,7 +537,7 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
  * are left out.  Outputs overlap nothing else.
  * ws: dev workspace of tpk_kv_pages_workspace_bytes(kv_slots, n_req) bytes, 16-byte aligned
  * (no initialisation); calls sharing one must not overlap on the GPU.  n_req in [1, 4096],
- * n_req * max_pages < 2^31, kv_slots + free_cap < 2^31.  Capturable once the device has
+ * n_req * max_pages < 2^31, kv_slots + free_cap < 2^31 - 8192.  Capturable once the device has
  * seen one uncaptured call.
  */
 size_t tpk_kv_pages_workspace_bytes(int64_t kv_slots, int n_req);
@@ -584,7 +584,7 @@ tpk_status tpk_kv_pages_compact(int n_req, int max_pages, int64_t kv_slots, cons
  *   k_pools, v_pools     host arrays of n_layers device pools [kv_slots][kv_heads][64][head_dim]
  *   src, dst             dev int32 [n_pages]
  * Of the shape kv_heads, head_dim, dtype and kv_slots count.  n_layers in [1, 4096]; n_pages
- * >= 0 (0 is a no-op).
+ * in [0, 2^31 - 16384) (0 is a no-op).
  */
 tpk_status tpk_kv_pages_copy(const tpk_paged_shape* shape, int n_layers, void* const* k_pools, void* const* v_pools,
                              int n_pages, const int32_t* src, const int32_t* dst, tpk_stream_t stream);

@@ -583,7 +583,7 @@ tpk_status tpk_kv_pages_copy(const tpk_paged_shape* shape, int n_layers, void* c
   const tpk_status st = check_paged(shape);
   if (st != TPK_OK) return st;
   if (n_layers < 1 || n_layers > kMaxLayers) return fail(TPK_ERR_INVALID, "n_layers %d out of [1, %d]", n_layers, kMaxLayers);
-  if (n_pages < 0) return fail(TPK_ERR_INVALID, "n_pages %d < 0", n_pages);
+  if (n_pages < 0 || n_pages > 0x7fffffff - 16384) return fail(TPK_ERR_INVALID, "n_pages %d", n_pages);
   if (!k_pools || !v_pools) return fail(TPK_ERR_INVALID, "null pointer argument");
   for (int i = 0; i < n_layers; ++i) {
     if (!k_pools[i] || !v_pools[i]) return fail(TPK_ERR_INVALID, "null pool of layer %d", i);
