@@ -240,7 +240,10 @@ __global__ void __launch_bounds__(kPartThreads, 1) fork_kernel(const ForkParams 
     // the stack's entries that this call pushed are not in free_slots yet
     const int from = there - 1 - rank;
     int got = kNone;
-    if (asks && rank < there) got = from < n_free ? p.free_slots[from] : Team::get(pushed + from - n_free);
+    if (asks && rank < there) {
+      got = from < n_free ? p.free_slots[from] : Team::get(pushed + from - n_free);
+      lost = !valid(got);  // an entry that is no slot: taken off the stack, and nobody's
+    }
     lost |= asks && rank >= there;
     if (b >= n) continue;
     const bool copied = asks && !lost, refused = lost || S.fresh[b] == kRefused;
