@@ -520,7 +520,7 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
  * First the slots that nobody holds any more are pushed on the stack of free slots, the
  * highest first; then the new slots are taken from its top, in request order.  A request
  * for whose copy no slot is left, or whose turn brings an entry of the stack that is outside
- * the pool (it is taken off all the same), keeps its whole pages only; one whose source, length or
+ * the pool (it is taken off all the same), keeps its whole pages only; one whose source or
  * len_keep is out of range (or more than its source has) stays as it was: both have
  * granted[b] = 0.
  *   source, len_in, len_keep  dev int32 [n_req]; len_in: the lengths before the call
@@ -533,9 +533,10 @@ tpk_status tpk_kv_tables_update(int n_req, int max_pages, const int32_t* len_old
  *                        clamped; slots pushed past free_cap are dropped)
  *   len_out              dev int32 [n_req] (may be len_in); granted: dev int32 [n_req]
  *   copy_src, copy_dst   dev int32 [n_req]: -1 where nothing is copied
- * Lengths out of [0, 64 * max_pages], table entries outside the pool, entries of the stack
- * outside the pool that are taken, more releases of a slot than it has holders, and dropped
- * slots set bit 0 of the device status; such entries are left out.  Outputs overlap nothing else.
+ * Lengths out of [0, 64 * max_pages] are clamped into it, and what is kept of such a history
+ * goes by the clamped one; table entries outside the pool are left out.  Both set bit 0 of the
+ * device status, and so do entries of the stack outside the pool that are taken, more releases
+ * of a slot than it has holders, and dropped slots.  Outputs overlap nothing else.
  * ws: dev workspace of tpk_kv_pages_workspace_bytes(kv_slots, n_req) bytes, 16-byte aligned
  * (no initialisation); calls sharing one must not overlap on the GPU.  n_req in [1, 4096],
  * n_req * max_pages < 2^31, kv_slots + free_cap < 2^31 - 8192.  Capturable once the device has

@@ -1,5 +1,5 @@
-"""Forks of batches whose stack of free slots holds what it should not: no slot from outside the pool is
-handed out, and the device status tells."""
+"""Forks of batches whose stack of free slots, or whose lengths, hold what they should not: no slot from
+outside the pool is handed out, and the device status tells."""
 import pytest
 import torch
 
@@ -46,3 +46,15 @@ def test_stack_entries_outside_the_pool_are_no_slots(entry, wide):
 def test_bad_entries_that_nobody_takes(wide):
     got = fork([0, 0], [70, 0], [[0, 1], [-1, -1]], [-1, 7000000, 2], 6, wide=wide)
     assert got["granted"] == [1, 1] and got["dst"] == [-1, 2] and got["n_free"] == 2 and got["status"] == (0, 0)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_lengths_out_of_range_are_cut(wide):
+    """A length past the row counts as the whole row, one below 0 as none; the status tells.  What a request
+    asks for of such a history goes by the length that it was cut to."""
+    got = fork([1, 1, 0], [200, -3, 10], [[0, 1], [2, 3], [4, 5]], [], 6, wide=wide)
+    assert got["status"] == (4, 1)
+    assert got["len"] == [0, 0, 128] and got["granted"] == [1, 1, 1]
+    assert got["rows"][2] == [0, 1] and got["shares"] == [0] * 6
+    got = fork([0, 0], [200, 64], [[0, 1], [2, 3]], [], 6, keep=[129, 128], wide=wide)
+    assert got["status"] == (4, 1) and got["granted"] == [0, 1] and got["len"] == [128, 128]
