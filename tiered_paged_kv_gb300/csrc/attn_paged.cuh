@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
     wait_before();
     if (tid == 0) {
       atomicOr(p.status, kStatusTimeout);
-      if (!p.whole) p.cuts[blockIdx.x].parts = 0;
+      if (kSpan == kSharedPrefix || !p.whole) p.cuts[blockIdx.x].parts = 0;
     }
     return;
   }
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
   const Batch<kSpan> batch{p, virtuals};
   Walk<kSpan> walk;
   int64_t per = 0;  // numbers of a range
-  if (p.whole) {
+  if (kSpan != kSharedPrefix && p.whole) {
     // a block per run: nothing to join, and nothing to number if every request has as many
     int64_t run;
     if (p.q_off) {
@@ -886,7 +886,6 @@ int device_sms();
 // Runs of a launch: a decode's, an upper bound of cross attention's.
 inline int64_t most_runs(const PagedParams& p) {
   const int64_t each = (p.G + p.run_rows - 1) / p.run_rows;
-  if (p.n_grp > 0) return p.H * ((int64_t)p.n_q * p.G / p.run_rows + p.n_grp + p.n_q * each);
   return p.H * (p.q_off ? (int64_t)p.n_q * p.G / p.run_rows + p.n_req : p.n_req * each);
 }
 

@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_half[i], 256);
+      if (kShare == 2) mbar_init(&S.p_half[i], 256);
       mbar_init(&S.p_full[i], kShare == 4 ? 4 * kTileRows : 256);
       mbar_init(&S.o_full[i], 1);
       mbar_init(&S.o_empty[i], kTileRows * kShare);
@@ -1155,9 +1155,13 @@ cudaError_t launch_tiles(const PagedParams& p, int groups, int splits, cudaStrea
   });
   if (e != cudaSuccess) return e;
   e = launch_early(tile_kernel<T, D, kT, kSpan>, groups * p.H * splits, C::kThreads, C::kSmem, stream, p, splits);
-  if (e != cudaSuccess || splits == 1 || kSpan == kSharedPrefix) return e;
-  // the fold's blocks may start while the last parts still run: they wait for them
-  return launch_early(tile_fold_kernel<T, D, kT>, groups * p.H * (C::kRows / 8), 256, 0, stream, p, splits);
+  if constexpr (kSpan == kSharedPrefix) {
+    return e;
+  } else {
+    if (e != cudaSuccess || splits == 1) return e;
+    // the fold's blocks may start while the last parts still run: they wait for them
+    return launch_early(tile_fold_kernel<T, D, kT>, groups * p.H * (C::kRows / 8), 256, 0, stream, p, splits);
+  }
 }
 
 template <int D, int kT, int kSpan>
