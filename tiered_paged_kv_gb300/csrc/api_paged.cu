@@ -782,7 +782,6 @@ tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n
   p.o = own_o;
   p.o_f32 = 1;
   p.o_stride = HQ * shape->head_dim;
-  p.sums = 1;
   p.lse = reinterpret_cast<float*>(own_ml);
   cudaError_t e;
   if (const int run_rows = shared_split(shape, n_req, n_grp)) {  // and the prefixes, in front of it
@@ -813,7 +812,7 @@ tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n
     e = launch_shared_tiles(g, shape->head_dim, shape->dtype, plan.tiles, (int)plan.groups, (int)plan.splits, cs);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
     p.begin = p.own_begin;
-    e = launch_paged_split(p, shape->head_dim, shape->dtype, cs);
+    e = launch_own_split(p, shape->head_dim, shape->dtype, cs);
     if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
     j.part_o = g.part_o;
     j.part_ml = g.part_ml;

@@ -233,13 +233,15 @@ __device__ __forceinline__ void store_pair(const PagedParams& p, int64_t row, in
   else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at) = T::pack(x, y);
 }
 
-// A row's log-sum; or, with p.sums, its maximum in base 2 and its sum, for a join.
+// A row's log-sum, or its maximum and sum.
+template <int kSpan>
 __device__ __forceinline__ void store_sum(const PagedParams& p, int64_t row, float M, float L) {
-  if (p.sums) reinterpret_cast<float2*>(p.lse)[row] = make_float2(M, L);
+  if (leaves_sums(kSpan)) reinterpret_cast<float2*>(p.lse)[row] = make_float2(M, L);
   else p.lse[row] = L == 0.f ? kEmpty : (M + log2f(L)) * kLn2;
 }
-// What a row's weighted values are multiplied by.
-__device__ __forceinline__ float over_sum(const PagedParams& p, float L) { return p.sums ? 1.f : L == 0.f ? 0.f : 1.f / L; }
+// What a row's values are multiplied by.
+template <int kSpan>
+__device__ __forceinline__ float over_sum(float L) { return leaves_sums(kSpan) ? 1.f : L == 0.f ? 0.f : 1.f / L; }
 
 // Row r of a run: its query token and query head; false past the run's last row.
 __device__ __forceinline__ bool run_row(const PagedParams& p, int first, int count, int h, int tile, int r, int& token,
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
         int token, head;
         if (!run_row(p, batch.out(walk.b, first), count, h, (int)run - h * tiles, i / (D / 2), token, head)) continue;
         store_pair<T>(p, token, head, D, i % (D / 2) * 2, 0.f, 0.f);
-        if (i % (D / 2) == 0) store_sum(p, (int64_t)token * p.H * p.G + head, kEmpty, 0.f);
+        if (i % (D / 2) == 0) store_sum<kSpan>(p, (int64_t)token * p.H * p.G + head, kEmpty, 0.f);
       }
       return;
     }
@@ -623,7 +625,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
       const int64_t r = i / (D / 2);
       store_pair<T>(p, first + r / HQ, (int)(r % HQ), D, (int)(i % (D / 2)) * 2, 0.f, 0.f);
     }
-    for (int64_t i = tid; i < (int64_t)count * HQ; i += kPagedThreads) store_sum(p, (int64_t)first * HQ + i, kEmpty, 0.f);
+    for (int64_t i = tid; i < (int64_t)count * HQ; i += kPagedThreads) store_sum<kSpan>(p, (int64_t)first * HQ + i, kEmpty, 0.f);
   }
     if (lo >= hi) return;
   }
@@ -765,13 +767,13 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
       for (int w = 0; w < kConsumers; ++w) L += exp2f(S.m[w][r] - (M == kEmpty ? 0.f : M)) * S.l[w][r];
       int token, head;
       const bool write = run_row(p, out, count, h, tile, r, token, head) && !dead;
-      const float inv = whole ? over_sum(p, L) : 1.f;
+      const float inv = whole ? over_sum<kSpan>(L) : 1.f;
       // the join's record: this block has the run's first page and not its last
       if (tid == 0 && pass == 0 && !whole && s.page == 0)
         p.cuts[blockIdx.x] = {out, count, h, tile, (int)((s.pages - s.count - 1) / per) + 2};
       if (write && tid % kPer == 0) {
         if (whole) {
-          store_sum(p, (int64_t)token * HQ + head, M, L);
+          store_sum<kSpan>(p, (int64_t)token * HQ + head, M, L);
         } else {
           p.part_ml[slot * kRowTile + r] = M;
           p.part_ml[(2 * (int64_t)gridDim.x + slot) * kRowTile + r] = L;
@@ -813,7 +815,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 128 && !kSmall ? 0 : split
 // partials' maxima are read at once, one a thread; then every thread sums its four
 // channels over the partials in block order, eight loads in flight.
 constexpr int kFoldParts = 64;  // weights held at a time
-template <typename T, int D>
+template <typename T, int D, int kSpan>
 __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ PagedParams p, int blocks, int rows) {
   __shared__ float weight[kFoldParts];
   __shared__ float red[2];
@@ -870,7 +872,7 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
         }
     }
   }
-  const float inv = over_sum(p, L);
+  const float inv = over_sum<kSpan>(L);
   if constexpr (kVec == 1) {
     const float x = o[0] * inv, y = __shfl_down_sync(0xffffffffu, x, 1);
     if ((tid & 1) == 0) store_pair<T>(p, token, head, D, c, x, y);
@@ -878,7 +880,7 @@ __global__ void __launch_bounds__(64) fold_paged_kernel(const __grid_constant__ 
 #pragma unroll
     for (int e = 0; e < kVec; e += 2) store_pair<T>(p, token, head, D, c + e, o[e] * inv, o[e + 1] * inv);
   }
-  if (tid == 0) store_sum(p, (int64_t)token * p.H * p.G + head, M, L);
+  if (tid == 0) store_sum<kSpan>(p, (int64_t)token * p.H * p.G + head, M, L);
 }
 
 int device_sms();
@@ -904,7 +906,7 @@ cudaError_t launch_split(const PagedParams& p, cudaStream_t stream) {
   if (e != cudaSuccess || p.whole || blocks == 1) return e;
   // the fold's blocks may start while the last ranges still run: they wait for them
   const int rows = p.q_off ? p.run_rows : min(p.G, p.run_rows);
-  return launch_early(fold_paged_kernel<T, D>, (blocks - 1) * rows, 64, 0, stream, p, blocks, rows);
+  return launch_early(fold_paged_kernel<T, D, kSpan>, (blocks - 1) * rows, 64, 0, stream, p, blocks, rows);
 }
 
 template <typename T, int D, int kSpan>

@@ -142,7 +142,6 @@ struct PagedParams {
   int32_t* own_begin;       // and where what it does not share begins (written)
   int n_grp;          // groups that share prefixes, in a split launch; 0: none
   int window, sinks;  // windows: tokens that a query sees up to its own, and first ones that it always sees
-  int sums;      // split launches: p.lse takes pairs (maximum in base 2, sum), p.o values that are not divided by it
   int run_rows;  // query rows of a run, 8 or 16 (set at launch)
   int whole;     // a block per run (set at launch)
   int stall_unit;  // test hook: this block's first page, or key tile, is neither copied nor signalled (-1: none)
@@ -152,6 +151,8 @@ constexpr int kTileBlocks = 152;  // SMs of the device: blocks a launch over row
 constexpr int kPagedMaxBlocks = 512;  // blocks of a split launch; each owns two partial slots
 constexpr int kRowTile = 16;          // query rows of a split run, at most
 cudaError_t launch_paged_split(PagedParams& p, int D, int dtype, cudaStream_t stream);
+// The same, for launch_shared_join: of [begin, n).
+cudaError_t launch_own_split(PagedParams& p, int D, int dtype, cudaStream_t stream);
 // The same over prefixes of groups and what each request has of its own, at most kVirtual of both, each
 // with results of its own (p.o and p.lse of [2][n_q] rows); run_rows: rows of a run.
 cudaError_t launch_shared_split(PagedParams& p, int D, int dtype, cudaStream_t stream);
@@ -331,7 +332,11 @@ __device__ __forceinline__ void request_span(const PagedParams& p, int b, int& l
 
 // What the queries of a launch see of their request: all of it (or [begin, n)), or its last tokens
 // and its first ones; or, a request being a group of decoding requests, the prefix that they share.
-enum : int { kWholeHistory = 0, kWindowed = 1, kSharedPrefix = 2 };
+// Besides, what one of these does not share, [begin, n) again.
+enum : int { kWholeHistory = 0, kWindowed = 1, kSharedPrefix = 2, kOwnTokens = 3 };
+// What is left for the join of prefixes: p.lse has pairs (maximum in base 2, sum), p.o float32 values that are not
+// divided by the sum.
+constexpr bool leaves_sums(int span) { return span == kSharedPrefix || span == kOwnTokens; }
 
 // Request b's query rows: tokens [first, first + count) of q.
 __device__ __forceinline__ void request_rows(const PagedParams& p, int b, int& first, int& count) {
