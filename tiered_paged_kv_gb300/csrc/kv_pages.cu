@@ -3,8 +3,8 @@
 //
 // Forks and compaction are bookkeeping on whole numbers: a few bytes for each page-table entry
 // and each slot, in phases that each need all of the phase before.  A small pool and table go to one
-// block, which keeps what it counts in shared memory (a beam step of 64 rows, 367 slots: 11.3 us
-// as a cluster, 6.6 so; compaction of 900 slots 12.6 and 5.1).  Others go to one cluster of kParts
+// block, which keeps what it counts in shared memory (a beam step of 64 rows, 367 slots: 9.5 us
+// as a cluster, 5.8 so; compaction of 900 slots 10.8 and 4.6; one_block).  Others go to one cluster of kParts
 // blocks, whose barrier separates the phases: they are bound by the latency of their phases, not
 // by what eight SMs can read, and a barrier of a cluster costs less than a launch.  Sums and counts
 // go by integer atomics, which give the same in any order; ranks go by scans, so that the result
@@ -487,8 +487,22 @@ static cudaError_t launch_team(void (*kernel)(P), size_t smem, cudaStream_t stre
 
 // Shared memory of one block's arrays: four words for each slot.
 static size_t local_bytes(int64_t slots) { return 4 * sizeof(int32_t) * slots; }
-static bool one_block(int n_req, int max_pages, int kv_slots) {
-  return kv_slots <= kLocalSlots && (int64_t)n_req * max_pages <= kLocalEntries;
+// Whether one block takes a call.  Its time grows with the slots, the requests (its 32 warps take one each)
+// and the entries that rows hold, a cluster's hardly: 40 requests, or 14 in a compaction, cost it what 1,600
+// and 560 slots do.  One block and the cluster, us, half of the requests forked:
+//   requests x pages, slots      fork           compaction
+//   64 x 56, 4,000               8.5   11.0     9.1   13.2
+//   128 x 28, 4,000              9.6   11.0     9.8   13.4
+//   256 x 1, 500                 10.2   9.6     8.5   12.0
+//   64 x 112, 8,000              12.3  11.3     14.5  13.8
+//   512 x 3, 2,000               17.9  12.0     14.8  13.5
+//   4,000 x 2, 6,050             113   30.5     84    23.7
+// What rows hold is not known here, and tables are mostly wider: their width counts only for what it may cost (64
+// rows of the same 500 pages 17.8 and 11.2 us, of 1,000 31 and 12.8; 16 rows of 10 pages in a table as wide 4.9
+// and 10.5).
+constexpr int kForkRequest = 40, kForkMost = 9200, kCompactRequest = 14, kCompactMost = 8000;
+static bool one_block(int n_req, int max_pages, int kv_slots, int request, int most) {
+  return kv_slots <= kLocalSlots && (int64_t)n_req * max_pages <= kLocalEntries && kv_slots + request * n_req <= most;
 }
 
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
@@ -500,7 +514,7 @@ cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
                                                        (int)sizeof(ForkShared));
   });
   if (e != cudaSuccess) return e;
-  return one_block(p.n_req, p.max_pages, p.kv_slots)
+  return one_block(p.n_req, p.max_pages, p.kv_slots, kForkRequest, kForkMost)
              ? launch_team<true>(fork_kernel<true>, sizeof(ForkShared) + local_bytes(p.kv_slots), stream, p)
              : launch_team<false>(fork_kernel<false>, sizeof(ForkShared), stream, p);
 }
@@ -511,7 +525,7 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
     return cudaFuncSetAttribute(compact_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)local_bytes(kLocalSlots));
   });
   if (e != cudaSuccess) return e;
-  return one_block(p.n_req, p.max_pages, p.kv_slots)
+  return one_block(p.n_req, p.max_pages, p.kv_slots, kCompactRequest, kCompactMost)
              ? launch_team<true>(compact_kernel<true>, local_bytes(p.kv_slots), stream, p)
              : launch_team<false>(compact_kernel<false>, 0, stream, p);
 }
