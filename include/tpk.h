@@ -708,8 +708,8 @@ tpk_status tpk_cross_attn_paged(const tpk_paged_shape* shape, int n_req, int n_q
  * which the prefix ends, of which each has a copy).  The prefix is read once for the whole
  * group, from the row of its first request that has the most of it; what a request has
  * beyond it, from its own row.  Results are those of tpk_decode_attn_paged without
- * tok_begin, to rounding (the prefix's weights are rounded once to the pools' type before
- * the product with the values), and bit-reproducible.  The two sides are joined by their maxima
+ * tok_begin, to rounding (where o is of the pools' type, the prefix's weights are rounded once
+ * to it before the product with the values), and bit-reproducible.  The two sides are joined by their maxima
  * and sums: equal scores weigh the same on both, however far out they are.
  *   n_tokens   dev int32 [n_req], the prefix counted in; a request with fewer tokens than
  *              n_shared[g] sees those it has, one with none gets o = 0, lse = -inf

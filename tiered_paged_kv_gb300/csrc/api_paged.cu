@@ -809,7 +809,8 @@ tpk_status tpk_decode_attn_shared(const tpk_paged_shape* shape, int n_req, int n
     g.own_lens = n_tokens;
     g.part_ml = reinterpret_cast<float*>(at(w.part_ml));
     g.part_o = reinterpret_cast<float*>(at(w.part_o));
-    e = launch_shared_tiles(g, shape->head_dim, shape->dtype, plan.tiles, (int)plan.groups, (int)plan.splits, cs);
+    e = (o_f32 ? launch_shared_tiles_f32 : launch_shared_tiles)(g, shape->head_dim, shape->dtype, plan.tiles, (int)plan.groups,
+                                                                (int)plan.splits, cs);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
     p.begin = p.own_begin;
     e = launch_own_split(p, shape->head_dim, shape->dtype, cs);

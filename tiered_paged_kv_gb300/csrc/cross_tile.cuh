@@ -26,7 +26,9 @@
 // below the maximum it was taken from: weights stay below 2^15, and those far below the
 // maximum are held to 2^-36 of it (struct F16).  Weights are rounded once to the input type -- as the
 // tensor core needs them beside V -- while their sum is kept unrounded in float32: the
-// rounding of a weight is of the size of the output's own.
+// rounding of a weight is of the size of the output's own.  Float32 outputs (of shared prefixes) have
+// no such rounding: there a second plane takes what the first left, for a product more (64 requests behind
+// 32,768 tokens, 4 x 8 heads of 256: 113 -> 132 us; 13 groups behind up to 9,000, 8 x 5 of 128: 115 -> 120).
 //
 // Few query rows leave the device empty, so the keys can be split into `splits` parts
 // per item; parts leave (maximum, sum, O) in the workspace and a fold joins them in part
@@ -378,7 +380,9 @@ struct Requests {
   }
 };
 
-template <typename T, int D, int kT, int kSpan>
+// kPlanes: 16-bit planes that weights enter the product with the values in, the second holding what the first's
+// rounding left.
+template <typename T, int D, int kT, int kSpan, int kPlanes>
 __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kThreads, 1)
     tile_kernel(const __grid_constant__ PagedParams p, int splits) {
   constexpr int kShare = kRowThreads<D, kT, kSpan>;
@@ -591,10 +595,16 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
 #pragma unroll
             for (int y = 0; y < 8 / kWaits; ++y) {
               const int i = kWaits == 1 ? y : (y >> 1) * 4 + 2 * s + (y & 1);  // 16 tokens: two 8-row groups
-              if (i < groups)
-                tc_mma_ts(tmem + 256 + x * 128 + c * 128,
-                          tmem + buf * kKeys + i / (8 / kShare) * (kKeys / kShare) + i % (8 / kShare) * 8,
-                          v + i * 128, id_pv, more || s > 0 || y > 0);
+              if (i >= groups) continue;
+              const uint32_t o = tmem + 256 + x * 128 + c * 128;
+              if constexpr (kPlanes == 2) {
+                const uint32_t w = tmem + buf * kKeys + i / 2 * 32 + i % 2 * 8;
+                tc_mma_ts(o, w, v + i * 128, id_pv, more || s > 0 || y > 0);
+                tc_mma_ts(o, w + 16, v + i * 128, id_pv, true);
+              } else {
+                tc_mma_ts(o, tmem + buf * kKeys + i / (8 / kShare) * (kKeys / kShare) + i % (8 / kShare) * 8, v + i * 128, id_pv,
+                          more || s > 0 || y > 0);
+              }
             }
             if (last && s + 1 == kWaits) tc_commit(empty + 8 * nth(at, c));
           }
@@ -972,7 +982,7 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
 #pragma unroll 1
         for (int c = 0; c < kMine; c += 32) {
           float x[32];
-          uint32_t w[16];
+          uint32_t w[16], rest[16];
           if (kShare == 4)
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = kept[e];
@@ -989,8 +999,14 @@ __global__ void __launch_bounds__(TileCfg<D, kT, kRowThreads<D, kT, kSpan>>::kTh
             v.y = ex2(v.y);
             sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], ::tpk::pair(v.x, v.y));
             w[e >> 1] = T::pack(v.x, v.y);
+            if constexpr (kPlanes == 2) {
+              const float2 back = T::unpack(w[e >> 1]);
+              rest[e >> 1] = T::pack(v.x - back.x, v.y - back.y);
+            }
           }
-          tc_st16(s_addr + (c >> 1), w);  // over scores of this half already used
+          // over scores of this half already used: 16 columns of weights, and 16 of what their rounding left
+          if constexpr (kPlanes == 2) tc_st16(s_addr + c + 16, rest);
+          tc_st16(s_addr + (kPlanes == 2 ? c : c >> 1), w);
           tc_wait_st();
           tc_fence_before();
           mbar_arrive(kShare == 2 && c == 0 ? &S.p_half[buf] : &S.p_full[buf]);
@@ -1146,15 +1162,15 @@ __global__ void __launch_bounds__(256) tile_fold_kernel(const __grid_constant__ 
 
 int device_sms();
 
-template <typename T, int D, int kT, int kSpan>
+template <typename T, int D, int kT, int kSpan, int kPlanes>
 cudaError_t launch_tiles(const PagedParams& p, int groups, int splits, cudaStream_t stream) {
   using C = TileCfg<D, kT, kRowThreads<D, kT, kSpan>>;
   static DeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(tile_kernel<T, D, kT, kSpan>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return cudaFuncSetAttribute(tile_kernel<T, D, kT, kSpan, kPlanes>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  e = launch_early(tile_kernel<T, D, kT, kSpan>, groups * p.H * splits, C::kThreads, C::kSmem, stream, p, splits);
+  e = launch_early(tile_kernel<T, D, kT, kSpan, kPlanes>, groups * p.H * splits, C::kThreads, C::kSmem, stream, p, splits);
   if constexpr (kSpan == kSharedPrefix) {
     return e;
   } else {
@@ -1164,19 +1180,20 @@ cudaError_t launch_tiles(const PagedParams& p, int groups, int splits, cudaStrea
   }
 }
 
-template <int D, int kT, int kSpan>
+template <int D, int kT, int kSpan, int kPlanes>
 cudaError_t launch_type(const PagedParams& p, int dtype, int groups, int splits, cudaStream_t stream) {
-  return dtype == 0 ? launch_tiles<Bf16, D, kT, kSpan>(p, groups, splits, stream) : launch_tiles<F16, D, kT, kSpan>(p, groups, splits, stream);
+  return dtype == 0 ? launch_tiles<Bf16, D, kT, kSpan, kPlanes>(p, groups, splits, stream)
+                    : launch_tiles<F16, D, kT, kSpan, kPlanes>(p, groups, splits, stream);
 }
 
-template <int kSpan>
+template <int kSpan, int kPlanes = 1>
 cudaError_t launch_tiles_of(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits, cudaStream_t stream) {
-  if (D == 256) return launch_type<256, 1, kSpan>(p, dtype, groups, splits, stream);
+  if (D == 256) return launch_type<256, 1, kSpan, kPlanes>(p, dtype, groups, splits, stream);
   if (D == 128)
-    return tiles == 1 ? launch_type<128, 1, kSpan>(p, dtype, groups, splits, stream)
-                      : launch_type<128, 2, kSpan>(p, dtype, groups, splits, stream);
-  return tiles == 1 ? launch_type<64, 1, kSpan>(p, dtype, groups, splits, stream)
-                    : launch_type<64, 2, kSpan>(p, dtype, groups, splits, stream);
+    return tiles == 1 ? launch_type<128, 1, kSpan, kPlanes>(p, dtype, groups, splits, stream)
+                      : launch_type<128, 2, kSpan, kPlanes>(p, dtype, groups, splits, stream);
+  return tiles == 1 ? launch_type<64, 1, kSpan, kPlanes>(p, dtype, groups, splits, stream)
+                    : launch_type<64, 2, kSpan, kPlanes>(p, dtype, groups, splits, stream);
 }
 
 }  // namespace tpk

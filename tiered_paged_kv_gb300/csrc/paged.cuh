@@ -191,6 +191,8 @@ cudaError_t launch_cross_tiles(const PagedParams& p, int D, int dtype, int tiles
 // Row tiles over the prefixes of groups; their parts stay in the workspace, for launch_shared_join:
 // p.part_o [split][n_q][H * G][D] beside p.part_ml.
 cudaError_t launch_shared_tiles(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits, cudaStream_t stream);
+// The same for float32 outputs: weights in two 16-bit planes.
+cudaError_t launch_shared_tiles_f32(const PagedParams& p, int D, int dtype, int tiles, int groups, int splits, cudaStream_t stream);
 struct SharedJoinParams {
   const float* part_o;
   const float* part_ml;
