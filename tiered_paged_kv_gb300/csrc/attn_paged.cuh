@@ -29,7 +29,8 @@
 // requests of up to 30,000 tokens, windows of 4,000 and 70 first tokens, 4 x 8 heads of 256: 101 us,
 // 6.1 TB/s).  Over shared prefixes (kSharedPrefix) the requests that are numbered are the groups'
 // prefixes, then what each request has of its own; a last kernel joins the two (cross_shared.cu; four
-// answers to a prompt of 1,900 tokens, 8 x 4 heads of 128: 12.7 us).
+// answers to a prompt of 1,900 tokens, 8 x 4 heads of 128: 12.6 us).  Where row tiles take the prefixes, what
+// requests have of their own is a launch like a decode's (kOwnTokens).
 //
 // Measured: 16 requests of 32,000 tokens at head sizes 64, 128, 256: 6.8, 6.9, 6.9 TB/s; one
 // request of 131,072 tokens (4 x 8 heads of 256, 537 MB) 86 us, 6.2 TB/s; one of 200 tokens

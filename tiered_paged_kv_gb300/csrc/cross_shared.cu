@@ -9,9 +9,9 @@
 // sum's logarithm to the maximum's unit: at scores of 2^20, weights off by some hundredths.)
 //
 // Bound: the tensor cores over the prefixes, HBM over the rest, one after the other.  Measured: 64
-// requests behind 32,768 tokens with 30 to 1,500 of their own, 4 x 8 heads of 256, 114 us (tiles 65,
-// decode 27, its fold 3, join 6); 13 groups of 1 to 24 behind 300 to 9,000 tokens with up to 2,500 of
-// their own, 8 x 5 heads of 128 (491 MB), 115 us (60, 40, 3, 5).
+// requests behind 32,768 tokens with 30 to 1,500 of their own, 4 x 8 heads of 256, 114 us (cut
+// short behind the tiles 70, the decode 107, its fold 108); 13 groups of 1 to 24 behind 300 to 9,000 tokens
+// with up to 2,500 of their own, 8 x 5 heads of 128 (491 MB), 115 us (62, 107, 109).
 #include "cross_tile.cuh"
 
 namespace tpk {

@@ -39,13 +39,13 @@
 // those from its first query's window on; a key tile is any two that follow each other in that list,
 // so that a few first tokens share a tile with the window's start.  Prompts of 900 to 2,500 tokens
 // through windows of 1,500 and 4 first tokens, 8 x 4 heads of 128: 115 us, 943 TFLOP/s of what is
-// seen; a seventh of the tiles' products lie outside the windows, and 5 waves hold 4.2 of work.
+// seen; a seventh of the tiles' products lie outside the windows, and 560 items are 3.7 waves.
 //
 // Over shared prefixes (kSharedPrefix) the requests are groups of decoding requests, one query token
 // each, and every part stays in the workspace for a join of its own (cross_shared.cu).  512 rows over
-// 32,768 tokens, 4 heads of 256: 67 us of 128,000 cycles in each block; 72,000 of them are products
-// (2,535 a key tile: the operands pass shared memory at its rate), 35,000 waits for keys and values
-// from a ring too short for a tile more, 11,000 for weights, 10,000 until the first keys are there.
+// 32,768 tokens, 4 heads of 256: 70 us, 124,000 cycles in each block; 76,000 of them are products and
+// their issue (2,700 a key tile; the operands pass shared memory in 2,560), 33,000 waits for keys and values
+// from a ring too short for a tile more, 4,000 for weights, 11,000 until the first keys are there.
 //
 // Measured: two requests of 4,096 tokens, 8,192 states, 8 x 4 heads: 922, 1,546 and 1,332
 // TFLOP/s at D = 64, 128, 256; eight requests of 300 to 1,500 tokens, 1,601 to 6,404
